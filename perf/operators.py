@@ -266,10 +266,10 @@ def _plain_rope_bwd(st):
 
 
 def _round_e4m3(y):
-    """To the nearest e4m3 value, ties to even, from 64 bits."""
-    _, e = torch.frexp(y)
-    step = torch.ldexp(torch.ones_like(y), (e - 1).clamp_min(-6) - 3)
-    return (torch.round(y / step) * step).clamp(-448.0, 448.0)
+    """To the nearest e4m3 value, ties to even, from 64 bits: four significant bits, or steps of 2^-9 below 2^-6."""
+    b = y.view(torch.int64)
+    b = (b + (2 ** 48 - 1) + ((b >> 49) & 1)) & -(2 ** 49)
+    return torch.where(y.abs() < 2.0 ** -6, torch.round(y * 512.0) * 2.0 ** -9, b.view(torch.float64)).clamp(-448.0, 448.0)
 
 
 def _plain_append(st):
@@ -412,14 +412,17 @@ def _exact_codes(x, fmt):
     """(value, scale): the definition of what a row is stored as."""
     x = x.double()
     top = x.abs().max(-1).values
-    scale = (top / (127 if fmt == "i8" else 448)).float().double()   # scales are held in 32 bits
+    scale = (top / torch.full_like(top, 127 if fmt == "i8" else 448)).float().double()   # scales are held in 32 bits
     scale[scale < 2.0 ** -60] = 0
     y = x / torch.where(scale > 0, scale, torch.ones_like(scale)).unsqueeze(-1)
     if fmt == "i8":
         code = y.round().clamp(-127, 127)
-    else:   # 16 steps a factor of two at the top, a fixed step below 2^-6
-        e = torch.floor(torch.log2(y.abs().clamp_min(2.0 ** -6)))
-        code = (torch.round(y * 2.0 ** (3 - e)) * 2.0 ** (e - 3)).clamp(-448, 448)
+    else:   # the nearest of the format's values, the even code of two that are as near
+        grid = torch.arange(127, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn).double()
+        hi = torch.bucketize(y.abs(), grid).clamp_max(126)
+        lo = (hi - 1).clamp_min(0)
+        up, down = grid[hi] - y.abs(), y.abs() - grid[lo]
+        code = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), grid[hi], grid[lo]) * y.sign()
     return torch.where(scale.unsqueeze(-1) > 0, code * scale.unsqueeze(-1), torch.zeros_like(code))
 
 
