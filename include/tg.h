@@ -49,7 +49,9 @@ typedef enum {
   TG_ERR_DEBUG_BOUNDS = 8   /* device, debug library only: an index outside its buffer, access skipped */
 } tg_status;
 
-typedef enum { TG_F32 = 0, TG_BF16 = 1 } tg_dtype;
+/* TG_I8 and TG_E4M3 (8-bit floating point, 4 exponent and 3 mantissa bits) are types
+ * of a quantised cache's codes only. */
+typedef enum { TG_F32 = 0, TG_BF16 = 1, TG_I8 = 2, TG_E4M3 = 3 } tg_dtype;
 
 typedef struct CUstream_st* tg_stream_t; /* same type as cudaStream_t */
 
@@ -311,6 +313,144 @@ tg_status tg_gated_decode_noalloc(const void* q, const void* k_cache, const void
                                   int cap, int max_len, int n_hq, int n_hkv, int head_dim,
                                   const float* gain, const float* tau, void* out,
                                   tg_stream_t stream);
+
+/*
+ * Norm of queries and keys per head with the rotary embedding, in one pass: what
+ * stands between the projections and the attention in models whose layers normalise
+ * q and k (the Qwen models the pages evaluate do; the pages do not describe it). To
+ * use it, project without rotation (tg_qkv_rope with every pos 0, which is the
+ * identity rotation). For token t and each head x of q and k, with that head kind's
+ * weight w:
+ *     n = w * x / sqrt(mean(x^2) + eps)
+ *     y_i        = n_i cos(a_i) - n_{i+r/2} sin(a_i)
+ *     y_{i+r/2}  = n_{i+r/2} cos(a_i) + n_i sin(a_i)     i < r/2, r = rot_dim
+ *     y_i        = n_i                                   i >= r
+ * with a_i = pos[t] * rope_base^(-2i/r). Angles are formed as in tg_qkv_rope, from an
+ * exact fixed-point product, so far positions lose nothing.
+ *   q [n_tokens, n_hq, head_dim], k [n_tokens, n_hkv, head_dim] dtype; the heads of a
+ *       token are dense, and *_stride is the distance in elements from one token to
+ *       the next (>= heads * head_dim), so views of a packed projection output work
+ *   q_weight, k_weight [head_dim] f32;  pos [n_tokens] int32 device
+ *   q_out, k_out  dtype outputs of the same shapes with strides of their own; q_out may
+ *       be q itself and k_out k itself (same pointer and stride), else no overlap
+ * TG_BF16 or TG_F32; head_dim a multiple of 8 up to 256, rot_dim a multiple of 8 in
+ * [0, head_dim]; 16-byte aligned pointers and strides; eps >= 0, rope_base > 1.
+ */
+tg_status tg_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          tg_dtype dtype, int64_t n_tokens, int n_hq, int n_hkv, int head_dim,
+                          int rot_dim, const float* q_weight, const float* k_weight, float eps,
+                          float rope_base, const int32_t* pos, void* q_out, int64_t q_out_stride,
+                          void* k_out, int64_t k_out_stride, tg_stream_t stream);
+
+/*
+ * Its backward: from the same q, k, weights, eps, rope_base and pos and the gradients
+ * dq_out, dk_out of the outputs, with r = 1 / sqrt(mean(x^2) + eps) and g the upstream
+ * gradient rotated back,
+ *   dq, dk         dtype       r (w g - x r^2 mean(w g x))
+ *   dq_weight, dk_weight [head_dim] f32   sum over tokens and heads of g x r
+ * Nothing is kept from the forward. The sums over tokens are taken in a fixed order.
+ * dq may be q or dq_out itself, dk may be k or dk_out itself (same pointer and stride);
+ * n_tokens == 0 writes zero weight gradients. workspace: caller-owned device scratch of
+ * at least tg_qk_norm_rope_bwd_workspace_size(...) bytes, 16-byte aligned, no initial
+ * value needed; calls that overlap on the GPU must not share it.
+ */
+size_t tg_qk_norm_rope_bwd_workspace_size(int64_t n_tokens, int n_hq, int n_hkv, int head_dim);
+tg_status tg_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* dq_out, int64_t dq_out_stride, const void* dk_out,
+                              int64_t dk_out_stride, tg_dtype dtype, int64_t n_tokens, int n_hq,
+                              int n_hkv, int head_dim, int rot_dim, const float* q_weight,
+                              const float* k_weight, float eps, float rope_base,
+                              const int32_t* pos, void* dq, int64_t dq_stride, void* dk,
+                              int64_t dk_stride, float* dq_weight, float* dk_weight,
+                              void* workspace, size_t workspace_bytes, tg_stream_t stream);
+
+/*
+ * The quantised cache. Row j of sequence b holds, for each KV head, head_dim 8-bit
+ * codes and one f32 scale for the key and for the value, and one f32 score:
+ *   k_cache, v_cache [batch, cap, n_hkv, head_dim] TG_I8 or TG_E4M3 codes
+ *   k_scale, v_scale [batch, cap, n_hkv] f32;   s_cache [batch, cap] f32
+ * A head's values are code * scale. A row is written with
+ *     scale = max|x| / qmax rounded to f32 (qmax 127 for TG_I8, 448 for TG_E4M3),
+ *     code  = the quotient x / scale rounded once to the nearest code, ties to even;
+ * scale and codes are 0 where the scale would be below 2^-60, and a head that holds an
+ * infinity or a NaN gets a NaN scale (it reads back as NaN) and codes 0.
+ * head_dim 64 or 128; k/v pointers 16-byte aligned.
+ *
+ * tg_quant_cache_append: sequence b's new rows, packed rows [cu_new[b], cu_new[b+1]) of
+ * n_new, go to cache rows start[b], start[b]+1, ..., and cache_len[b] becomes start[b]
+ * plus their number.
+ *   k_new, v_new [n_src, n_hkv, head_dim] bf16, s_new [n_src] f32
+ *   src_idx [n_new] int32 device or NULL: packed row r is source row src_idx[r] (the
+ *           accepted ones among drafted tokens); NULL: row r itself (n_new == n_src).
+ *           An index outside [0, n_src) stores a row of zeros with score 0 and records
+ *           TG_ERR_DEVICE_CHECK
+ *   cu_new [batch+1] int32 device; packed rows behind cu_new[batch] are not read
+ *   start [batch] int32 device or NULL: NULL (or cache_len itself) appends to the rows
+ *           there; another array, which must not overlap cache_len, writes from any row
+ *           (a sequence taken back to an earlier length)
+ * A sequence whose rows do not fit its capacity, or whose offsets are out of order, is
+ * left unchanged, its cache_len too, and TG_ERR_DEVICE_CHECK recorded.
+ */
+tg_status tg_quant_cache_append(const void* k_new, const void* v_new, const float* s_new,
+                                int64_t n_src, const int32_t* src_idx, int64_t n_new,
+                                const int32_t* cu_new, const int32_t* start, int batch, int cap,
+                                int n_hkv, int head_dim, tg_dtype cache_dtype, void* k_cache,
+                                void* v_cache, float* k_scale, float* v_scale, float* s_cache,
+                                int32_t* cache_len, tg_stream_t stream);
+
+/*
+ * tg_quant_cache_read: rows given back, packed (as tg_gated_attention takes them):
+ * cache rows start[b] .. start[b] + cu_rows[b+1] - cu_rows[b] - 1 of sequence b go to
+ * rows [cu_rows[b], cu_rows[b+1]) of k, v [n_rows, n_hkv, head_dim] (TG_BF16 or TG_F32:
+ * code * scale in f32, rounded once) and s [n_rows] f32. start NULL: from row 0. Rows
+ * of the outputs behind cu_rows[batch] are left as they were. A sequence that asks for
+ * rows behind its cache_len (or cap) is skipped and TG_ERR_DEVICE_CHECK recorded.
+ */
+tg_status tg_quant_cache_read(const void* k_cache, const void* v_cache, const float* k_scale,
+                              const float* v_scale, const float* s_cache,
+                              const int32_t* cache_len, const int32_t* start,
+                              const int32_t* cu_rows, int64_t n_rows, int batch, int cap,
+                              int n_hkv, int head_dim, tg_dtype cache_dtype, tg_dtype out_dtype,
+                              void* k, void* v, float* s, tg_stream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the cache: what checks several drafted
+ * continuations of a sequence in one pass. Drafted token t of sequence b sees every
+ * cache row j < cache_len[b] and those drafted tokens i whose bit is set in
+ * tree_mask[b][t] (itself and its ancestors; any set of bits is allowed):
+ *     z = q . k / (sqrt(head_dim) * tau[hq]) + gain[hq] * s
+ *     out[b, t, hq] = sum softmax(z) v
+ * over both, with KV head hq / (n_hq / n_hkv). One drafted token with mask 1 is decode
+ * of a single token whose k, v and score are not in the cache yet.
+ *   q [batch, n_draft, n_hq, head_dim] bf16, rotated at the tokens' positions
+ *   k_draft, v_draft [batch, n_draft, n_hkv, head_dim] bf16, s_draft [batch, n_draft] f32
+ *   tree_mask [batch, n_draft] int64 device; n_draft <= 64
+ *   draft_len [batch] int32 device or NULL (n_draft for all): tokens t >= draft_len[b]
+ *           are not there: no token sees them, and their rows of out are left as they were
+ *   cache_dtype TG_BF16: the cache of tg_cache_append, k_scale and v_scale NULL;
+ *           TG_I8, TG_E4M3: the quantised cache, with its scales (0 or >= 2^-60)
+ *   max_len (host) bounds every cache_len[b]; max_len <= cap
+ *   out [batch, n_draft, n_hq, head_dim] bf16
+ * A token that sees nothing (mask 0 over an empty cache, or every logit -inf) gets
+ * zeros. Infinities and NaN in drafted tokens that a token does not see, and in cache
+ * rows behind cache_len, do not reach it. A sequence with cache_len outside
+ * [0, min(cap, max_len)] or draft_len outside [0, n_draft] is skipped (its out rows are
+ * left as they were) and TG_ERR_DEVICE_CHECK recorded.
+ * head_dim 64 or 128, n_hq / n_hkv <= 128, batch <= 1024; q, drafts, caches, out and
+ * workspace 16-byte aligned. workspace: caller-owned device scratch of at least
+ * tg_tree_attention_workspace_size(...) bytes, no initial value needed; calls that
+ * overlap on the GPU must not share it.
+ */
+size_t tg_tree_attention_workspace_size(int batch, int n_draft, int max_len, int n_hq, int n_hkv,
+                                        int head_dim);
+tg_status tg_tree_attention(const void* q, const void* k_draft, const void* v_draft,
+                            const float* s_draft, const int64_t* tree_mask,
+                            const int32_t* draft_len, int batch, int n_draft,
+                            const void* k_cache, const void* v_cache, tg_dtype cache_dtype,
+                            const float* k_scale, const float* v_scale, const float* s_cache,
+                            const int32_t* cache_len, int cap, int max_len, int n_hq, int n_hkv,
+                            int head_dim, const float* gain, const float* tau, void* out,
+                            void* workspace, size_t workspace_bytes, tg_stream_t stream);
 
 /*
  * Gated delta rule over the kept tokens: the recurrence of the hybrid model's Gated

@@ -39,6 +39,18 @@ SIGNATURES = {
     "tg_gated_decode": (INT, [P, P, P, P, P, INT, INT, INT, INT, INT, INT, P, P, P, P,
                               ctypes.c_size_t, P]),
     "tg_gated_decode_noalloc": (INT, [P, P, P, P, P, INT, INT, INT, INT, INT, INT, P, P, P, P]),
+    "tg_qk_norm_rope": (INT, [P, I64, P, I64, INT, I64, INT, INT, INT, INT, P, P, F32, F32, P, P,
+                              I64, P, I64, P]),
+    "tg_qk_norm_rope_bwd_workspace_size": (ctypes.c_size_t, [I64, INT, INT, INT]),
+    "tg_qk_norm_rope_bwd": (INT, [P, I64, P, I64, P, I64, P, I64, INT, I64, INT, INT, INT, INT, P, P,
+                                  F32, F32, P, P, I64, P, I64, P, P, P, ctypes.c_size_t, P]),
+    "tg_quant_cache_append": (INT, [P, P, P, I64, P, I64, P, P, INT, INT, INT, INT, INT, P, P, P, P,
+                                    P, P, P]),
+    "tg_quant_cache_read": (INT, [P, P, P, P, P, P, P, P, I64, INT, INT, INT, INT, INT, INT, P, P,
+                                  P, P]),
+    "tg_tree_attention_workspace_size": (ctypes.c_size_t, [INT, INT, INT, INT, INT, INT]),
+    "tg_tree_attention": (INT, [P, P, P, P, P, P, INT, INT, P, P, INT, P, P, P, P, INT, INT, INT,
+                                INT, INT, P, P, P, P, ctypes.c_size_t, P]),
     "tg_gated_delta_rule_workspace_size": (ctypes.c_size_t, [INT, I64, INT, INT]),
     "tg_gated_delta_rule": (INT, [P, P, P, INT, P, P, P, INT, I64, INT, INT, INT, INT, P, P,
                                   ctypes.c_size_t, P]),

@@ -6,6 +6,7 @@ status. All arithmetic happens in the CUDA kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Optional, Sequence
@@ -15,8 +16,9 @@ import torch
 from . import _lib
 from ._lib import TokenGateError, check
 
-TG_F32, TG_BF16 = 0, 1
+TG_F32, TG_BF16, TG_I8, TG_E4M3 = 0, 1, 2, 3
 _DT = {torch.float32: TG_F32, torch.bfloat16: TG_BF16}
+_CODE_DT = {torch.int8: TG_I8, torch.float8_e4m3fn: TG_E4M3}
 
 
 def _stream(stream=None) -> int:
@@ -378,6 +380,317 @@ def gated_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         _cuda(workspace, "workspace"), workspace.numel() * workspace.element_size(),
         _stream(stream))
     check(st, "tg_gated_decode")
+    return out
+
+
+def _launch_on(stream, *tensors):
+    """(context, stream handle) for a call on these tensors (None entries are skipped):
+    they must share one CUDA device, which is made current for the call if it is not,
+    and the stream is that device's current one unless given."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise TokenGateError("every tensor must be a CUDA tensor")
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise TokenGateError("every tensor must be on the same device")
+    if stream is not None and stream.device.index != dev:
+        raise TokenGateError("the stream must be on the tensors' device")
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    ctx = contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+    return ctx, s.cuda_stream
+
+
+def _keep_for(stream, *tensors) -> None:
+    """Tensors allocated here (on the current stream) but used on a given stream."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _heads(t: torch.Tensor, T: int, H: int, dh: int, name: str, dtype) -> int:
+    """Token stride in elements of a [T, H, dh] tensor whose heads are dense."""
+    if t.shape != (T, H, dh):
+        raise TokenGateError(f"{name} must have shape {(T, H, dh)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TokenGateError(f"{name} must be {dtype}, got {t.dtype}")
+    st, sh, sd = t.stride()
+    if (dh > 1 and sd != 1) or (H > 1 and sh != dh):
+        raise TokenGateError(f"{name} must have dense heads (strides [*, {dh}, 1])")
+    return st if T > 1 else H * dh
+
+
+def _norm_rope_args(what, q, k, q_weight, k_weight, pos, rot_dim):
+    if q.dim() != 3 or k.dim() != 3:
+        raise TokenGateError(f"{what}: q [T,Hq,dh], k [T,Hkv,dh]")
+    T, hq, dh = q.shape
+    hkv = k.shape[1]
+    if q.dtype not in _DT:
+        raise TokenGateError(f"{what}: unsupported dtype {q.dtype}")
+    _shape(q_weight, (dh,), "q_weight", torch.float32)
+    _shape(k_weight, (dh,), "k_weight", torch.float32)
+    _shape(pos, (T,), "pos", torch.int32)
+    return T, hq, hkv, dh, (dh if rot_dim is None else int(rot_dim))
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                 pos: torch.Tensor, eps: float = 1e-6, rope_base: float = 1e6,
+                 rot_dim: Optional[int] = None, out=None, stream=None):
+    """RMS norm of every head of q [T,Hq,dh] and k [T,Hkv,dh] (weights [dh] f32), then the
+    rotary embedding of the first rot_dim elements (None: all) at pos [T] int32. q and k
+    may be views with any token stride (of a packed projection output); returns (q_out,
+    k_out), dense unless `out` is given. `out` may be (q, k) themselves."""
+    T, hq, hkv, dh, rot = _norm_rope_args("qk_norm_rope", q, k, q_weight, k_weight, pos, rot_dim)
+    q_st = _heads(q, T, hq, dh, "q", q.dtype)
+    k_st = _heads(k, T, hkv, dh, "k", q.dtype)
+    new = out is None
+    if new:
+        out = (torch.empty((T, hq, dh), dtype=q.dtype, device=q.device),
+               torch.empty((T, hkv, dh), dtype=q.dtype, device=q.device))
+    qo, ko = out
+    qo_st = _heads(qo, T, hq, dh, "q_out", q.dtype)
+    ko_st = _heads(ko, T, hkv, dh, "k_out", q.dtype)
+    w_q, w_k, p = (_cuda(q_weight, "q_weight"), _cuda(k_weight, "k_weight"), _cuda(pos, "pos"))
+    ctx, s = _launch_on(stream, q, k, q_weight, k_weight, pos, qo, ko)
+    with ctx:
+        st = _lib.load().tg_qk_norm_rope(q.data_ptr(), q_st, k.data_ptr(), k_st, _DT[q.dtype], T, hq,
+                                         hkv, dh, rot, w_q, w_k, float(eps), float(rope_base), p,
+                                         qo.data_ptr(), qo_st, ko.data_ptr(), ko_st, s)
+    check(st, "tg_qk_norm_rope")
+    if new:
+        _keep_for(stream, qo, ko)
+    return qo, ko
+
+
+def qk_norm_rope_bwd_workspace_size(n_tokens: int, n_hq: int, n_hkv: int, head_dim: int) -> int:
+    return int(_lib.load().tg_qk_norm_rope_bwd_workspace_size(n_tokens, n_hq, n_hkv, head_dim))
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
+                     k_weight: torch.Tensor, pos: torch.Tensor, dq_out: torch.Tensor,
+                     dk_out: torch.Tensor, eps: float = 1e-6, rope_base: float = 1e6,
+                     rot_dim: Optional[int] = None, grads=None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of qk_norm_rope for upstream dq_out, dk_out, from the forward's inputs:
+    returns (dq, dk, dq_weight, dk_weight), the latter two [dh] f32. Every [T,H,dh]
+    tensor may have any token stride."""
+    T, hq, hkv, dh, rot = _norm_rope_args("qk_norm_rope_bwd", q, k, q_weight, k_weight, pos, rot_dim)
+    dt = q.dtype
+    q_st = _heads(q, T, hq, dh, "q", dt)
+    k_st = _heads(k, T, hkv, dh, "k", dt)
+    gq_st = _heads(dq_out, T, hq, dh, "dq_out", dt)
+    gk_st = _heads(dk_out, T, hkv, dh, "dk_out", dt)
+    new = []
+    if grads is None:
+        grads = new = [torch.empty((T, hq, dh), dtype=dt, device=q.device),
+                       torch.empty((T, hkv, dh), dtype=dt, device=q.device),
+                       torch.empty(dh, dtype=torch.float32, device=q.device),
+                       torch.empty(dh, dtype=torch.float32, device=q.device)]
+    dq, dk, dwq, dwk = grads
+    dq_st = _heads(dq, T, hq, dh, "dq", dt)
+    dk_st = _heads(dk, T, hkv, dh, "dk", dt)
+    _shape(dwq, (dh,), "dq_weight", torch.float32)
+    _shape(dwk, (dh,), "dk_weight", torch.float32)
+    lib = _lib.load()
+    if workspace is None:
+        need = int(lib.tg_qk_norm_rope_bwd_workspace_size(T, hq, hkv, dh))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        new = [*new, workspace]
+    w_q, w_k, p = (_cuda(q_weight, "q_weight"), _cuda(k_weight, "k_weight"), _cuda(pos, "pos"))
+    ctx, s = _launch_on(stream, q, k, q_weight, k_weight, pos, dq_out, dk_out, dq, dk, dwq, dwk,
+                        workspace)
+    with ctx:
+        st = lib.tg_qk_norm_rope_bwd(
+            q.data_ptr(), q_st, k.data_ptr(), k_st, dq_out.data_ptr(), gq_st, dk_out.data_ptr(), gk_st,
+            _DT[dt], T, hq, hkv, dh, rot, w_q, w_k, float(eps), float(rope_base), p, dq.data_ptr(),
+            dq_st, dk.data_ptr(), dk_st, _cuda(dwq, "dq_weight"), _cuda(dwk, "dk_weight"),
+            _cuda(workspace, "workspace"), workspace.numel() * workspace.element_size(), s)
+    check(st, "tg_qk_norm_rope_bwd")
+    _keep_for(stream, *new)
+    return dq, dk, dwq, dwk
+
+
+def _quant_cache(what, k_cache, v_cache, k_scale, v_scale, s_cache, cache_len):
+    if k_cache.dim() != 4:
+        raise TokenGateError(f"{what}: caches [B,cap,Hkv,dh]")
+    B, cap, hkv, dh = k_cache.shape
+    if k_cache.dtype not in _CODE_DT:
+        raise TokenGateError(f"{what}: a quantised cache is int8 or float8_e4m3fn, got {k_cache.dtype}")
+    _shape(v_cache, k_cache.shape, "v_cache", k_cache.dtype)
+    _shape(k_scale, (B, cap, hkv), "k_scale", torch.float32)
+    _shape(v_scale, (B, cap, hkv), "v_scale", torch.float32)
+    _shape(s_cache, (B, cap), "s_cache", torch.float32)
+    _shape(cache_len, (B,), "cache_len", torch.int32)
+    return B, cap, hkv, dh
+
+
+def quant_cache_append(k_new: torch.Tensor, v_new: torch.Tensor, s_new: torch.Tensor,
+                       cu_new: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       k_scale: torch.Tensor, v_scale: torch.Tensor, s_cache: torch.Tensor,
+                       cache_len: torch.Tensor, start: Optional[torch.Tensor] = None,
+                       src_idx: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise rows into a cache: sequence b's packed rows [cu_new[b], cu_new[b+1]) go to
+    its cache rows from start[b] (None: from cache_len[b]) on, and cache_len[b] becomes
+    the row behind them. k_new, v_new [R,Hkv,dh] bf16, s_new [R] f32; packed row r is row
+    src_idx[r] of them (int32), or row r when src_idx is None. Caches [B,cap,Hkv,dh] int8
+    or float8_e4m3fn with scales [B,cap,Hkv] f32, s_cache [B,cap] f32."""
+    B, cap, hkv, dh = _quant_cache("quant_cache_append", k_cache, v_cache, k_scale, v_scale, s_cache,
+                                   cache_len)
+    R = s_new.numel()
+    _shape(s_new, (R,), "s_new", torch.float32)
+    _shape(k_new, (R, hkv, dh), "k_new", torch.bfloat16)
+    _shape(v_new, (R, hkv, dh), "v_new", torch.bfloat16)
+    _shape(cu_new, (B + 1,), "cu_new", torch.int32)
+    n_new = R
+    if src_idx is not None:
+        n_new = src_idx.numel()
+        _shape(src_idx, (n_new,), "src_idx", torch.int32)
+    if start is not None:
+        _shape(start, (B,), "start", torch.int32)
+    args = (_cuda(k_new, "k_new"), _cuda(v_new, "v_new"), _cuda(s_new, "s_new"), R,
+            None if src_idx is None else _cuda(src_idx, "src_idx"), n_new, _cuda(cu_new, "cu_new"),
+            None if start is None else _cuda(start, "start"), B, cap, hkv, dh,
+            _CODE_DT[k_cache.dtype], _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache"),
+            _cuda(k_scale, "k_scale"), _cuda(v_scale, "v_scale"), _cuda(s_cache, "s_cache"),
+            _cuda(cache_len, "cache_len"))
+    ctx, s = _launch_on(stream, k_new, v_new, s_new, src_idx, cu_new, start, k_cache, v_cache, k_scale,
+                        v_scale, s_cache, cache_len)
+    with ctx:
+        st = _lib.load().tg_quant_cache_append(*args, s)
+    check(st, "tg_quant_cache_append")
+
+
+def quant_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                     v_scale: torch.Tensor, s_cache: torch.Tensor, cache_len: torch.Tensor,
+                     cu_rows: torch.Tensor, total: int, start: Optional[torch.Tensor] = None,
+                     dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """Rows of a quantised cache as packed (k [total,Hkv,dh], v, s [total] f32), k and v in
+    `dtype` (bf16 or f32): sequence b's cache rows from start[b] (None: 0) on fill rows
+    [cu_rows[b], cu_rows[b+1])."""
+    B, cap, hkv, dh = _quant_cache("quant_cache_read", k_cache, v_cache, k_scale, v_scale, s_cache,
+                                   cache_len)
+    total = int(total)
+    _shape(cu_rows, (B + 1,), "cu_rows", torch.int32)
+    if start is not None:
+        _shape(start, (B,), "start", torch.int32)
+    new = out is None
+    if new:
+        out = (torch.empty((total, hkv, dh), dtype=dtype, device=k_cache.device),
+               torch.empty((total, hkv, dh), dtype=dtype, device=k_cache.device),
+               torch.empty(total, dtype=torch.float32, device=k_cache.device))
+    k, v, s_out = out
+    if k.dtype not in _DT:
+        raise TokenGateError(f"quant_cache_read: unsupported dtype {k.dtype}")
+    _shape(k, (total, hkv, dh), "k", k.dtype)
+    _shape(v, (total, hkv, dh), "v", k.dtype)
+    _shape(s_out, (total,), "s", torch.float32)
+    args = (_cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache"), _cuda(k_scale, "k_scale"),
+            _cuda(v_scale, "v_scale"), _cuda(s_cache, "s_cache"), _cuda(cache_len, "cache_len"),
+            None if start is None else _cuda(start, "start"), _cuda(cu_rows, "cu_rows"), total, B, cap,
+            hkv, dh, _CODE_DT[k_cache.dtype], _DT[k.dtype], _cuda(k, "k"), _cuda(v, "v"),
+            _cuda(s_out, "s"))
+    ctx, s = _launch_on(stream, k_cache, v_cache, k_scale, v_scale, s_cache, cache_len, start, cu_rows,
+                        k, v, s_out)
+    with ctx:
+        st = _lib.load().tg_quant_cache_read(*args, s)
+    check(st, "tg_quant_cache_read")
+    if new:
+        _keep_for(stream, k, v, s_out)
+    return k, v, s_out
+
+
+def tree_mask(parents: Sequence[Sequence[int]]) -> torch.Tensor:
+    """tree_attention's mask ([B, T] int64, on the CPU) of a tree per sequence: parents[b][t]
+    is the drafted token that t continues, or -1 where it continues the cache itself. A
+    parent comes before its children; shorter trees are filled up with 0."""
+    T = max((len(p) for p in parents), default=0)
+    if T > 64:
+        raise TokenGateError(f"tree_mask: at most 64 drafted tokens, got {T}")
+    rows = []
+    for b, par in enumerate(parents):
+        bits = []
+        for t, p in enumerate(par):
+            if not -1 <= p < t:
+                raise TokenGateError(f"tree_mask: parents[{b}][{t}] = {p} must be in [-1, {t})")
+            bits.append((bits[p] if p >= 0 else 0) | 1 << t)
+        rows.append([x - (1 << 64) if x >> 63 else x for x in bits] + [0] * (T - len(bits)))
+    return torch.tensor(rows, dtype=torch.int64).reshape(len(rows), T)
+
+
+def tree_attention_workspace_size(batch: int, n_draft: int, n_hq: int, n_hkv: int, head_dim: int,
+                                  max_len: int) -> int:
+    return int(_lib.load().tg_tree_attention_workspace_size(batch, n_draft, max_len, n_hq, n_hkv,
+                                                            head_dim))
+
+
+def tree_attention(q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor,
+                   s_draft: torch.Tensor, tree_mask: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, s_cache: torch.Tensor, cache_len: torch.Tensor,
+                   gain: torch.Tensor, tau: torch.Tensor, max_len: int,
+                   draft_len: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of T drafted tokens per sequence (q [B,T,Hq,dh], k_draft/v_draft
+    [B,T,Hkv,dh] bf16, s_draft [B,T] f32) over the cache rows j < cache_len[b] and the
+    drafted tokens in their tree_mask ([B,T] int64, bit i: token i). The cache is bf16
+    (cache_append's) or, with k_scale and v_scale, quantised (quant_cache_append's).
+    draft_len [B] int32: drafted tokens of each sequence (None: T); rows of out behind
+    them are left as they were. Returns out [B,T,Hq,dh] bf16."""
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise TokenGateError("tree_attention: q [B,T,Hq,dh], caches [B,cap,Hkv,dh]")
+    B, T, hq, dh = q.shape
+    cap, hkv = k_cache.shape[1], k_cache.shape[2]
+    _shape(k_cache, (B, cap, hkv, dh), "k_cache")
+    _shape(v_cache, k_cache.shape, "v_cache", k_cache.dtype)
+    _shape(k_draft, (B, T, hkv, dh), "k_draft", torch.bfloat16)
+    _shape(v_draft, (B, T, hkv, dh), "v_draft", torch.bfloat16)
+    _shape(s_draft, (B, T), "s_draft", torch.float32)
+    _shape(tree_mask, (B, T), "tree_mask", torch.int64)
+    _shape(s_cache, (B, cap), "s_cache", torch.float32)
+    _shape(cache_len, (B,), "cache_len", torch.int32)
+    _shape(gain, (hq,), "gain", torch.float32)
+    _shape(tau, (hq,), "tau", torch.float32)
+    if draft_len is not None:
+        _shape(draft_len, (B,), "draft_len", torch.int32)
+    if k_cache.dtype in _CODE_DT:
+        if k_scale is None or v_scale is None:
+            raise TokenGateError("tree_attention: a quantised cache needs k_scale and v_scale")
+        cdt = _CODE_DT[k_cache.dtype]
+        _shape(k_scale, (B, cap, hkv), "k_scale", torch.float32)
+        _shape(v_scale, (B, cap, hkv), "v_scale", torch.float32)
+        ks, vs = _cuda(k_scale, "k_scale"), _cuda(v_scale, "v_scale")
+    else:
+        if k_cache.dtype != torch.bfloat16 or k_scale is not None or v_scale is not None:
+            raise TokenGateError("tree_attention: a cache is bf16 without scales, or int8 or "
+                                 "float8_e4m3fn with them")
+        cdt, ks, vs = TG_BF16, None, None
+    new = []
+    if out is None:
+        out = torch.empty_like(q)
+        new.append(out)
+    _shape(out, q.shape, "out", torch.bfloat16)
+    lib = _lib.load()
+    if workspace is None:
+        need = int(lib.tg_tree_attention_workspace_size(B, T, int(max_len), hq, hkv, dh))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        new.append(workspace)
+    args = (_cuda(q, "q", torch.bfloat16), _cuda(k_draft, "k_draft"), _cuda(v_draft, "v_draft"),
+            _cuda(s_draft, "s_draft"), _cuda(tree_mask, "tree_mask"),
+            None if draft_len is None else _cuda(draft_len, "draft_len"), B, T,
+            _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache"), cdt, ks, vs,
+            _cuda(s_cache, "s_cache"), _cuda(cache_len, "cache_len"), cap, int(max_len), hq, hkv, dh,
+            _cuda(gain, "gain"), _cuda(tau, "tau"), _cuda(out, "out"), _cuda(workspace, "workspace"),
+            workspace.numel() * workspace.element_size())
+    ctx, s = _launch_on(stream, q, k_draft, v_draft, s_draft, tree_mask, draft_len, k_cache, v_cache,
+                        k_scale, v_scale, s_cache, cache_len, gain, tau, out, workspace)
+    with ctx:
+        st = lib.tg_tree_attention(*args, s)
+    check(st, "tg_tree_attention")
+    _keep_for(stream, *new)
     return out
 
 
