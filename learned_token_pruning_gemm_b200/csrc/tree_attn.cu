@@ -5,18 +5,65 @@
 // of sequence b sees every cache row j < cache_len[b] and the drafted tokens whose bit
 // is set in tree_mask[b][t]:
 //     z_j = q . k_j / (sqrt(dh) tau_h) + g_h s_j,   O = sum_j softmax_j(z) v_j.
+//
+// The cache is read once per KV head and serves all drafted tokens and query heads of
+// the group: with R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product
+// and back, so rows are packed into M = 128 tiles (row r is token r / G, head r % G)
+// and both products run on the tensor cores with accumulators in TMEM. Up to some 100
+// rows the work is bound by the bytes of the cache; beyond, by the products.
+//
+// Work units are tiles of 128 keys. The items (sequence, KV head, row tile) have
+// ceil(len / 128) cache tiles and one tile of drafted rows each; all units of all items
+// are numbered in a row and every CTA (one per SM) takes an equal share of that row, so
+// ragged lengths and few heads fill the machine alike. An item that lies inside one
+// CTA's share is finished there; one that is cut leaves a partial (max, sum, O) per
+// CTA, which a second kernel adds up in CTA order: results do not depend on timing.
+//
+// Per CTA, pipelines run over the units:
+//   warp 0       K tiles by TMA (bf16: into the operand ring; codes: K and V codes into
+//                a raw ring). A tile that ends inside (the last of a cache, the drafted
+//                rows) is copied row by row with the rest of it zero.
+//   warp 3       V tiles likewise (bf16 cache)
+//   warp 2       the rows' queries, and per key: score, scales (a ring of four tiles)
+//   warps 12-15  codes only: widen the raw tiles into bf16 operand tiles. Codes are exact
+//                in bf16, so scales are applied in fp32: the key's to the logit, the
+//                value's to the weight.
+//   warp 1       MMA issuer (one thread): S_0, .., PV_0, S_n, PV_1, ...; S_j = Q K_j^T into
+//                one of kS 128-column TMEM buffers, O += P_j V_j with P_j read from TMEM
+//                (it overwrites S_j) and V_j as an MN-major shared-memory operand.
+//   warps 4-11   softmax, 16 rows each, those with rows only: logits in the log2 domain,
+//                masks in the tiles that need them, a running max that moves only when it
+//                grows by more than 2^8 (O is then rescaled in TMEM), P in bf16. The row
+//                sum adds the rounded weights, so that a key which dominates its row
+//                gives its value exactly.
+// The parity waits are exact for the reasons given at the gated attention's kernel:
+// S_g is issued after PV_{g - kS}, and a softmax warp is never more than kS tiles ahead.
+//
+// Values of drafted rows that are not finite never enter the products (0 * inf would
+// reach tokens that do not see the row): they are zero in the operand tile, their rows
+// are noted, and the epilogue adds them to the rows that see them.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kBM = 128;           // rows of a row tile
+constexpr int kBN = 128;           // keys of a unit
 constexpr int kMaxDraft = 64;
+constexpr int kMaxBatch = 1024;
+constexpr int kKeyStages = 4;
+constexpr int kBadRing = 8;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kConvWarps = 4;
+constexpr int kMaxCtas = 148;      // one per SM
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr uint32_t kHalfBytes = kBN * 128;  // 64 columns of 128 rows, bf16, 128-byte swizzle
+constexpr uint32_t kTmemCols = 512, kColO = 384;
 
 struct TreeArgs {
-  const __nv_bfloat16 *q, *kd, *vd;
+  const __nv_bfloat16 *kd, *vd;
   const float* sd;
   const int64_t* mask;
   const int32_t* draft_len;
@@ -25,106 +72,939 @@ struct TreeArgs {
   const int32_t* cache_len;
   const float *gain, *tau;
   __nv_bfloat16* out;
-  int batch, n_draft, cap, max_len, n_hq, n_hkv;
+  int64_t* base;      // [batch + 1] first unit of each sequence (written by CTA 0)
+  float* part;        // partials: [2 * CTAs][rows][dh], then [2 * CTAs][rows][2] (max, sum)
+  int batch, n_draft, cap, max_len, n_hq, n_hkv, group;
+  int tm;             // tokens of a row tile
+  int n_cta;
   int* status;
 };
 
-template <int DH, int kType>
-__device__ __forceinline__ float cache_value(const uint8_t* p, int64_t i) {
-  if constexpr (kType == TG_BF16) {
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-  } else if constexpr (kType == TG_I8) {
-    return static_cast<float>(static_cast<int8_t>(p[i]));
+// A sequence's lengths, or no drafted tokens where they are out of range.
+__device__ __forceinline__ int2 seq_lens(const TreeArgs& A, int b, bool record) {
+  const int len = A.cache_len[b], dl = A.draft_len ? A.draft_len[b] : A.n_draft;
+  if (len < 0 || len > A.cap || len > A.max_len || dl < 0 || dl > A.n_draft) {
+    if (record) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
+    return make_int2(0, 0);
+  }
+  return make_int2(len, dl);
+}
+__device__ __forceinline__ int row_tiles(const TreeArgs& A, int dl) { return (dl + A.tm - 1) / A.tm; }
+__device__ __forceinline__ int key_tiles(int len) { return (len + kBN - 1) / kBN + 1; }
+
+// CTAs that share W units: no share is empty, so every CTA between an item's first and
+// last holds a part of it. CTA c has the units [W c / G, W (c + 1) / G).
+__device__ __forceinline__ int64_t share_ctas(const TreeArgs& A, int64_t W) {
+  return W < A.n_cta ? W : A.n_cta;
+}
+
+template <int DH, bool kQ>
+struct Cfg {
+  static constexpr int kHalves = DH / 64;
+  static constexpr int kS = kQ ? 2 : 3;                                  // S/P buffers in TMEM
+  static constexpr int kK = kQ ? (DH == 128 ? 2 : 3) : (DH == 128 ? 3 : 5);   // K operand tiles
+  static constexpr int kV = kQ ? (DH == 128 ? 1 : 2) : (DH == 128 ? 2 : 4);   // V operand tiles
+  static constexpr int kRaw = kQ ? (DH == 128 ? 4 : 8) : 1;              // raw tiles of codes
+  static constexpr int kRawBytes = kQ ? kBN * DH : 16;
+  static constexpr int kThreads = 128 + kSoftmaxWarps * 32 + (kQ ? kConvWarps * 32 : 0);
+  static constexpr int kFullArrivals = kQ ? kConvWarps : 1;              // a K or V tile is ready
+};
+
+template <int DH, bool kQ>
+struct TreeSmem {
+  using C = Cfg<DH, kQ>;
+  uint8_t q[C::kHalves][kHalfBytes];
+  uint8_t k[C::kK][C::kHalves][kHalfBytes];
+  uint8_t v[C::kV][C::kHalves][kHalfBytes];
+  uint8_t raw[C::kRaw][C::kRawBytes];
+  float key[kKeyStages][kQ ? 4 : 1][kBN];   // score, then (codes) key scale, value scale and its inverse
+  uint16_t bad[kBadRing][4];                // drafted rows with values that are not finite, 16 rows a word
+  int64_t base[kMaxBatch + 1];
+  int len[kMaxBatch];
+  uint8_t dl[kMaxBatch];
+  uint64_t q_full, q_empty;
+  uint64_t k_full[C::kK], k_empty[C::kK];
+  uint64_t v_full[C::kV], v_empty[C::kV];
+  uint64_t raw_full[C::kRaw], raw_empty[C::kRaw];
+  uint64_t b_full[kKeyStages], b_empty[kKeyStages];
+  uint64_t s_full[C::kS], p_full[C::kS], o_done[C::kS];
+  uint64_t o_free;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__device__ __forceinline__ bool all_alive(bool a) { return __all_sync(0xFFFFFFFFu, a); }
+
+// Walks a CTA's units in order: the unit's sequence, KV head, row tile and key tile.
+struct Cursor {
+  int64_t u, u1;
+  int b, item, n_items, kvh, mt, j, nt, len, dl;
+  template <class S>
+  __device__ __forceinline__ void load_seq(const TreeArgs& A, const S& s) {
+    len = s.len[b];
+    dl = s.dl[b];
+    nt = key_tiles(len);
+    n_items = A.n_hkv * row_tiles(A, dl);
+  }
+  __device__ __forceinline__ void split_item(const TreeArgs& A) {
+    const int amt = row_tiles(A, dl);
+    kvh = item / amt;
+    mt = item - kvh * amt;
+  }
+  template <class S>
+  __device__ __forceinline__ void start(const TreeArgs& A, const S& s, int64_t first, int64_t last) {
+    u = first;
+    u1 = last;
+    int lo = 0, hi = A.batch - 1;   // the last b with base[b] <= u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.base[mid] <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    load_seq(A, s);
+    const int64_t rem = u - s.base[b];
+    item = static_cast<int>(rem / nt);
+    j = static_cast<int>(rem - static_cast<int64_t>(item) * nt);
+    split_item(A);
+  }
+  template <class S>
+  __device__ __forceinline__ void advance(const TreeArgs& A, const S& s) {
+    ++u;
+    if (++j < nt || u >= u1) return;
+    j = 0;
+    if (++item == n_items) {
+      item = 0;
+      do ++b;
+      while (s.base[b + 1] == s.base[b]);   // sequences without units
+      load_seq(A, s);
+    }
+    split_item(A);
+  }
+  __device__ __forceinline__ bool draft() const { return j == nt - 1; }
+  __device__ __forceinline__ int keys() const { return draft() ? dl : min(kBN, len - j * kBN); }
+  // units of the current item from here on within the CTA's share
+  __device__ __forceinline__ int run() const {
+    const int64_t left = u1 - u;
+    return nt - j < left ? nt - j : static_cast<int>(left);
+  }
+};
+
+// 16 bytes global -> shared, or 16 zero bytes when !ok (src is not read then)
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// byte offset of 16-byte column c (0 .. dh/8 - 1) of row r in a swizzled operand tile
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  return (c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
+                                      float c0, float c1) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// Two codes (bytes i and i + 1 of w as selected by sel) to two bf16 values, exactly.
+// int8: with the low seven bits as mantissa over 128, (128 + low) - (128 or 256 by the
+// sign bit). e4m3: its exponent and mantissa bits sit in place in a bf16 whose exponent
+// is 120 too small, which a product with 2^120 restores (subnormals too).
+template <bool kE4m3>
+__device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t sel) {
+  uint32_t d;
+  if constexpr (kE4m3) {
+    const uint32_t x = __byte_perm(w, 0, sel);   // the codes in the high bytes
+    const uint32_t y = (x & 0x80008000u) | ((x & 0x7F007F00u) >> 4);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(y), "r"(0x7B807B80u));
   } else {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(p[i])));
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
+    const uint32_t x = __byte_perm(w, 0, sel);   // the codes in the low bytes
+    asm("sub.rn.bf16x2 %0, %1, %2;"
+        : "=r"(d)
+        : "r"((x & 0x007F007Fu) | 0x43004300u), "r"((x & 0x00800080u) | 0x43004300u));
+  }
+  return d;
+}
+
+// A bf16 pair with values that are not finite replaced by 0; *bad is set if there were any.
+__device__ __forceinline__ uint32_t finite2(uint32_t u, bool* bad) {
+  if ((u & 0x7F80u) == 0x7F80u) u &= 0xFFFF0000u, *bad = true;
+  if ((u & 0x7F800000u) == 0x7F800000u) u &= 0x0000FFFFu, *bad = true;
+  return u;
+}
+
+// Rows r0, r0 + step, .. below r1 of the drafted keys of (b, kvh) into an operand tile.
+template <int DH>
+__device__ __forceinline__ void draft_keys(const TreeArgs& A, const Cursor& c, uint8_t* dst, int r0,
+                                           int r1, int lane) {
+  constexpr int kC = DH / 8;   // 16-byte columns of a row
+  r1 = min(r1, c.dl);
+  for (int i = r0 * kC + lane; i < r1 * kC; i += 32) {
+    const int r = i / kC, cc = i % kC;
+    const int64_t hr = (static_cast<int64_t>(c.b) * A.n_draft + r) * A.n_hkv + c.kvh;
+    if (!tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hkv, A.status)) continue;
+    cp16(tg::smem_u32(dst) + tile_off(r, cc), A.kd + hr * DH + 8 * cc, true);
+  }
+  cp_wait_all();
+}
+
+// The same for drafted values: zeros behind the last one up to a multiple of 16 rows and
+// in place of what is not finite. Rows r0 .. r1 - 1 lie in 16-row words r0 / 16, ...
+template <int DH>
+__device__ __forceinline__ void draft_values(const TreeArgs& A, const Cursor& c, uint8_t* dst,
+                                             uint16_t* bad, int r0, int r1, int lane) {
+  constexpr int kC = DH / 8;
+  for (int w = r0; w < r1; w += 16) {   // one word of `bad` at a time
+    uint32_t word = 0;
+    for (int i = w * kC + lane; i < (w + 16) * kC; i += 32) {
+      const int r = i / kC, cc = i % kC;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      const int64_t hr = (static_cast<int64_t>(c.b) * A.n_draft + r) * A.n_hkv + c.kvh;
+      if (r < c.dl && tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hkv, A.status))
+        x = *reinterpret_cast<const uint4*>(A.vd + hr * DH + 8 * cc);
+      bool inf = false;
+      x.x = finite2(x.x, &inf);
+      x.y = finite2(x.y, &inf);
+      x.z = finite2(x.z, &inf);
+      x.w = finite2(x.w, &inf);
+      if (inf) word |= 1u << (r - w);
+      *reinterpret_cast<uint4*>(dst + tile_off(r, cc)) = x;
+    }
+    word = __reduce_or_sync(0xFFFFFFFFu, word);
+    if (lane == 0) bad[w >> 4] = static_cast<uint16_t>(word);
   }
 }
 
-// One warp per (sequence, drafted token, query head), one key at a time.
 template <int DH, int kType>
-__global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeArgs A) {
+__global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs A) {
+  constexpr bool kQ = kType != TG_BF16;
+  using C = Cfg<DH, kQ>;
+  using Smem = TreeSmem<DH, kQ>;
+  constexpr uint32_t kTileBytes = C::kHalves * kHalfBytes;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (tg::smem_u32(smem_raw) & 1023u)) & 1023u;
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw + pad);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = A.group * A.tm;                    // rows in use of a row tile
+  const int n_act = (rows + 15) / 16;                 // softmax warps with rows
+
+  if (tid == 0) {
+    tg::mbar_init(&S.q_full, 1);
+    tg::mbar_init(&S.q_empty, 1);
+    for (int s = 0; s < C::kK; ++s) {
+      tg::mbar_init(&S.k_full[s], C::kFullArrivals);
+      tg::mbar_init(&S.k_empty[s], 1);
+    }
+    for (int s = 0; s < C::kV; ++s) {
+      tg::mbar_init(&S.v_full[s], C::kFullArrivals);
+      tg::mbar_init(&S.v_empty[s], 1);
+    }
+    for (int s = 0; s < C::kRaw; ++s) {
+      tg::mbar_init(&S.raw_full[s], 1);
+      tg::mbar_init(&S.raw_empty[s], kConvWarps);
+    }
+    for (int s = 0; s < kKeyStages; ++s) {
+      tg::mbar_init(&S.b_full[s], 32);
+      tg::mbar_init(&S.b_empty[s], n_act);
+    }
+    for (int s = 0; s < C::kS; ++s) {
+      tg::mbar_init(&S.s_full[s], 1);
+      tg::mbar_init(&S.p_full[s], n_act);
+      tg::mbar_init(&S.o_done[s], 1);
+    }
+    tg::mbar_init(&S.o_free, n_act);
+    S.abort_flag = 0;
+    tg::fence_barrier_init();
+    tg::tma_prefetch_desc(&tm_q);
+    tg::tma_prefetch_desc(&tm_k);
+    tg::tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 2) {
+    tg::tmem_alloc(&S.tmem_base, kTmemCols);
+    tg::tmem_relinquish();
+  }
+  tg::pdl_launch_dependents();
+  tg::pdl_wait();   // global memory only from here on
+  for (int b = tid; b < A.batch; b += C::kThreads) {
+    const int2 l = seq_lens(A, b, blockIdx.x == 0);
+    S.len[b] = l.x;
+    S.dl[b] = static_cast<uint8_t>(l.y);
+    S.base[b + 1] = static_cast<int64_t>(A.n_hkv) * row_tiles(A, l.y) * key_tiles(l.x);
+  }
+  tg::tc_fence_before();
+  __syncthreads();
+  tg::tc_fence_after();
+  if (warp == 0) {   // running sums of the units
+    int64_t carry = 0;
+    for (int b0 = 0; b0 < A.batch; b0 += 32) {
+      int64_t x = b0 + lane < A.batch ? S.base[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b0 + lane < A.batch) S.base[b0 + lane + 1] = carry + x;
+      carry += __shfl_sync(0xFFFFFFFFu, x, 31);
+    }
+    if (lane == 0) S.base[0] = 0;
+  }
+  __syncthreads();
+  const uint32_t tmem = S.tmem_base;
+  const int64_t W = S.base[A.batch];
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= A.batch; b += C::kThreads) A.base[b] = S.base[b];
+  const int64_t G = share_ctas(A, W), cta = blockIdx.x;
+  const int64_t u0 = cta < G ? W * cta / G : 0, u1 = cta < G ? W * (cta + 1) / G : 0;
+  const int n = static_cast<int>(u1 - u0);
+  if (n == 0) {   // uniform: nothing to do here
+    if (warp == 2) tg::tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
+  Cursor c;
+  c.start(A, S, u0, u1);
+
+  if (!kQ && (warp == 0 || warp == 3)) {
+    // ---------------- K (warp 0) or V (warp 3) tiles of a bf16 cache ----------------
+    const bool val = warp == 3;
+    constexpr int kC = DH / 8;
+    const int n_st = val ? C::kV : C::kK;
+    uint64_t* full = val ? S.v_full : S.k_full;
+    uint64_t* empty = val ? S.v_empty : S.k_empty;
+    const CUtensorMap* map = val ? &tm_v : &tm_k;
+    const __nv_bfloat16* cache = reinterpret_cast<const __nv_bfloat16*>(val ? A.vc : A.kc);
+    int n_draft = 0, g = 0;
+    for (; g < n; ++g, c.advance(A, S)) {
+      const int s = g % n_st;
+      if (g >= n_st &&
+          !all_alive(tg::mbar_wait(&empty[s], ((g / n_st) - 1) & 1, A.status, &S.abort_flag)))
+        break;
+      uint8_t* dst = val ? S.v[s % C::kV][0] : S.k[s % C::kK][0];
+      const int nv = c.keys();
+      if (c.draft() || nv < kBN) {
+        if (!c.draft()) {
+          const int r1 = val ? (nv + 15) & ~15 : nv;
+          for (int i = lane; i < r1 * kC; i += 32) {
+            const int r = i / kC, cc = i % kC;
+            const int64_t hr = (static_cast<int64_t>(c.b) * A.cap + c.j * kBN + min(r, nv - 1)) * A.n_hkv + c.kvh;
+            const bool ok = r < nv && tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.cap * A.n_hkv, A.status);
+            cp16(tg::smem_u32(dst) + tile_off(r, cc), cache + hr * DH + 8 * cc, ok);
+          }
+          cp_wait_all();
+        } else if (val) {
+          draft_values<DH>(A, c, dst, S.bad[n_draft % kBadRing], 0, kMaxDraft, lane);
+        } else {
+          draft_keys<DH>(A, c, dst, 0, kMaxDraft, lane);
+        }
+        tg::fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) tg::mbar_arrive(&full[s]);
+      } else if (lane == 0) {
+        tg::mbar_arrive_expect_tx(&full[s], kTileBytes);
+        const int row = static_cast<int>(static_cast<int64_t>(c.b) * A.cap + c.j * kBN);
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          tg::tma_load_3d(dst + h * kHalfBytes, map, &full[s], 64 * h, c.kvh, row);
+      }
+      if (c.draft()) ++n_draft;
+      __syncwarp();
+    }
+    if (S.abort_flag && lane == 0)   // let copies in flight land before the CTA exits
+      for (int i = g > n_st ? g - n_st : 0; i < g; ++i)
+        tg::mbar_wait(&full[i % n_st], (i / n_st) & 1, A.status, nullptr);
+    __syncwarp();
+  } else if (kQ && warp == 0) {
+    // ---------------- codes by TMA: K_0, K_1, V_0, K_2, V_1, ... ----------------
+    if (lane == 0) {
+      Cursor cv = c;
+      int r = 0;
+      auto load = [&](const Cursor& t, const CUtensorMap* map) -> bool {
+        if (t.draft()) return true;   // drafted rows are bf16: the converters read them
+        const int s = r % C::kRaw;
+        if (r >= C::kRaw &&
+            !tg::mbar_wait(&S.raw_empty[s], ((r / C::kRaw) - 1) & 1, A.status, &S.abort_flag))
+          return false;
+        tg::mbar_arrive_expect_tx(&S.raw_full[s], C::kRawBytes);
+        tg::tma_load_3d(S.raw[s], map, &S.raw_full[s], 0, t.kvh,
+                        static_cast<int>(static_cast<int64_t>(t.b) * A.cap + t.j * kBN));
+        ++r;
+        return true;
+      };
+      bool alive = load(c, &tm_k);
+      for (int g = 0; g < n && alive; ++g) {
+        if (g + 1 < n) {
+          c.advance(A, S);
+          alive = load(c, &tm_k);
+        }
+        if (alive) alive = load(cv, &tm_v);
+        cv.advance(A, S);
+      }
+      if (S.abort_flag)
+        for (int i = r > C::kRaw ? r - C::kRaw : 0; i < r; ++i)
+          tg::mbar_wait(&S.raw_full[i % C::kRaw], (i / C::kRaw) & 1, A.status, nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------- queries, and what each key brings besides K and V ----------------
+    constexpr int kN = kQ ? 3 : 1;
+    Cursor la = c;   // loads run two tiles ahead
+    int g_la = 0;
+    auto load_next = [&](float (&x)[kN][4]) {
+      const bool there = g_la < n;
+      const int nv = there ? la.keys() : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = lane + 32 * i;
+        x[0][i] = 0.f;
+        if constexpr (kQ) x[1][i] = x[2][i] = 1.f;
+        if (j >= nv) continue;
+        if (la.draft()) {
+          const int64_t row = static_cast<int64_t>(la.b) * A.n_draft + j;
+          if (tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.n_draft, A.status)) x[0][i] = A.sd[row];
+        } else {
+          const int64_t row = static_cast<int64_t>(la.b) * A.cap + la.j * kBN + j;
+          if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
+          x[0][i] = A.sc[row];
+          if constexpr (kQ) {
+            x[1][i] = A.ks[row * A.n_hkv + la.kvh];
+            x[2][i] = A.vs[row * A.n_hkv + la.kvh];
+          }
+        }
+      }
+      if (there) {
+        la.advance(A, S);
+        ++g_la;
+      }
+    };
+    float x0[kN][4], x1[kN][4], x2[kN][4];
+    load_next(x0);
+    load_next(x1);
+    load_next(x2);
+    int n_q = 0;
+    for (int g = 0; g < n; ++g, c.advance(A, S)) {
+      if (g == 0 || c.j == 0) {   // a new item: its queries, once the last one's S are done
+        if (n_q > 0 &&
+            !all_alive(tg::mbar_wait(&S.q_empty, (n_q - 1) & 1, A.status, &S.abort_flag)))
+          break;
+        if (lane == 0) {
+          tg::mbar_arrive_expect_tx(&S.q_full, C::kHalves * rows * 128);
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tg::tma_load_3d(S.q[h], &tm_q, &S.q_full, 64 * h, c.kvh * A.group,
+                            c.b * A.n_draft + c.mt * A.tm);
+        }
+        ++n_q;
+        __syncwarp();
+      }
+      const int s = g % kKeyStages;
+      if (g >= kKeyStages &&
+          !all_alive(tg::mbar_wait(&S.b_empty[s], ((g / kKeyStages) - 1) & 1, A.status, &S.abort_flag)))
+        break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = lane + 32 * i;
+        S.key[s][0][j] = x0[0][i];
+        if constexpr (kQ) {
+          // a value scale of 0 has codes 0: any weight will do, and 1 keeps the row sum
+          const float vs = x0[2][i] == 0.f ? 1.f : x0[2][i];
+          S.key[s][1][j] = x0[1][i];
+          S.key[s][2][j] = vs;
+          S.key[s][3][j] = 1.f / vs;
+        }
+      }
+      tg::mbar_arrive(&S.b_full[s]);
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x0[e][i] = x1[e][i];
+          x1[e][i] = x2[e][i];
+        }
+      load_next(x2);
+    }
+    if (S.abort_flag && n_q > 0 && lane == 0)
+      tg::mbar_wait(&S.q_full, (n_q - 1) & 1, A.status, nullptr);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = tg::idesc_bf16_f32(kBM, kBN, false, false);
+      constexpr uint32_t idesc_o = tg::idesc_bf16_f32(kBM, DH, false, true);
+      const uint32_t q0 = tg::smem_u32(S.q[0]);
+      auto issue_s = [&](int g) -> bool {
+        const int s = g % C::kK;
+        if (!tg::mbar_wait(&S.k_full[s], (g / C::kK) & 1, A.status, &S.abort_flag)) return false;
+        tg::tc_fence_after();
+        const uint32_t k0 = tg::smem_u32(S.k[s][0]);
+        const uint32_t d = tmem + 128u * (g % C::kS);
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+          tg::mma_bf16_ss(d, tg::smem_desc_sw128(q0 + off, 16, 1024),
+                          tg::smem_desc_sw128(k0 + off, 16, 1024), idesc_s, kk != 0);
+        }
+        tg::mma_commit(&S.s_full[g % C::kS]);
+        tg::mma_commit(&S.k_empty[s]);
+        return true;
+      };
+      bool alive = true;
+      int g0 = 0;
+      for (int seg = 0; g0 < n && alive; ++seg) {
+        const int nt = c.run();
+        alive = tg::mbar_wait(&S.q_full, seg & 1, A.status, &S.abort_flag);
+        for (int j = 0; j < C::kS && j < nt && alive; ++j) alive = issue_s(g0 + j);
+        if (alive && nt <= C::kS) tg::mma_commit(&S.q_empty);   // every S of the item issued
+        for (int j = 0; j < nt && alive; ++j) {
+          const int g = g0 + j, s = g % C::kV;
+          alive = tg::mbar_wait(&S.p_full[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag) &&
+                  tg::mbar_wait(&S.v_full[s], (g / C::kV) & 1, A.status, &S.abort_flag);
+          if (alive && j == 0 && seg > 0)
+            alive = tg::mbar_wait(&S.o_free, (seg - 1) & 1, A.status, &S.abort_flag);
+          if (!alive) break;
+          tg::tc_fence_after();
+          const uint32_t v0 = tg::smem_u32(S.v[s][0]);
+          const int steps = (c.keys() + 15) / 16;   // rows of V behind these are not set
+          for (int kk = 0; kk < steps; ++kk) {
+            const uint64_t bdesc = tg::smem_desc_sw128(v0 + kk * 16 * 128, kHalfBytes, 1024);
+            tg::mma_bf16_ts(tmem + kColO, tmem + 128u * (g % C::kS) + kk * 8, bdesc, idesc_o, (j | kk) != 0);
+          }
+          tg::mma_commit(&S.o_done[g % C::kS]);
+          tg::mma_commit(&S.v_empty[s]);
+          if (j + C::kS < nt) {
+            alive = issue_s(g + C::kS);
+            if (alive && j + C::kS + 1 == nt) tg::mma_commit(&S.q_empty);
+          }
+          c.advance(A, S);
+        }
+        g0 += nt;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 4 + kSoftmaxWarps) {
+    // ---------------- softmax: one warp per 16 rows ----------------
+    // 16x256b TMEM loads: thread l holds rows ra = l/4 and rb = ra + 8 of the warp's 16
+    // at columns 8i + 2(l%4) + {0, 1}, so a row's keys sit in one quad of threads.
+    const int row0 = (warp & 3) * 32 + ((warp - 4) >> 2) * 16;
+    if (row0 < rows) {
+      const int r2[2] = {row0 + (lane >> 2), row0 + (lane >> 2) + 8};
+      const int cq = 2 * (lane & 3);
+      const uint32_t lane_base = static_cast<uint32_t>(row0) << 16;
+      float ch[2], gh[2], m[2], l[2];
+      uint64_t see[2];
+      int seg = 0, n_draft = 0;
+      bool first = true, whole = false, alive = true;
+      for (int g = 0; g < n; ++g) {
+        if (first) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int hq = c.kvh * A.group + r2[e] % A.group;
+            ch[e] = kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]);
+            gh[e] = A.gain[hq] * kLog2e;
+            const int t = c.mt * A.tm + r2[e] / A.group;   // tokens behind the last see nothing
+            see[e] = t < c.dl && c.j + c.run() == c.nt
+                         ? static_cast<uint64_t>(A.mask[static_cast<int64_t>(c.b) * A.n_draft + t]) : 0;
+            if (c.dl < 64) see[e] &= (1ull << c.dl) - 1;
+            m[e] = -INFINITY;
+            l[e] = 0.f;
+          }
+          whole = c.j == 0;
+        }
+        const int s = g % kKeyStages;
+        const uint32_t sbuf = tmem + lane_base + 128u * (g % C::kS);
+        alive = tg::mbar_wait(&S.s_full[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag) &&
+                tg::mbar_wait(&S.b_full[s], (g / kKeyStages) & 1, A.status, &S.abort_flag);
+        if (!all_alive(alive)) { alive = false; break; }
+        tg::tc_fence_after();
+        float z[64];
+        {
+          uint32_t u[64];
+          tg::tmem_ld_16x256b_x16(sbuf, u);
+          tg::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 sk = *reinterpret_cast<const float2*>(&S.key[s][0][8 * i + cq]);
+            float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                          __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
+            if constexpr (kQ) {
+              const float2 ks = *reinterpret_cast<const float2*>(&S.key[s][1][8 * i + cq]);
+              fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
+              fmul2(x[2], x[3], x[2], x[3], ks.x, ks.y);
+            }
+            float b0, b1;
+            fmul2(b0, b1, gh[0], gh[0], sk.x, sk.y);
+            ffma2(z[4 * i], z[4 * i + 1], x[0], x[1], ch[0], ch[0], b0, b1);
+            fmul2(b0, b1, gh[1], gh[1], sk.x, sk.y);
+            ffma2(z[4 * i + 2], z[4 * i + 3], x[2], x[3], ch[1], ch[1], b0, b1);
+          }
+        }
+        const int nv = c.keys();
+        if (c.draft()) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int col = 8 * i + cq + (e & 1);
+              if (i >= 8 || !((see[e >> 1] >> (col & 63)) & 1)) z[4 * i + e] = -INFINITY;
+            }
+        } else if (nv < kBN) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (8 * i + cq + (e & 1) >= nv) z[4 * i + e] = -INFINITY;
+        }
+        float alpha[2] = {1.f, 1.f}, nm[2];
+        bool rescale = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t0 = fmaxf(z[2 * e], z[2 * e + 1]), t1 = fmaxf(z[4 + 2 * e], z[5 + 2 * e]);
+#pragma unroll
+          for (int i = 2; i < 16; i += 2) {
+            t0 = fmaxf(t0, fmaxf(z[4 * i + 2 * e], z[4 * i + 2 * e + 1]));
+            t1 = fmaxf(t1, fmaxf(z[4 * i + 4 + 2 * e], z[4 * i + 5 + 2 * e]));
+          }
+          float mt = fmaxf(t0, t1);
+          mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 1));
+          mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2));
+          if (first) {
+            m[e] = mt;
+          } else if (mt > m[e] + kRescaleThreshold) {
+            alpha[e] = tg::exp2_approx(m[e] - mt);
+            m[e] = mt;
+            rescale = true;
+          }
+          nm[e] = m[e] == -INFINITY ? 0.f : -m[e];   // a row that has seen nothing: weights 0
+        }
+        uint32_t pk[32];
+        float sum[2][2] = {};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            fadd2(p[2 * e], p[2 * e + 1], z[4 * i + 2 * e], z[4 * i + 2 * e + 1], nm[e], nm[e]);
+            p[2 * e] = tg::exp2_approx(p[2 * e]);
+            p[2 * e + 1] = tg::exp2_approx(p[2 * e + 1]);
+          }
+          if constexpr (kQ) {
+            const float2 vs = *reinterpret_cast<const float2*>(&S.key[s][2][8 * i + cq]);
+            const float2 iv = *reinterpret_cast<const float2*>(&S.key[s][3][8 * i + cq]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              fmul2(p[2 * e], p[2 * e + 1], p[2 * e], p[2 * e + 1], vs.x, vs.y);
+              pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
+              ffma2(sum[e][0], sum[e][1], bf16_lo(pk[2 * i + e]), bf16_hi(pk[2 * i + e]), iv.x, iv.y,
+                    sum[e][0], sum[e][1]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
+              fadd2(sum[e][0], sum[e][1], bf16_lo(pk[2 * i + e]), bf16_hi(pk[2 * i + e]), sum[e][0],
+                    sum[e][1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tg::mbar_arrive(&S.b_empty[s]);   // this warp is done with the keys' data
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], alpha[e], sum[e][0] + sum[e][1]);
+        if (__any_sync(0xFFFFFFFFu, rescale)) {
+          // O must hold PV_{g-1} before it is scaled
+          alive = tg::mbar_wait(&S.o_done[(g - 1) % C::kS], ((g - 1) / C::kS) & 1, A.status, &S.abort_flag);
+          if (!all_alive(alive)) { alive = false; break; }
+          tg::tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h) {
+            uint32_t o[32];
+            const uint32_t at = tmem + lane_base + kColO + 64u * h;
+            tg::tmem_ld_16x256b_x8(at, o);
+            tg::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
+            tg::tmem_st_16x256b_x8(at, o);
+          }
+        }
+        tg::tmem_st_16x128b_x16(sbuf, pk);   // P_g over S_g
+        tg::tmem_st_wait();
+        tg::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tg::mbar_arrive(&S.p_full[g % C::kS]);
+        first = c.run() == 1;   // the last unit of its item here: O is complete after PV_g
+        if (first) {
+          const bool with_draft = c.draft();
+          whole = whole && with_draft;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+          }
+          alive = tg::mbar_wait(&S.o_done[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag);
+          if (!all_alive(alive)) { alive = false; break; }
+          tg::tc_fence_after();
+          uint64_t bad = 0;
+          if (with_draft) bad = *reinterpret_cast<const uint64_t*>(S.bad[n_draft % kBadRing]);
+          const int slot = 2 * blockIdx.x + (seg > 0);
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h) {
+            uint32_t o[32];
+            tg::tmem_ld_16x256b_x8(tmem + lane_base + kColO + 64u * h, o);
+            tg::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int t = c.mt * A.tm + r2[e] / A.group, gq = r2[e] % A.group;
+              if (r2[e] >= rows || t >= c.dl) continue;
+              for (uint64_t left = bad & see[e]; left; left &= left - 1) {
+                // a visible drafted row with infinities or NaN: they join O here
+                const int r = __ffsll(static_cast<long long>(left)) - 1;
+                const __nv_bfloat16* v =
+                    A.vd + ((static_cast<int64_t>(c.b) * A.n_draft + r) * A.n_hkv + c.kvh) * DH + 64 * h + cq;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float x = __bfloat162float(v[8 * (i >> 1) + (i & 1)]);
+                  uint32_t& y = o[4 * (i >> 1) + 2 * e + (i & 1)];
+                  if (!isfinite(x)) y = __float_as_uint(__uint_as_float(y) + x);
+                }
+              }
+              if (whole) {
+                const int64_t row = (static_cast<int64_t>(c.b) * A.n_draft + t) * A.n_hq + c.kvh * A.group + gq;
+                if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)) continue;
+                const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];   // nothing seen: zeros
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  *reinterpret_cast<uint32_t*>(A.out + row * DH + 64 * h + 8 * i + cq) =
+                      tg::pack_bf16x2(__uint_as_float(o[4 * i + 2 * e]) * inv,
+                                      __uint_as_float(o[4 * i + 2 * e + 1]) * inv);
+              } else {
+                float* pr = A.part + (static_cast<int64_t>(slot) * rows + r2[e]) * DH + 64 * h + cq;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  *reinterpret_cast<uint2*>(pr + 8 * i) = make_uint2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
+                if (h == 0 && (lane & 3) == 0) {
+                  float* ml = A.part + static_cast<int64_t>(2 * A.n_cta) * rows * DH +
+                              (static_cast<int64_t>(slot) * rows + r2[e]) * 2;
+                  *reinterpret_cast<float2*>(ml) = make_float2(m[e], l[e]);
+                }
+              }
+            }
+          }
+          tg::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tg::mbar_arrive(&S.o_free);   // O may be overwritten
+          if (with_draft) ++n_draft;
+          ++seg;
+        }
+        c.advance(A, S);
+      }
+    }
+  } else if (kQ && warp >= 4 + kSoftmaxWarps) {
+    // ---------------- codes to operand tiles, 32 rows a warp ----------------
+    constexpr bool kE4m3 = kType == TG_E4M3;
+    const int cw = warp - 4 - kSoftmaxWarps;
+    Cursor cv = c;
+    int r = 0, gk = 0, gv = 0, n_draft = 0;
+    auto convert = [&](const Cursor& t, bool val) -> bool {
+      int& g = val ? gv : gk;
+      const int n_st = val ? C::kV : C::kK, s = g % n_st;
+      uint64_t* full = val ? &S.v_full[s % C::kV] : &S.k_full[s % C::kK];
+      uint64_t* empty = val ? &S.v_empty[s % C::kV] : &S.k_empty[s % C::kK];
+      uint8_t* dst = val ? S.v[s % C::kV][0] : S.k[s % C::kK][0];
+      if (g >= n_st && !all_alive(tg::mbar_wait(empty, ((g / n_st) - 1) & 1, A.status, &S.abort_flag)))
+        return false;
+      if (t.draft()) {
+        if (val) draft_values<DH>(A, t, dst, S.bad[n_draft++ % kBadRing], 16 * cw, 16 * cw + 16, lane);
+        else draft_keys<DH>(A, t, dst, 16 * cw, 16 * cw + 16, lane);
+      } else {
+        const int rs = r % C::kRaw;
+        if (!all_alive(tg::mbar_wait(&S.raw_full[rs], (r / C::kRaw) & 1, A.status, &S.abort_flag)))
+          return false;
+        constexpr int kC16 = DH / 16;        // 16-code columns of a row
+        constexpr int kRpp = 32 / kC16;      // rows a pass
+        const int c16 = lane % kC16, nv = t.keys();
+        const int r1 = (nv + 15) & ~15;      // rows behind are not multiplied
+#pragma unroll 4
+        for (int rr = 32 * cw + lane / kC16; rr < 32 * cw + 32; rr += kRpp) {
+          uint4 x = *reinterpret_cast<const uint4*>(S.raw[rs] + rr * DH + 16 * c16);
+          if (val && rr >= nv) x = make_uint4(0, 0, 0, 0);
+          if (rr >= r1) continue;
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[2 * i] = widen2<kE4m3>(w[i], kE4m3 ? 0x1404 : 0x4140);
+            y[2 * i + 1] = widen2<kE4m3>(w[i], kE4m3 ? 0x3424 : 0x4342);
+          }
+          // lanes of the two column halves store their two 16-byte pieces in opposite
+          // order, so that a quarter warp's stores fall into different banks
+          const int sw = (c16 >> 2) & 1;
+          *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * c16 + sw)) =
+              sw ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * c16 + 1 - sw)) =
+              sw ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        __syncwarp();
+        if (lane == 0) tg::mbar_arrive(&S.raw_empty[rs]);
+        ++r;
+      }
+      tg::fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) tg::mbar_arrive(full);
+      ++g;
+      return true;
+    };
+    bool alive = convert(c, false);
+    for (int g = 0; g < n && alive; ++g) {
+      if (g + 1 < n) {
+        c.advance(A, S);
+        alive = convert(c, false);
+      }
+      if (alive) alive = convert(cv, true);
+      cv.advance(A, S);
+    }
+  }
+  tg::tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tg::tc_fence_after();
+    tg::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Adds up the partials of the items that were cut, one warp per output row: the row's
+// CTAs c0 .. c1 in order. What CTA c holds of an item is its first segment (slot 2c)
+// unless the item starts inside its share (slot 2c + 1).
+constexpr int kCombineWarps = 4;
+
+template <int DH>
+__global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const TreeArgs A) {
   constexpr int kE = DH / 32;
   tg::pdl_launch_dependents();
   tg::pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
   if (w >= static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq) return;
   const int hq = static_cast<int>(w % A.n_hq);
   const int64_t bt = w / A.n_hq;
   const int t = static_cast<int>(bt % A.n_draft), b = static_cast<int>(bt / A.n_draft);
-  const int kvh = hq / (A.n_hq / A.n_hkv);
-  const int len = A.cache_len[b], dl = A.draft_len ? A.draft_len[b] : A.n_draft;
-  if (len < 0 || len > A.cap || len > A.max_len || dl < 0 || dl > A.n_draft) {
-    if (lane == 0) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
-    return;
-  }
-  if (t >= dl) return;
-  float q[kE], o[kE];
-  const float c = kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]);
-  const float g = A.gain[hq] * kLog2e;
+  const int2 sl = seq_lens(A, b, false);
+  if (t >= sl.y) return;
+  const int64_t W = A.base[A.batch], G = share_ctas(A, W);
+  const int amt = row_tiles(A, sl.y), nt = key_tiles(sl.x);
+  const int kvh = hq / A.group, mt = t / A.tm;
+  const int row = (t - mt * A.tm) * A.group + hq - kvh * A.group, rows = A.group * A.tm;
+  const int64_t first = A.base[b] + (static_cast<int64_t>(kvh) * amt + mt) * nt;
+  const int c0 = static_cast<int>(((first + 1) * G - 1) / W);        // the CTA of unit u is the
+  const int c1 = static_cast<int>(((first + nt) * G - 1) / W);       // last c with W c / G <= u
+  if (c0 == c1) return;                                              // finished by that CTA
+  const int slot0 = 2 * c0 + (W * c0 / G != first);
+  const float* ml = A.part + static_cast<int64_t>(2 * A.n_cta) * rows * DH;
+  auto slot = [&](int c) -> int64_t { return c == c0 ? slot0 : 2 * c; };
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, ml[(slot(c) * rows + row) * 2]);
 #pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    q[e] = __bfloat162float(A.q[w * DH + lane * kE + e]);
-    o[e] = 0.f;
-  }
-  const uint64_t mask = static_cast<uint64_t>(A.mask[bt]);
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < len + dl; ++j) {
-    float k[kE], v[kE], ksc = 1.f, vsc = 1.f, s;
-    if (j < len) {
-      const int64_t row = static_cast<int64_t>(b) * A.cap + j, hr = row * A.n_hkv + kvh;
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[kE] = {};
+  for (int cb = c0; cb <= c1; cb += 32) {
+    float2 v = make_float2(-INFINITY, 0.f);
+    if (cb + lane <= c1) v = *reinterpret_cast<const float2*>(ml + (slot(cb + lane) * rows + row) * 2);
+    const float wt = tg::exp2_approx(v.x - base);
+    const int ns = min(32, c1 - cb + 1);
+#pragma unroll 8
+    for (int i = 0; i < ns; ++i) {
+      const float wi = __shfl_sync(0xFFFFFFFFu, wt, i);
+      L = fmaf(wi, __shfl_sync(0xFFFFFFFFu, v.y, i), L);
+      const float* o = A.part + (slot(cb + i) * rows + row) * DH + lane * kE;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        k[e] = cache_value<DH, kType>(A.kc, hr * DH + lane * kE + e);
-        v[e] = cache_value<DH, kType>(A.vc, hr * DH + lane * kE + e);
-      }
-      if constexpr (kType != TG_BF16) ksc = A.ks[hr], vsc = A.vs[hr];
-      s = A.sc[row];
-    } else {
-      const int i = j - len;
-      if (!((mask >> i) & 1)) continue;
-      const int64_t row = static_cast<int64_t>(b) * A.n_draft + i, hr = row * A.n_hkv + kvh;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        k[e] = __bfloat162float(A.kd[hr * DH + lane * kE + e]);
-        v[e] = __bfloat162float(A.vd[hr * DH + lane * kE + e]);
-      }
-      s = A.sd[row];
+      for (int e = 0; e < kE; ++e) acc[e] = fmaf(wi, o[e], acc[e]);
     }
-    float z = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) z = fmaf(q[e], k[e], z);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
-    z = fmaf(z * ksc, c, g * s);
-    if (z == -INFINITY) continue;   // a weight of zero
-    const float mn = fmaxf(m, z);
-    const float a = exp2f(m - mn), p = exp2f(z - mn);
-    l = fmaf(l, a, p);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = fmaf(o[e], a, p * vsc * v[e]);
-    m = mn;
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // nothing visible: zeros
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  if (!tg::in_bounds(w, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)) return;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) A.out[w * DH + lane * kE + e] = __float2bfloat16_rn(o[e] * inv);
+  for (int e = 0; e < kE; e += 2)
+    *reinterpret_cast<uint32_t*>(A.out + w * DH + lane * kE + e) =
+        tg::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// How a call is laid out: tokens per row tile, CTAs, and the workspace's two parts.
+struct Plan {
+  int tm, n_cta;
+  size_t base_bytes, bytes;
+};
+Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim) {
+  Plan p;
+  const int group = n_hq / n_hkv;
+  p.tm = kBM / group < n_draft ? kBM / group : n_draft;
+  const int64_t units = static_cast<int64_t>(batch) * n_hkv * ((n_draft + p.tm - 1) / p.tm) *
+                        ((max_len + static_cast<int64_t>(kBN) - 1) / kBN + 1);
+  p.n_cta = static_cast<int>(units < kMaxCtas ? units : kMaxCtas);
+  p.base_bytes = (static_cast<size_t>(batch) + 1) * sizeof(int64_t);
+  p.base_bytes = (p.base_bytes + 255) / 256 * 256;
+  p.bytes = p.base_bytes + static_cast<size_t>(2) * p.n_cta * group * p.tm * (head_dim + 2) * sizeof(float);
+  return p;
 }
 
 template <int DH, int kType>
-tg_status launch_tree(const TreeArgs& a, cudaStream_t st) {
+tg_status launch_tree(const TreeArgs& a, const void* q, cudaStream_t st) {
+  constexpr bool kQ = kType != TG_BF16;
+  using C = Cfg<DH, kQ>;
+  CUtensorMap tq, tk, tv;
+  const uint64_t qdims[3] = {DH, static_cast<uint64_t>(a.n_hq), static_cast<uint64_t>(a.batch) * a.n_draft};
+  const uint64_t qstr[2] = {DH * 2, static_cast<uint64_t>(a.n_hq) * DH * 2};
+  const uint32_t qbox[3] = {64, static_cast<uint32_t>(a.group), static_cast<uint32_t>(a.tm)};
+  const int es = kQ ? 1 : 2;
+  const uint64_t dims[3] = {DH, static_cast<uint64_t>(a.n_hkv), static_cast<uint64_t>(a.batch) * a.cap};
+  const uint64_t str[2] = {static_cast<uint64_t>(DH) * es, static_cast<uint64_t>(a.n_hkv) * DH * es};
+  const uint32_t box[3] = {kQ ? DH : 64, 1, kBN};
+  const auto type = kQ ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto swz = kQ ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!tg::encode_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qdims, qstr, qbox,
+                       CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tg::encode_tmap(&tk, type, 3, a.kc, dims, str, box, swz) ||
+      !tg::encode_tmap(&tv, type, 3, a.vc, dims, str, box, swz))
+    return TG_ERR_CUDA;
+  constexpr int smem = sizeof(TreeSmem<DH, kQ>) + 1024;
+  static_assert(smem <= 232448, "the shared memory of one SM");
+  if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_attn_kernel<DH, kType>), smem)) return TG_ERR_CUDA;
+  const tg_status r = tg::launch(tree_attn_kernel<DH, kType>, dim3(a.n_cta), dim3(C::kThreads), smem, st, 0,
+                                 tq, tk, tv, a);
+  if (r != TG_OK || a.max_len == 0) return r;   // without a cache every item is one unit
   const int64_t warps = static_cast<int64_t>(a.batch) * a.n_draft * a.n_hq;
-  return tg::launch(tree_attn_kernel<DH, kType>, dim3(static_cast<unsigned>((warps + 3) / 4)),
-                    dim3(kThreads), 0, st, 0, a);
+  return tg::launch(tree_combine_kernel<DH>,
+                    dim3(static_cast<unsigned>((warps + kCombineWarps - 1) / kCombineWarps)),
+                    dim3(32 * kCombineWarps), 0, st, 0, a);
 }
 
 }  // namespace
 
 extern "C" size_t tg_tree_attention_workspace_size(int batch, int n_draft, int max_len, int n_hq,
                                                    int n_hkv, int head_dim) {
-  if (batch <= 0 || n_draft <= 0 || max_len < 0 || n_hq <= 0 || n_hkv <= 0 || head_dim <= 0) return 0;
-  return 16;
+  if (batch <= 0 || n_draft <= 0 || max_len < 0 || n_hkv <= 0 || n_hq < n_hkv || n_hq / n_hkv > kBM ||
+      head_dim <= 0)
+    return 0;
+  return plan(batch, n_draft, max_len, n_hq, n_hkv, head_dim).bytes;
 }
 
 extern "C" tg_status tg_tree_attention(
@@ -146,29 +1026,31 @@ extern "C" tg_status tg_tree_attention(
     return TG_ERR_INVALID_ARG;
   const bool quantised = cache_dtype != TG_BF16;
   if (quantised ? !k_scale || !v_scale : k_scale || v_scale) return TG_ERR_INVALID_ARG;
-  if ((head_dim != 64 && head_dim != 128) || n_draft > kMaxDraft || n_hq / n_hkv > 128 ||
-      batch > 1024 || n_hkv > 1024 || static_cast<int64_t>(batch) * cap > INT32_MAX - 128)
+  if ((head_dim != 64 && head_dim != 128) || n_draft > kMaxDraft || n_hq / n_hkv > kBM ||
+      batch > kMaxBatch || n_hkv > 1024 || static_cast<int64_t>(batch) * cap > INT32_MAX - kBN)
     return TG_ERR_UNSUPPORTED;
   if (!tg::aligned16(q) || !tg::aligned16(k_draft) || !tg::aligned16(v_draft) ||
       !tg::aligned16(k_cache) || !tg::aligned16(v_cache) || !tg::aligned16(out))
     return TG_ERR_MISALIGNED;
-  const size_t need = tg_tree_attention_workspace_size(batch, n_draft, max_len, n_hq, n_hkv, head_dim);
-  if (!workspace || workspace_bytes < need) return TG_ERR_WORKSPACE;
+  const Plan p = plan(batch, n_draft, max_len, n_hq, n_hkv, head_dim);
+  if (!workspace || workspace_bytes < p.bytes) return TG_ERR_WORKSPACE;
   if (!tg::aligned16(workspace)) return TG_ERR_MISALIGNED;
   TreeArgs a = {};
-  a.q = static_cast<const __nv_bfloat16*>(q);
   a.kd = static_cast<const __nv_bfloat16*>(k_draft), a.vd = static_cast<const __nv_bfloat16*>(v_draft);
   a.sd = s_draft, a.mask = tree_mask, a.draft_len = draft_len;
   a.kc = static_cast<const uint8_t*>(k_cache), a.vc = static_cast<const uint8_t*>(v_cache);
   a.ks = k_scale, a.vs = v_scale, a.sc = s_cache, a.cache_len = cache_len;
   a.gain = gain, a.tau = tau, a.out = static_cast<__nv_bfloat16*>(out);
+  a.base = static_cast<int64_t*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.base_bytes);
   a.batch = batch, a.n_draft = n_draft, a.cap = cap, a.max_len = max_len, a.n_hq = n_hq, a.n_hkv = n_hkv;
+  a.group = n_hq / n_hkv, a.tm = p.tm, a.n_cta = p.n_cta;
   a.status = tg::status_word();
   if (!a.status) return TG_ERR_CUDA;
   if (head_dim == 128) {
-    if (cache_dtype == TG_BF16) return launch_tree<128, TG_BF16>(a, stream);
-    return cache_dtype == TG_I8 ? launch_tree<128, TG_I8>(a, stream) : launch_tree<128, TG_E4M3>(a, stream);
+    if (cache_dtype == TG_BF16) return launch_tree<128, TG_BF16>(a, q, stream);
+    return cache_dtype == TG_I8 ? launch_tree<128, TG_I8>(a, q, stream) : launch_tree<128, TG_E4M3>(a, q, stream);
   }
-  if (cache_dtype == TG_BF16) return launch_tree<64, TG_BF16>(a, stream);
-  return cache_dtype == TG_I8 ? launch_tree<64, TG_I8>(a, stream) : launch_tree<64, TG_E4M3>(a, stream);
+  if (cache_dtype == TG_BF16) return launch_tree<64, TG_BF16>(a, q, stream);
+  return cache_dtype == TG_I8 ? launch_tree<64, TG_I8>(a, q, stream) : launch_tree<64, TG_E4M3>(a, q, stream);
 }
