@@ -25,17 +25,17 @@
 //                rows) is copied row by row with the rest of it zero.
 //   warp 3       V tiles likewise (bf16 cache)
 //   warp 2       the rows' queries, and per key: score, scales (a ring of four tiles)
-//   warps 12-15  codes only: widen the raw tiles into bf16 operand tiles. Codes are exact
+//   warps 12-19  codes only: widen the raw tiles into bf16 operand tiles. Codes are exact
 //                in bf16, so scales are applied in fp32: the key's to the logit, the
 //                value's to the weight.
 //   warp 1       MMA issuer (one thread): S_0, .., PV_0, S_n, PV_1, ...; S_j = Q K_j^T into
 //                one of kS 128-column TMEM buffers, O += P_j V_j with P_j read from TMEM
 //                (it overwrites S_j) and V_j as an MN-major shared-memory operand.
 //   warps 4-11   softmax, 16 rows each, those with rows only: logits in the log2 domain,
-//                masks in the tiles that need them, a running max that moves only when it
-//                grows by more than 2^8 (O is then rescaled in TMEM), P in bf16. The row
-//                sum adds the rounded weights, so that a key which dominates its row
-//                gives its value exactly.
+//                masks in the tiles that need them, a running reference that moves only
+//                when a logit exceeds it by more than 2^8 (O is then rescaled in TMEM), P in
+//                bf16. The row sum adds the rounded weights, so that a key which dominates
+//                its row gives its value exactly.
 // The parity waits are exact for the reasons given at the gated attention's kernel:
 // S_g is issued after PV_{g - kS}, and a softmax warp is never more than kS tiles ahead.
 //
@@ -55,7 +55,7 @@ constexpr int kMaxBatch = 1024;
 constexpr int kKeyStages = 4;
 constexpr int kBadRing = 8;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = 8;
 constexpr int kMaxCtas = 148;      // one per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
@@ -133,7 +133,21 @@ struct TreeSmem {
   int abort_flag;
 };
 
+// The slow side of a wait is one function: with it inlined at every site the roles'
+// loops no longer fit the instruction cache together.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  return tg::mbar_wait(bar, parity, status, abort);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  return tg::mbar_try_wait(tg::smem_u32(bar), parity) || wait_slow(bar, parity, status, abort);
+}
 __device__ __forceinline__ bool all_alive(bool a) { return __all_sync(0xFFFFFFFFu, a); }
+
+// The order in which the tiles of a quantised cache pass, K one unit ahead of V:
+// K_0, K_1, V_0, K_2, V_1, .., K_{n-1}, V_{n-2}, V_{n-1}. Whether turn i is a V.
+__device__ __forceinline__ bool value_turn(int i, int n) {
+  return i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
+}
 
 // Walks a CTA's units in order: the unit's sequence, KV head, row tile and key tile.
 struct Cursor {
@@ -190,6 +204,15 @@ struct Cursor {
   }
 };
 
+// What the copy of one unit needs to know of it.
+struct Tile {
+  int b, kvh, j, nv;
+  bool draft;
+};
+__device__ __forceinline__ Tile tile_of(const Cursor& c) {
+  return Tile{c.b, c.kvh, c.j, c.keys(), c.draft()};
+}
+
 // 16 bytes global -> shared, or 16 zero bytes when !ok (src is not read then)
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
@@ -221,6 +244,30 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, 
       "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 16 rows by 32 columns: thread l holds (row l/4, column 4i + l%4) in register 2i and
+// the same column of row l/4 + 8 in register 2i + 1.
+__device__ __forceinline__ void tmem_ld_16x128b_x8(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x128b.x8.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32"
+      " [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
@@ -254,13 +301,14 @@ __device__ __forceinline__ uint32_t finite2(uint32_t u, bool* bad) {
 
 // Rows r0, r0 + step, .. below r1 of the drafted keys of (b, kvh) into an operand tile.
 template <int DH>
-__device__ __forceinline__ void draft_keys(const TreeArgs& A, const Cursor& c, uint8_t* dst, int r0,
-                                           int r1, int lane) {
+__device__ __noinline__ void draft_keys(const TreeArgs& A, int b, int kvh, int dl, uint8_t* dst, int r0,
+                                        int r1, int lane) {
   constexpr int kC = DH / 8;   // 16-byte columns of a row
-  r1 = min(r1, c.dl);
+  r1 = min(r1, dl);
+#pragma unroll 1
   for (int i = r0 * kC + lane; i < r1 * kC; i += 32) {
     const int r = i / kC, cc = i % kC;
-    const int64_t hr = (static_cast<int64_t>(c.b) * A.n_draft + r) * A.n_hkv + c.kvh;
+    const int64_t hr = (static_cast<int64_t>(b) * A.n_draft + r) * A.n_hkv + kvh;
     if (!tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hkv, A.status)) continue;
     cp16(tg::smem_u32(dst) + tile_off(r, cc), A.kd + hr * DH + 8 * cc, true);
   }
@@ -270,16 +318,17 @@ __device__ __forceinline__ void draft_keys(const TreeArgs& A, const Cursor& c, u
 // The same for drafted values: zeros behind the last one up to a multiple of 16 rows and
 // in place of what is not finite. Rows r0 .. r1 - 1 lie in 16-row words r0 / 16, ...
 template <int DH>
-__device__ __forceinline__ void draft_values(const TreeArgs& A, const Cursor& c, uint8_t* dst,
-                                             uint16_t* bad, int r0, int r1, int lane) {
+__device__ __noinline__ void draft_values(const TreeArgs& A, int b, int kvh, int dl, uint8_t* dst,
+                                          uint16_t* bad, int r0, int r1, int lane) {
   constexpr int kC = DH / 8;
   for (int w = r0; w < r1; w += 16) {   // one word of `bad` at a time
     uint32_t word = 0;
+#pragma unroll 2
     for (int i = w * kC + lane; i < (w + 16) * kC; i += 32) {
       const int r = i / kC, cc = i % kC;
       uint4 x = make_uint4(0, 0, 0, 0);
-      const int64_t hr = (static_cast<int64_t>(c.b) * A.n_draft + r) * A.n_hkv + c.kvh;
-      if (r < c.dl && tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hkv, A.status))
+      const int64_t hr = (static_cast<int64_t>(b) * A.n_draft + r) * A.n_hkv + kvh;
+      if (r < dl && tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hkv, A.status))
         x = *reinterpret_cast<const uint4*>(A.vd + hr * DH + 8 * cc);
       bool inf = false;
       x.x = finite2(x.x, &inf);
@@ -291,6 +340,25 @@ __device__ __forceinline__ void draft_values(const TreeArgs& A, const Cursor& c,
     }
     word = __reduce_or_sync(0xFFFFFFFFu, word);
     if (lane == 0) bad[w >> 4] = static_cast<uint16_t>(word);
+  }
+}
+
+// The values that are not finite of the drafted rows in `rows` join a token's output
+// (out, or its partial) at this thread's elements: columns cq and cq + 1 of each 8.
+template <int DH>
+__device__ __noinline__ void add_infinite(const TreeArgs& A, int b, int kvh, uint64_t rows,
+                                          __nv_bfloat16* out, float* part, int cq) {
+  for (; rows; rows &= rows - 1) {
+    const int r = __ffsll(static_cast<long long>(rows)) - 1;
+    const __nv_bfloat16* v = A.vd + ((static_cast<int64_t>(b) * A.n_draft + r) * A.n_hkv + kvh) * DH + cq;
+#pragma unroll 1
+    for (int i = 0; i < DH / 4; ++i) {
+      const int at = 8 * (i >> 1) + (i & 1);
+      const float x = __bfloat162float(v[at]);
+      if (isfinite(x)) continue;
+      if (out) out[at] = __float2bfloat16_rn(__bfloat162float(out[at]) + x);
+      else part[at] += x;
+    }
   }
 }
 
@@ -397,13 +465,14 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     for (; g < n; ++g, c.advance(A, S)) {
       const int s = g % n_st;
       if (g >= n_st &&
-          !all_alive(tg::mbar_wait(&empty[s], ((g / n_st) - 1) & 1, A.status, &S.abort_flag)))
+          !all_alive(wait(&empty[s], ((g / n_st) - 1) & 1, A.status, &S.abort_flag)))
         break;
       uint8_t* dst = val ? S.v[s % C::kV][0] : S.k[s % C::kK][0];
       const int nv = c.keys();
       if (c.draft() || nv < kBN) {
         if (!c.draft()) {
           const int r1 = val ? (nv + 15) & ~15 : nv;
+#pragma unroll 1
           for (int i = lane; i < r1 * kC; i += 32) {
             const int r = i / kC, cc = i % kC;
             const int64_t hr = (static_cast<int64_t>(c.b) * A.cap + c.j * kBN + min(r, nv - 1)) * A.n_hkv + c.kvh;
@@ -412,9 +481,9 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           }
           cp_wait_all();
         } else if (val) {
-          draft_values<DH>(A, c, dst, S.bad[n_draft % kBadRing], 0, kMaxDraft, lane);
+          draft_values<DH>(A, c.b, c.kvh, c.dl, dst, S.bad[n_draft % kBadRing], 0, kMaxDraft, lane);
         } else {
-          draft_keys<DH>(A, c, dst, 0, kMaxDraft, lane);
+          draft_keys<DH>(A, c.b, c.kvh, c.dl, dst, 0, kMaxDraft, lane);
         }
         tg::fence_proxy_async_shared();
         __syncwarp();
@@ -431,81 +500,73 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     }
     if (S.abort_flag && lane == 0)   // let copies in flight land before the CTA exits
       for (int i = g > n_st ? g - n_st : 0; i < g; ++i)
-        tg::mbar_wait(&full[i % n_st], (i / n_st) & 1, A.status, nullptr);
+        wait(&full[i % n_st], (i / n_st) & 1, A.status, nullptr);
     __syncwarp();
   } else if (kQ && warp == 0) {
     // ---------------- codes by TMA: K_0, K_1, V_0, K_2, V_1, ... ----------------
     if (lane == 0) {
-      Cursor cv = c;
+      Tile cur = {}, prev = {};
       int r = 0;
-      auto load = [&](const Cursor& t, const CUtensorMap* map) -> bool {
-        if (t.draft()) return true;   // drafted rows are bf16: the converters read them
+#pragma unroll 1
+      for (int i = 0; i < 2 * n; ++i) {
+        const bool val = value_turn(i, n);
+        if (!val) {
+          prev = cur;
+          cur = tile_of(c);
+          c.advance(A, S);
+        }
+        const Tile t = val && i < 2 * n - 1 ? prev : cur;
+        if (t.draft) continue;   // drafted rows are bf16: the converters read them
         const int s = r % C::kRaw;
-        if (r >= C::kRaw &&
-            !tg::mbar_wait(&S.raw_empty[s], ((r / C::kRaw) - 1) & 1, A.status, &S.abort_flag))
-          return false;
+        if (r >= C::kRaw && !wait(&S.raw_empty[s], ((r / C::kRaw) - 1) & 1, A.status, &S.abort_flag)) break;
         tg::mbar_arrive_expect_tx(&S.raw_full[s], C::kRawBytes);
-        tg::tma_load_3d(S.raw[s], map, &S.raw_full[s], 0, t.kvh,
+        tg::tma_load_3d(S.raw[s], val ? &tm_v : &tm_k, &S.raw_full[s], 0, t.kvh,
                         static_cast<int>(static_cast<int64_t>(t.b) * A.cap + t.j * kBN));
         ++r;
-        return true;
-      };
-      bool alive = load(c, &tm_k);
-      for (int g = 0; g < n && alive; ++g) {
-        if (g + 1 < n) {
-          c.advance(A, S);
-          alive = load(c, &tm_k);
-        }
-        if (alive) alive = load(cv, &tm_v);
-        cv.advance(A, S);
       }
       if (S.abort_flag)
         for (int i = r > C::kRaw ? r - C::kRaw : 0; i < r; ++i)
-          tg::mbar_wait(&S.raw_full[i % C::kRaw], (i / C::kRaw) & 1, A.status, nullptr);
+          wait(&S.raw_full[i % C::kRaw], (i / C::kRaw) & 1, A.status, nullptr);
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---------------- queries, and what each key brings besides K and V ----------------
     constexpr int kN = kQ ? 3 : 1;
-    Cursor la = c;   // loads run two tiles ahead
-    int g_la = 0;
-    auto load_next = [&](float (&x)[kN][4]) {
-      const bool there = g_la < n;
-      const int nv = there ? la.keys() : 0;
+    constexpr int kAhead = 3;
+    Cursor la = c;   // loads run three tiles ahead
+    float x[kAhead + 1][kN][4];
+    int n_q = 0;
+#pragma unroll 1
+    for (int g = -kAhead; g < n; ++g) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = lane + 32 * i;
-        x[0][i] = 0.f;
-        if constexpr (kQ) x[1][i] = x[2][i] = 1.f;
-        if (j >= nv) continue;
-        if (la.draft()) {
-          const int64_t row = static_cast<int64_t>(la.b) * A.n_draft + j;
-          if (tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.n_draft, A.status)) x[0][i] = A.sd[row];
-        } else {
-          const int64_t row = static_cast<int64_t>(la.b) * A.cap + la.j * kBN + j;
-          if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
-          x[0][i] = A.sc[row];
+      for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+        for (int e = 0; e < kN; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[a][e][i] = x[a + 1][e][i];
+      if (g + kAhead < n) {
+        const bool draft = la.draft();
+        const int nv = la.keys();
+        const int64_t row0 = draft ? static_cast<int64_t>(la.b) * A.n_draft
+                                   : static_cast<int64_t>(la.b) * A.cap + la.j * kBN;
+        const int64_t n_rows = static_cast<int64_t>(A.batch) * (draft ? A.n_draft : A.cap);
+        const float* sc = (draft ? A.sd : A.sc) + row0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = lane + 32 * i;
+          const bool there = j < nv && tg::in_bounds(row0 + j, n_rows, A.status);
+          x[kAhead][0][i] = there ? sc[j] : 0.f;
           if constexpr (kQ) {
-            x[1][i] = A.ks[row * A.n_hkv + la.kvh];
-            x[2][i] = A.vs[row * A.n_hkv + la.kvh];
+            const int64_t hr = (row0 + j) * A.n_hkv + la.kvh;
+            x[kAhead][1][i] = there && !draft ? A.ks[hr] : 1.f;
+            x[kAhead][2][i] = there && !draft ? A.vs[hr] : 1.f;
           }
         }
-      }
-      if (there) {
         la.advance(A, S);
-        ++g_la;
       }
-    };
-    float x0[kN][4], x1[kN][4], x2[kN][4];
-    load_next(x0);
-    load_next(x1);
-    load_next(x2);
-    int n_q = 0;
-    for (int g = 0; g < n; ++g, c.advance(A, S)) {
+      if (g < 0) continue;
       if (g == 0 || c.j == 0) {   // a new item: its queries, once the last one's S are done
-        if (n_q > 0 &&
-            !all_alive(tg::mbar_wait(&S.q_empty, (n_q - 1) & 1, A.status, &S.abort_flag)))
-          break;
+        if (n_q > 0 && !all_alive(wait(&S.q_empty, (n_q - 1) & 1, A.status, &S.abort_flag))) break;
         if (lane == 0) {
           tg::mbar_arrive_expect_tx(&S.q_full, C::kHalves * rows * 128);
 #pragma unroll
@@ -518,32 +579,25 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       }
       const int s = g % kKeyStages;
       if (g >= kKeyStages &&
-          !all_alive(tg::mbar_wait(&S.b_empty[s], ((g / kKeyStages) - 1) & 1, A.status, &S.abort_flag)))
+          !all_alive(wait(&S.b_empty[s], ((g / kKeyStages) - 1) & 1, A.status, &S.abort_flag)))
         break;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = lane + 32 * i;
-        S.key[s][0][j] = x0[0][i];
+        S.key[s][0][j] = x[0][0][i];
         if constexpr (kQ) {
           // a value scale of 0 has codes 0: any weight will do, and 1 keeps the row sum
-          const float vs = x0[2][i] == 0.f ? 1.f : x0[2][i];
-          S.key[s][1][j] = x0[1][i];
+          const float vs = x[0][2][i] == 0.f ? 1.f : x[0][2][i];
+          S.key[s][1][j] = x[0][1][i];
           S.key[s][2][j] = vs;
           S.key[s][3][j] = 1.f / vs;
         }
       }
       tg::mbar_arrive(&S.b_full[s]);
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x0[e][i] = x1[e][i];
-          x1[e][i] = x2[e][i];
-        }
-      load_next(x2);
+      c.advance(A, S);
     }
     if (S.abort_flag && n_q > 0 && lane == 0)
-      tg::mbar_wait(&S.q_full, (n_q - 1) & 1, A.status, nullptr);
+      wait(&S.q_full, (n_q - 1) & 1, A.status, nullptr);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
@@ -553,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       const uint32_t q0 = tg::smem_u32(S.q[0]);
       auto issue_s = [&](int g) -> bool {
         const int s = g % C::kK;
-        if (!tg::mbar_wait(&S.k_full[s], (g / C::kK) & 1, A.status, &S.abort_flag)) return false;
+        if (!wait(&S.k_full[s], (g / C::kK) & 1, A.status, &S.abort_flag)) return false;
         tg::tc_fence_after();
         const uint32_t k0 = tg::smem_u32(S.k[s][0]);
         const uint32_t d = tmem + 128u * (g % C::kS);
@@ -571,15 +625,15 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       int g0 = 0;
       for (int seg = 0; g0 < n && alive; ++seg) {
         const int nt = c.run();
-        alive = tg::mbar_wait(&S.q_full, seg & 1, A.status, &S.abort_flag);
+        alive = wait(&S.q_full, seg & 1, A.status, &S.abort_flag);
         for (int j = 0; j < C::kS && j < nt && alive; ++j) alive = issue_s(g0 + j);
         if (alive && nt <= C::kS) tg::mma_commit(&S.q_empty);   // every S of the item issued
         for (int j = 0; j < nt && alive; ++j) {
           const int g = g0 + j, s = g % C::kV;
-          alive = tg::mbar_wait(&S.p_full[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag) &&
-                  tg::mbar_wait(&S.v_full[s], (g / C::kV) & 1, A.status, &S.abort_flag);
+          alive = wait(&S.p_full[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag) &&
+                  wait(&S.v_full[s], (g / C::kV) & 1, A.status, &S.abort_flag);
           if (alive && j == 0 && seg > 0)
-            alive = tg::mbar_wait(&S.o_free, (seg - 1) & 1, A.status, &S.abort_flag);
+            alive = wait(&S.o_free, (seg - 1) & 1, A.status, &S.abort_flag);
           if (!alive) break;
           tg::tc_fence_after();
           const uint32_t v0 = tg::smem_u32(S.v[s][0]);
@@ -631,183 +685,208 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         }
         const int s = g % kKeyStages;
         const uint32_t sbuf = tmem + lane_base + 128u * (g % C::kS);
-        alive = tg::mbar_wait(&S.s_full[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag) &&
-                tg::mbar_wait(&S.b_full[s], (g / kKeyStages) & 1, A.status, &S.abort_flag);
+        alive = wait(&S.s_full[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag) &&
+                wait(&S.b_full[s], (g / kKeyStages) & 1, A.status, &S.abort_flag);
         if (!all_alive(alive)) { alive = false; break; }
         tg::tc_fence_after();
-        float z[64];
-        {
-          uint32_t u[64];
-          tg::tmem_ld_16x256b_x16(sbuf, u);
-          tg::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 sk = *reinterpret_cast<const float2*>(&S.key[s][0][8 * i + cq]);
-            float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
-                          __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
-            if constexpr (kQ) {
-              const float2 ks = *reinterpret_cast<const float2*>(&S.key[s][1][8 * i + cq]);
-              fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
-              fmul2(x[2], x[3], x[2], x[3], ks.x, ks.y);
-            }
-            float b0, b1;
-            fmul2(b0, b1, gh[0], gh[0], sk.x, sk.y);
-            ffma2(z[4 * i], z[4 * i + 1], x[0], x[1], ch[0], ch[0], b0, b1);
-            fmul2(b0, b1, gh[1], gh[1], sk.x, sk.y);
-            ffma2(z[4 * i + 2], z[4 * i + 3], x[2], x[3], ch[1], ch[1], b0, b1);
-          }
-        }
+        // 64 keys at a time: half the registers and half the code
         const int nv = c.keys();
-        if (c.draft()) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int col = 8 * i + cq + (e & 1);
-              if (i >= 8 || !((see[e >> 1] >> (col & 63)) & 1)) z[4 * i + e] = -INFINITY;
-            }
-        } else if (nv < kBN) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (8 * i + cq + (e & 1) >= nv) z[4 * i + e] = -INFINITY;
-        }
-        float alpha[2] = {1.f, 1.f}, nm[2];
-        bool rescale = false;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t0 = fmaxf(z[2 * e], z[2 * e + 1]), t1 = fmaxf(z[4 + 2 * e], z[5 + 2 * e]);
-#pragma unroll
-          for (int i = 2; i < 16; i += 2) {
-            t0 = fmaxf(t0, fmaxf(z[4 * i + 2 * e], z[4 * i + 2 * e + 1]));
-            t1 = fmaxf(t1, fmaxf(z[4 * i + 4 + 2 * e], z[4 * i + 5 + 2 * e]));
-          }
-          float mt = fmaxf(t0, t1);
-          mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 1));
-          mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2));
-          if (first) {
-            m[e] = mt;
-          } else if (mt > m[e] + kRescaleThreshold) {
-            alpha[e] = tg::exp2_approx(m[e] - mt);
-            m[e] = mt;
-            rescale = true;
-          }
-          nm[e] = m[e] == -INFINITY ? 0.f : -m[e];   // a row that has seen nothing: weights 0
-        }
-        uint32_t pk[32];
-        float sum[2][2] = {};
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            fadd2(p[2 * e], p[2 * e + 1], z[4 * i + 2 * e], z[4 * i + 2 * e + 1], nm[e], nm[e]);
-            p[2 * e] = tg::exp2_approx(p[2 * e]);
-            p[2 * e + 1] = tg::exp2_approx(p[2 * e + 1]);
-          }
-          if constexpr (kQ) {
-            const float2 vs = *reinterpret_cast<const float2*>(&S.key[s][2][8 * i + cq]);
-            const float2 iv = *reinterpret_cast<const float2*>(&S.key[s][3][8 * i + cq]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              fmul2(p[2 * e], p[2 * e + 1], p[2 * e], p[2 * e + 1], vs.x, vs.y);
-              pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
-              ffma2(sum[e][0], sum[e][1], bf16_lo(pk[2 * i + e]), bf16_hi(pk[2 * i + e]), iv.x, iv.y,
-                    sum[e][0], sum[e][1]);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
-              fadd2(sum[e][0], sum[e][1], bf16_lo(pk[2 * i + e]), bf16_hi(pk[2 * i + e]), sum[e][0],
-                    sum[e][1]);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) tg::mbar_arrive(&S.b_empty[s]);   // this warp is done with the keys' data
-#pragma unroll
-        for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], alpha[e], sum[e][0] + sum[e][1]);
-        if (__any_sync(0xFFFFFFFFu, rescale)) {
-          // O must hold PV_{g-1} before it is scaled
-          alive = tg::mbar_wait(&S.o_done[(g - 1) % C::kS], ((g - 1) / C::kS) & 1, A.status, &S.abort_flag);
-          if (!all_alive(alive)) { alive = false; break; }
-          tg::tc_fence_after();
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h) {
-            uint32_t o[32];
-            const uint32_t at = tmem + lane_base + kColO + 64u * h;
-            tg::tmem_ld_16x256b_x8(at, o);
+        const bool draft = c.draft();
+        bool fresh = first;   // nothing of this item in O or P yet
+#pragma unroll 1
+        for (int hf = 0; 64 * hf < nv; ++hf) {
+          const float* key = S.key[s][0] + 64 * hf + cq;
+          float z[32];
+          {
+            uint32_t u[32];
+            tg::tmem_ld_16x256b_x8(sbuf + 64u * hf, u);
             tg::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
-            tg::tmem_st_16x256b_x8(at, o);
+            for (int i = 0; i < 8; ++i) {
+              const float2 sk = *reinterpret_cast<const float2*>(key + 8 * i);
+              float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                            __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
+              if constexpr (kQ) {
+                const float2 ks = *reinterpret_cast<const float2*>(key + kBN + 8 * i);
+                fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
+                fmul2(x[2], x[3], x[2], x[3], ks.x, ks.y);
+              }
+              float b0, b1;
+              fmul2(b0, b1, gh[0], gh[0], sk.x, sk.y);
+              ffma2(z[4 * i], z[4 * i + 1], x[0], x[1], ch[0], ch[0], b0, b1);
+              fmul2(b0, b1, gh[1], gh[1], sk.x, sk.y);
+              ffma2(z[4 * i + 2], z[4 * i + 3], x[2], x[3], ch[1], ch[1], b0, b1);
+            }
           }
+          if (draft || nv - 64 * hf < 64) {   // what is not there, or not seen
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t there = draft ? see[e] : (1ull << (nv - 64 * hf)) - 1;
+              const uint32_t w[2] = {static_cast<uint32_t>(there) >> cq,
+                                     static_cast<uint32_t>(there >> 32) >> cq};
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                  if (!((w[i >> 2] >> (8 * (i & 3) + f)) & 1)) z[4 * i + 2 * e + f] = -INFINITY;
+            }
+          }
+          // The reference of the weights is a whole number at or above the largest logit
+          // when it is set, so that moving it scales by an exact power of two; it moves
+          // only when a logit exceeds it by more than 2^8.
+          float alpha[2] = {1.f, 1.f}, nm[2];
+          bool rescale = false;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t0 = fmaxf(z[2 * e], z[2 * e + 1]), t1 = fmaxf(z[4 + 2 * e], z[5 + 2 * e]);
+#pragma unroll
+            for (int i = 2; i < 8; i += 2) {
+              t0 = fmax3(t0, z[4 * i + 2 * e], z[4 * i + 2 * e + 1]);
+              t1 = fmax3(t1, z[4 * i + 4 + 2 * e], z[4 * i + 5 + 2 * e]);
+            }
+            float mt = fmaxf(t0, t1);
+            mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 1));
+            mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2));
+            if (fresh) {
+              m[e] = ceilf(mt);
+            } else if (mt > m[e] + kRescaleThreshold) {
+              mt = ceilf(mt);
+              alpha[e] = tg::exp2_approx(m[e] - mt);
+              m[e] = mt;
+              rescale = true;
+            }
+            nm[e] = m[e] == -INFINITY ? 0.f : -m[e];   // a row that has seen nothing: weights 0
+          }
+          if (__any_sync(0xFFFFFFFFu, rescale)) {
+            if (!first) {   // O must hold PV_{g-1} before it is scaled
+              alive = wait(&S.o_done[(g - 1) % C::kS], ((g - 1) / C::kS) & 1, A.status, &S.abort_flag);
+              if (!all_alive(alive)) { alive = false; break; }
+              tg::tc_fence_after();
+#pragma unroll 1
+              for (int h = 0; h < C::kHalves; ++h) {
+                uint32_t o[32];
+                const uint32_t at = tmem + lane_base + kColO + 64u * h;
+                tg::tmem_ld_16x256b_x8(at, o);
+                tg::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
+                tg::tmem_st_16x256b_x8(at, o);
+              }
+            }
+            if (hf > 0) {   // and the unit's first weights
+              uint32_t w[16];
+              tg::tmem_st_wait();
+              tmem_ld_16x128b_x8(sbuf, w);
+              tg::tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                w[i] = tg::pack_bf16x2(bf16_lo(w[i]) * alpha[i & 1], bf16_hi(w[i]) * alpha[i & 1]);
+              tmem_st_16x128b_x8(sbuf, w);
+            }
+          }
+          uint32_t pk[16];
+          float sum[2][2] = {};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              fadd2(p[2 * e], p[2 * e + 1], z[4 * i + 2 * e], z[4 * i + 2 * e + 1], nm[e], nm[e]);
+              p[2 * e] = tg::exp2_approx(p[2 * e]);
+              p[2 * e + 1] = tg::exp2_approx(p[2 * e + 1]);
+            }
+            if constexpr (kQ) {
+              const float2 vs = *reinterpret_cast<const float2*>(key + 2 * kBN + 8 * i);
+              const float2 iv = *reinterpret_cast<const float2*>(key + 3 * kBN + 8 * i);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                fmul2(p[2 * e], p[2 * e + 1], p[2 * e], p[2 * e + 1], vs.x, vs.y);
+                pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
+                ffma2(sum[e][0], sum[e][1], bf16_lo(pk[2 * i + e]), bf16_hi(pk[2 * i + e]), iv.x, iv.y,
+                      sum[e][0], sum[e][1]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
+                fadd2(sum[e][0], sum[e][1], bf16_lo(pk[2 * i + e]), bf16_hi(pk[2 * i + e]), sum[e][0],
+                      sum[e][1]);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], alpha[e], sum[e][0] + sum[e][1]);
+          tmem_st_16x128b_x8(sbuf + 32u * hf, pk);   // P over S columns that are read
+          fresh = false;
         }
-        tg::tmem_st_16x128b_x16(sbuf, pk);   // P_g over S_g
+        if (!alive) break;
+        __syncwarp();
+        if (lane == 0) tg::mbar_arrive(&S.b_empty[s]);   // this warp is done with the keys' data
         tg::tmem_st_wait();
         tg::tc_fence_before();
         __syncwarp();
         if (lane == 0) tg::mbar_arrive(&S.p_full[g % C::kS]);
         first = c.run() == 1;   // the last unit of its item here: O is complete after PV_g
         if (first) {
-          const bool with_draft = c.draft();
+          const bool with_draft = draft;
           whole = whole && with_draft;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
             l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
           }
-          alive = tg::mbar_wait(&S.o_done[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag);
+          alive = wait(&S.o_done[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag);
           if (!all_alive(alive)) { alive = false; break; }
           tg::tc_fence_after();
           uint64_t bad = 0;
           if (with_draft) bad = *reinterpret_cast<const uint64_t*>(S.bad[n_draft % kBadRing]);
           const int slot = 2 * blockIdx.x + (seg > 0);
+          // where this thread's elements go: row r2[e], columns cq and cq + 1 of each 8
+          int64_t at[2];
+          float inv[2];
 #pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int t = c.mt * A.tm + r2[e] / A.group;
+            at[e] = whole ? (static_cast<int64_t>(c.b) * A.n_draft + t) * A.n_hq + c.kvh * A.group + r2[e] % A.group
+                          : static_cast<int64_t>(slot) * rows + r2[e];
+            if (r2[e] >= rows || t >= c.dl ||
+                (whole && !tg::in_bounds(at[e], static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)))
+              at[e] = -1;
+            inv[e] = l[e] == 0.f ? 0.f : 1.f / l[e];   // nothing seen: zeros
+          }
+#pragma unroll 1
           for (int h = 0; h < C::kHalves; ++h) {
             uint32_t o[32];
             tg::tmem_ld_16x256b_x8(tmem + lane_base + kColO + 64u * h, o);
             tg::tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int t = c.mt * A.tm + r2[e] / A.group, gq = r2[e] % A.group;
-              if (r2[e] >= rows || t >= c.dl) continue;
-              for (uint64_t left = bad & see[e]; left; left &= left - 1) {
-                // a visible drafted row with infinities or NaN: they join O here
-                const int r = __ffsll(static_cast<long long>(left)) - 1;
-                const __nv_bfloat16* v =
-                    A.vd + ((static_cast<int64_t>(c.b) * A.n_draft + r) * A.n_hkv + c.kvh) * DH + 64 * h + cq;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float x = __bfloat162float(v[8 * (i >> 1) + (i & 1)]);
-                  uint32_t& y = o[4 * (i >> 1) + 2 * e + (i & 1)];
-                  if (!isfinite(x)) y = __float_as_uint(__uint_as_float(y) + x);
-                }
-              }
+              if (at[e] < 0) continue;
               if (whole) {
-                const int64_t row = (static_cast<int64_t>(c.b) * A.n_draft + t) * A.n_hq + c.kvh * A.group + gq;
-                if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)) continue;
-                const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];   // nothing seen: zeros
+                __nv_bfloat16* p = A.out + at[e] * DH + 64 * h + cq;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint32_t*>(A.out + row * DH + 64 * h + 8 * i + cq) =
-                      tg::pack_bf16x2(__uint_as_float(o[4 * i + 2 * e]) * inv,
-                                      __uint_as_float(o[4 * i + 2 * e + 1]) * inv);
+                  *reinterpret_cast<uint32_t*>(p + 8 * i) =
+                      tg::pack_bf16x2(__uint_as_float(o[4 * i + 2 * e]) * inv[e],
+                                      __uint_as_float(o[4 * i + 2 * e + 1]) * inv[e]);
               } else {
-                float* pr = A.part + (static_cast<int64_t>(slot) * rows + r2[e]) * DH + 64 * h + cq;
+                float* p = A.part + at[e] * DH + 64 * h + cq;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint2*>(pr + 8 * i) = make_uint2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
-                if (h == 0 && (lane & 3) == 0) {
-                  float* ml = A.part + static_cast<int64_t>(2 * A.n_cta) * rows * DH +
-                              (static_cast<int64_t>(slot) * rows + r2[e]) * 2;
-                  *reinterpret_cast<float2*>(ml) = make_float2(m[e], l[e]);
-                }
+                  *reinterpret_cast<uint2*>(p + 8 * i) = make_uint2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
               }
             }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (at[e] < 0) continue;
+            if (!whole && (lane & 3) == 0)
+              *reinterpret_cast<float2*>(A.part + static_cast<int64_t>(2 * A.n_cta) * rows * DH + at[e] * 2) =
+                  make_float2(m[e], l[e]);
+            if (bad & see[e])
+              add_infinite<DH>(A, c.b, c.kvh, bad & see[e], whole ? A.out + at[e] * DH + cq : nullptr,
+                               whole ? nullptr : A.part + at[e] * DH + cq, cq);
           }
           tg::tc_fence_before();
           __syncwarp();
@@ -819,49 +898,62 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       }
     }
   } else if (kQ && warp >= 4 + kSoftmaxWarps) {
-    // ---------------- codes to operand tiles, 32 rows a warp ----------------
+    // ---------------- codes to operand tiles, 16 rows a warp ----------------
     constexpr bool kE4m3 = kType == TG_E4M3;
     const int cw = warp - 4 - kSoftmaxWarps;
-    Cursor cv = c;
+    // Eight lanes take one 16-code column of eight rows, so that reads of the swizzled raw
+    // tile and stores to the swizzled operand tile both fall into different banks.
+    constexpr int kC16 = DH / 16;                          // 16-code columns of a row
+    constexpr int kRows = kBN / kConvWarps;                // rows of a warp
+    constexpr int kPasses = kRows * kC16 / 32;
+    const int rl = lane & 7, cl = lane >> 3;               // row of eight, column of four
+    Tile cur = {}, prev = {};
     int r = 0, gk = 0, gv = 0, n_draft = 0;
-    auto convert = [&](const Cursor& t, bool val) -> bool {
-      int& g = val ? gv : gk;
+#pragma unroll 1
+    for (int i = 0; i < 2 * n; ++i) {
+      const bool val = value_turn(i, n);
+      if (!val) {
+        prev = cur;
+        cur = tile_of(c);
+        c.advance(A, S);
+      }
+      const Tile t = val && i < 2 * n - 1 ? prev : cur;
+      const int g = val ? gv++ : gk++;
       const int n_st = val ? C::kV : C::kK, s = g % n_st;
-      uint64_t* full = val ? &S.v_full[s % C::kV] : &S.k_full[s % C::kK];
-      uint64_t* empty = val ? &S.v_empty[s % C::kV] : &S.k_empty[s % C::kK];
-      uint8_t* dst = val ? S.v[s % C::kV][0] : S.k[s % C::kK][0];
-      if (g >= n_st && !all_alive(tg::mbar_wait(empty, ((g / n_st) - 1) & 1, A.status, &S.abort_flag)))
-        return false;
-      if (t.draft()) {
-        if (val) draft_values<DH>(A, t, dst, S.bad[n_draft++ % kBadRing], 16 * cw, 16 * cw + 16, lane);
-        else draft_keys<DH>(A, t, dst, 16 * cw, 16 * cw + 16, lane);
+      uint64_t* full = val ? &S.v_full[s] : &S.k_full[s];
+      uint64_t* empty = val ? &S.v_empty[s] : &S.k_empty[s];
+      uint8_t* dst = val ? S.v[0][0] : S.k[0][0];
+      dst += s * kTileBytes;
+      if (g >= n_st && !all_alive(wait(empty, ((g / n_st) - 1) & 1, A.status, &S.abort_flag))) break;
+      if (t.draft) {
+        if (cw < kMaxDraft / 16) {   // 16 rows each
+          if (val) draft_values<DH>(A, t.b, t.kvh, t.nv, dst, S.bad[n_draft % kBadRing], 16 * cw, 16 * cw + 16, lane);
+          else draft_keys<DH>(A, t.b, t.kvh, t.nv, dst, 16 * cw, 16 * cw + 16, lane);
+        }
+        if (val) ++n_draft;
       } else {
         const int rs = r % C::kRaw;
-        if (!all_alive(tg::mbar_wait(&S.raw_full[rs], (r / C::kRaw) & 1, A.status, &S.abort_flag)))
-          return false;
-        constexpr int kC16 = DH / 16;        // 16-code columns of a row
-        constexpr int kRpp = 32 / kC16;      // rows a pass
-        const int c16 = lane % kC16, nv = t.keys();
-        const int r1 = (nv + 15) & ~15;      // rows behind are not multiplied
-#pragma unroll 4
-        for (int rr = 32 * cw + lane / kC16; rr < 32 * cw + 32; rr += kRpp) {
-          uint4 x = *reinterpret_cast<const uint4*>(S.raw[rs] + rr * DH + 16 * c16);
-          if (val && rr >= nv) x = make_uint4(0, 0, 0, 0);
-          if (rr >= r1) continue;
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        if (!all_alive(wait(&S.raw_full[rs], (r / C::kRaw) & 1, A.status, &S.abort_flag))) break;
+        const uint8_t* src = S.raw[0] + rs * C::kRawBytes;
+        uint4 x[kPasses];
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+          const int rr = kRows * cw + 8 * (p / (kC16 / 4)) + rl, cc = cl + 4 * (p % (kC16 / 4));
+          x[p] = *reinterpret_cast<const uint4*>(src + rr * DH + ((DH == 128 ? cc ^ rl : cc ^ ((rl >> 1) & 3)) << 4));
+        }
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+          const int rr = kRows * cw + 8 * (p / (kC16 / 4)) + rl, cc = cl + 4 * (p % (kC16 / 4));
+          if (val && rr >= t.nv) x[p] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
+          const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
           uint32_t y[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[2 * i] = widen2<kE4m3>(w[i], kE4m3 ? 0x1404 : 0x4140);
-            y[2 * i + 1] = widen2<kE4m3>(w[i], kE4m3 ? 0x3424 : 0x4342);
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] = widen2<kE4m3>(w[e], kE4m3 ? 0x1404 : 0x4140);
+            y[2 * e + 1] = widen2<kE4m3>(w[e], kE4m3 ? 0x3424 : 0x4342);
           }
-          // lanes of the two column halves store their two 16-byte pieces in opposite
-          // order, so that a quarter warp's stores fall into different banks
-          const int sw = (c16 >> 2) & 1;
-          *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * c16 + sw)) =
-              sw ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * c16 + 1 - sw)) =
-              sw ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]);
+          *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
         }
         __syncwarp();
         if (lane == 0) tg::mbar_arrive(&S.raw_empty[rs]);
@@ -870,17 +962,6 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       tg::fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) tg::mbar_arrive(full);
-      ++g;
-      return true;
-    };
-    bool alive = convert(c, false);
-    for (int g = 0; g < n && alive; ++g) {
-      if (g + 1 < n) {
-        c.advance(A, S);
-        alive = convert(c, false);
-      }
-      if (alive) alive = convert(cv, true);
-      cv.advance(A, S);
     }
   }
   tg::tc_fence_before();
@@ -931,7 +1012,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     if (cb + lane <= c1) v = *reinterpret_cast<const float2*>(ml + (slot(cb + lane) * rows + row) * 2);
     const float wt = tg::exp2_approx(v.x - base);
     const int ns = min(32, c1 - cb + 1);
-#pragma unroll 8
+#pragma unroll 4
     for (int i = 0; i < ns; ++i) {
       const float wi = __shfl_sync(0xFFFFFFFFu, wt, i);
       L = fmaf(wi, __shfl_sync(0xFFFFFFFFu, v.y, i), L);
@@ -979,7 +1060,7 @@ tg_status launch_tree(const TreeArgs& a, const void* q, cudaStream_t st) {
   const uint64_t str[2] = {static_cast<uint64_t>(DH) * es, static_cast<uint64_t>(a.n_hkv) * DH * es};
   const uint32_t box[3] = {kQ ? DH : 64, 1, kBN};
   const auto type = kQ ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const auto swz = kQ ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+  const auto swz = kQ && DH == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   if (!tg::encode_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qdims, qstr, qbox,
                        CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tg::encode_tmap(&tk, type, 3, a.kc, dims, str, box, swz) ||
