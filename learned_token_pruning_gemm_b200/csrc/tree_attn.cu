@@ -44,79 +44,26 @@
 // are noted, and the epilogue adds them to the rows that see them.
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "tree.cuh"
 
 namespace {
+
+using tg::TreeArgs;
+using tg::bf16_hi;
+using tg::bf16_lo;
+using tg::kLog2e;
+using tg::wait;
 
 constexpr int kBM = 128;           // rows of a row tile
 constexpr int kBN = 128;           // keys of a unit
 constexpr int kMaxDraft = 64;
-constexpr int kMaxBatch = 1024;
 constexpr int kKeyStages = 4;
 constexpr int kBadRing = 8;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kConvWarps = 8;
 constexpr int kMaxCtas = 148;      // one per SM
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr uint32_t kHalfBytes = kBN * 128;  // 64 columns of 128 rows, bf16, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512, kColO = 384;
-
-struct TreeArgs {
-  const __nv_bfloat16 *kd, *vd;
-  const float* sd;
-  const int64_t* mask;
-  const int32_t* draft_len;
-  const uint8_t *kc, *vc;
-  const float *ks, *vs, *sc;
-  const int32_t* cache_len;
-  const float *gain, *tau;
-  __nv_bfloat16* out;
-  int64_t* base;      // [batch + 1] first unit of each sequence (written by CTA 0)
-  float* part;        // partials: [slots][hw * kw][rows][dh], then [slots][hw * kw][rows][2] (max, sum)
-  int64_t slots;
-  int batch, n_draft, cap, max_len, n_hq, n_hkv, group;
-  int tm;             // tokens of a row tile
-  int unit;           // keys of a unit
-  int few;            // tree_rows_kernel: units of the cache only
-  int hw, kw;         // KV heads of an item, and warps that share a head's keys of a unit
-  int n_cta;
-  int* status;
-};
-
-// A sequence's lengths, or no drafted tokens where they are out of range.
-__device__ __forceinline__ int2 seq_lens(const TreeArgs& A, int b, bool record) {
-  const int len = A.cache_len[b], dl = A.draft_len ? A.draft_len[b] : A.n_draft;
-  if (len < 0 || len > A.cap || len > A.max_len || dl < 0 || dl > A.n_draft) {
-    if (record) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
-    return make_int2(0, 0);
-  }
-  return make_int2(len, dl);
-}
-__device__ __forceinline__ int row_tiles(const TreeArgs& A, int dl) { return (dl + A.tm - 1) / A.tm; }
-__device__ __forceinline__ int key_units(const TreeArgs& A, int keys) { return (keys + A.unit - 1) / A.unit; }
-// units of an item: those of the cache, then those of the drafted rows
-__device__ __forceinline__ int item_units(const TreeArgs& A, int len, int dl) {
-  return key_units(A, len) + (A.few ? 0 : key_units(A, dl));
-}
-__device__ __forceinline__ int head_groups(const TreeArgs& A) { return (A.n_hkv + A.hw - 1) / A.hw; }
-// Where the maxima and sums of the partials begin.
-__device__ __forceinline__ float* part_ml(const TreeArgs& A, int rows, int dh) {
-  return A.part + A.slots * A.hw * A.kw * rows * dh;
-}
-
-// CTAs that share W units: no share is empty, so every CTA between an item's first and
-// last holds a part of it. CTA c has the units [W c / G, W (c + 1) / G).
-__device__ __forceinline__ int64_t share_ctas(const TreeArgs& A, int64_t W) {
-  return W < A.n_cta ? W : A.n_cta;
-}
-
-// a * b / c with c > 0, b < 2^16: in 32 bits where they hold the product
-__device__ __forceinline__ int64_t mul_div(int64_t a, int b, int64_t c) {
-  if (a < (1 << 16) && c <= 0xFFFFFFFFll)
-    return static_cast<uint32_t>(a) * static_cast<uint32_t>(b) / static_cast<uint32_t>(c);
-  return a * b / c;
-}
 
 template <int DH, bool kQ>
 struct Cfg {
@@ -139,9 +86,9 @@ struct TreeSmem {
   uint8_t raw[C::kRaw][C::kRawBytes];
   float key[kKeyStages][kQ ? 4 : 1][kBN];   // score, then (codes) key scale, value scale and its inverse
   uint16_t bad[kBadRing][4];                // drafted rows with values that are not finite, 16 rows a word
-  int64_t base[kMaxBatch + 1];
-  int len[kMaxBatch];
-  uint8_t dl[kMaxBatch];
+  int base[tg::kTreeMaxBatch + 1];
+  int len[tg::kTreeMaxBatch];
+  uint8_t dl[tg::kTreeMaxBatch];
   uint64_t q_full, q_empty;
   uint64_t k_full[C::kK], k_empty[C::kK];
   uint64_t v_full[C::kV], v_empty[C::kV];
@@ -153,14 +100,6 @@ struct TreeSmem {
   int abort_flag;
 };
 
-// The slow side of a wait is one function: with it inlined at every site the roles'
-// loops no longer fit the instruction cache together.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
-  return tg::mbar_wait(bar, parity, status, abort);
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
-  return tg::mbar_try_wait(tg::smem_u32(bar), parity) || wait_slow(bar, parity, status, abort);
-}
 __device__ __forceinline__ bool all_alive(bool a) { return __all_sync(0xFFFFFFFFu, a); }
 
 // The order in which the tiles of a quantised cache pass, K one unit ahead of V:
@@ -169,74 +108,31 @@ __device__ __forceinline__ bool value_turn(int i, int n) {
   return i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
 }
 
-// Every sequence's lengths and first unit into shared memory (CTA 0: the units also to the
-// workspace, for the second kernel); all threads of the block, with barriers. Returns the
-// number of units.
-template <int kThreads, class Smem>
-__device__ __forceinline__ int64_t count_units(const TreeArgs& A, Smem& S) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  for (int b = tid; b < A.batch; b += kThreads) {
-    const int2 l = seq_lens(A, b, blockIdx.x == 0);
-    S.len[b] = l.x;
-    S.dl[b] = static_cast<uint8_t>(l.y);
-    S.base[b + 1] = static_cast<int64_t>(head_groups(A)) * row_tiles(A, l.y) * item_units(A, l.x, l.y);
-  }
-  __syncthreads();
-  if (tid < 32) {
-    int64_t carry = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < A.batch; b0 += 32) {
-      int64_t x = b0 + lane < A.batch ? S.base[b0 + lane + 1] : 0;
-#pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b0 + lane < A.batch) S.base[b0 + lane + 1] = carry + x;
-      carry += __shfl_sync(0xFFFFFFFFu, x, 31);
-    }
-    if (lane == 0) S.base[0] = 0;
-  }
-  __syncthreads();
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= A.batch; b += kThreads) A.base[b] = S.base[b];
-  return S.base[A.batch];
-}
-
-// Walks a CTA's units in order: the unit's sequence, first KV head, row tile and place
-// among its item's units, those of the cache before those of the drafted rows.
+// Walks a CTA's units in order: the unit's sequence, KV head, row tile and place among its
+// item's units, those of the cache before the one of the drafted rows.
 struct Cursor {
-  int64_t u, u1;
-  int b, item, n_items, kvh, mt, j, nk, nt, len, dl, unit;
+  int u, u1, b, item, n_items, kvh, mt, j, nk, nt, len, dl;
   template <class S>
   __device__ __forceinline__ void load_seq(const TreeArgs& A, const S& s) {
     len = s.len[b];
     dl = s.dl[b];
-    nk = key_units(A, len);
-    nt = item_units(A, len, dl);
-    n_items = head_groups(A) * row_tiles(A, dl);
+    nk = (len + kBN - 1) / kBN;
+    nt = nk + 1;
+    n_items = A.n_hkv * tg::row_tiles(A, dl);
   }
   __device__ __forceinline__ void split_item(const TreeArgs& A) {
-    const int amt = row_tiles(A, dl), group = item / amt;
-    kvh = group * A.hw;
-    mt = item - group * amt;
+    const int amt = tg::row_tiles(A, dl);
+    kvh = item / amt;
+    mt = item - kvh * amt;
   }
   template <class S>
-  __device__ __forceinline__ void start(const TreeArgs& A, const S& s, int64_t first, int64_t last) {
+  __device__ __forceinline__ void start(const TreeArgs& A, const S& s, int first, int n) {
     u = first;
-    u1 = last;
-    unit = A.unit;
-    int lo = 0, hi = A.batch - 1;   // the last b with base[b] <= u
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s.base[mid] <= u) lo = mid;
-      else hi = mid - 1;
-    }
-    b = lo;
+    u1 = first + n;
+    b = tg::sequence_of(A, s, u);
     load_seq(A, s);
-    const int64_t rem = u - s.base[b];
-    item = static_cast<int>(rem >> 31 ? rem / nt : static_cast<uint32_t>(rem) / static_cast<uint32_t>(nt));
-    j = static_cast<int>(rem - static_cast<int64_t>(item) * nt);
+    item = (u - s.base[b]) / nt;
+    j = u - s.base[b] - item * nt;
     split_item(A);
   }
   template <class S>
@@ -252,14 +148,10 @@ struct Cursor {
     }
     split_item(A);
   }
-  __device__ __forceinline__ bool draft() const { return j >= nk; }
-  __device__ __forceinline__ int key0() const { return (draft() ? j - nk : j) * unit; }
-  __device__ __forceinline__ int keys() const { return min(unit, (draft() ? dl : len) - key0()); }
+  __device__ __forceinline__ bool draft() const { return j == nk; }
+  __device__ __forceinline__ int keys() const { return draft() ? dl : min(kBN, len - j * kBN); }
   // units of the current item from here on within the CTA's share
-  __device__ __forceinline__ int run() const {
-    const int64_t left = u1 - u;
-    return nt - j < left ? nt - j : static_cast<int>(left);
-  }
+  __device__ __forceinline__ int run() const { return min(nt - j, u1 - u); }
 };
 
 // What the copy of one unit needs to know of it.
@@ -327,9 +219,6 @@ __device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-
 // Two codes (bytes of a and b, as __byte_perm selects them into the low bytes of the two
 // halves for int8 and into the high ones for e4m3) to two bf16 values, exactly.
 // int8: with the low seven bits as mantissa over 128, (128 + low) - (128 or 256 by the
@@ -474,19 +363,16 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
   tg::pdl_launch_dependents();
   tg::pdl_wait();   // global memory only from here on
   tg::tc_fence_before();
-  const int64_t W = count_units<C::kThreads>(A, S);
+  const tg::Shares share(A, tg::count_units<C::kThreads>(A, S));
   tg::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-  const int64_t G = share_ctas(A, W);
-  const int cta = blockIdx.x;
-  const int64_t u0 = cta < G ? mul_div(W, cta, G) : 0, u1 = cta < G ? mul_div(W, cta + 1, G) : 0;
-  const int n = static_cast<int>(u1 - u0);
+  const int n = share.size(blockIdx.x);
   if (n == 0) {   // uniform: nothing to do here
     if (warp == 2) tg::tmem_dealloc(tmem, kTmemCols);
     return;
   }
   Cursor c;
-  c.start(A, S, u0, u1);
+  c.start(A, S, share.first(blockIdx.x), n);
 
   if (!kQ && (warp == 0 || warp == 3)) {
     // ---------------- K (warp 0) or V (warp 3) tiles of a bf16 cache ----------------
@@ -707,10 +593,10 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         if (first) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int hq = c.kvh * A.group + r2[e] % A.group;
+            const int tok = tg::token_of(A, r2[e]), hq = c.kvh * A.group + r2[e] - tok * A.group;
             ch[e] = kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]);
             gh[e] = A.gain[hq] * kLog2e;
-            const int t = c.mt * A.tm + r2[e] / A.group;   // tokens behind the last see nothing
+            const int t = c.mt * A.tm + tok;   // tokens behind the last see nothing
             see[e] = t < c.dl
                          ? static_cast<uint64_t>(A.mask[static_cast<int64_t>(c.b) * A.n_draft + t]) : 0;
             if (c.dl < 64) see[e] &= (1ull << c.dl) - 1;
@@ -785,7 +671,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
             mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2));
             if (fresh) {
               m[e] = ceilf(mt);
-            } else if (mt > m[e] + kRescaleThreshold) {
+            } else if (mt > m[e] + tg::kRescaleThreshold) {
               mt = ceilf(mt);
               alpha[e] = tg::exp2_approx(m[e] - mt);
               m[e] = mt;
@@ -883,8 +769,8 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           float inv[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int t = c.mt * A.tm + r2[e] / A.group;
-            at[e] = whole ? (static_cast<int64_t>(c.b) * A.n_draft + t) * A.n_hq + c.kvh * A.group + r2[e] % A.group
+            const int tok = tg::token_of(A, r2[e]), t = c.mt * A.tm + tok;
+            at[e] = whole ? (static_cast<int64_t>(c.b) * A.n_draft + t) * A.n_hq + c.kvh * A.group + r2[e] - tok * A.group
                           : static_cast<int64_t>(slot) * rows + r2[e];
             if (r2[e] >= rows || t >= c.dl ||
                 (whole && !tg::in_bounds(at[e], static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)))
@@ -918,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             if (at[e] < 0) continue;
             if (!whole && (lane & 3) == 0)
-              *reinterpret_cast<float2*>(part_ml(A, rows, DH) + at[e] * 2) =
+              *reinterpret_cast<float2*>(tg::part_ml(A, rows, DH) + at[e] * 2) =
                   make_float2(m[e], l[e]);
             if (bad & see[e])
               add_infinite<DH>(A, c.b, c.kvh, bad & see[e], whole ? A.out + at[e] * DH + cq : nullptr,
@@ -1008,432 +894,6 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
   }
 }
 
-// ---- few rows: products of 16 rows in registers ----
-//
-// Up to 32 rows (drafted tokens x group) of head dim 128 there is little to multiply per
-// byte of cache, and the tensor-core tiles above, 128 rows high, spend their time in the
-// hand-over between roles. Here eight warps run the same code instead, straight from the
-// TMA ring into the register fragments of m16n8k16 products (codes are widened in
-// registers), each with its own running maximum, sum and O, so nothing joins them but the
-// ring. A unit is 16 keys a warp: the warps share hw KV heads of the same cache rows (all
-// of them up to eight, so that a tile is one contiguous piece of the cache) and, where
-// there are fewer, split the keys in kw parts; every part leaves its own partial. The
-// drafted rows, 32 at most, are left to the second kernel. A unit's code is run from the
-// instruction cache by all warps; what is run once an item is kept small.
-// Codes are widened to fp16, which they fit exactly at half the instructions that bf16
-// takes, so the queries are too, after a row's largest value is brought near 2^8.
-// Any dimension may take any place of a product's inner index or of its columns, as long
-// as both operands agree, so every thread reads 16 contiguous bytes:
-//   S = Q K^T: thread (g = lane / 4, i = lane % 4) reads dims 32i .. 32i+31 of key g (codes;
-//              for bf16 the 8-dim columns 2i and 2i+1 of both 64-dim halves);
-//   O = P V:   column n of product t is dim 16n + t (codes; bf16: 64 (t/8) + 8n + t%8), so
-//              thread g reads 16 contiguous dims of its four keys.
-constexpr int kRowWarps = 8;
-constexpr int kRowThreads = 32 * kRowWarps;
-constexpr int kRowMax = 32;        // rows of this kernel, at most
-
-template <bool kQ, int MT>
-struct RowCfg {
-  static constexpr int kHalf = 16 * kRowWarps * 128;        // 128-byte rows of one tile (half)
-  static constexpr int kTile = kHalf * (kQ ? 1 : 2);        // bytes of a K or V tile, at most
-  static constexpr int kRing = kQ ? 9 : MT == 1 ? 5 : 4;    // tiles of the ring: K, V, K, V, ..
-};
-
-template <bool kQ, int MT>
-struct RowSmem {
-  uint8_t tile[RowCfg<kQ, MT>::kRing][RowCfg<kQ, MT>::kTile];
-  uint4 q[kRowWarps][MT][8][32];               // A fragments of each warp's queries
-  float2 cg[kRowWarps][16 * MT];               // each row's logit factor and gain, log2 domain
-  int64_t base[kMaxBatch + 1];
-  int len[kMaxBatch];
-  uint8_t dl[kMaxBatch];
-  uint64_t full[RowCfg<kQ, MT>::kRing], empty[RowCfg<kQ, MT>::kRing];
-  Cursor next;                                 // the unit that is loaded next, and
-  int issued;                                  // the tiles that are on their way or here
-  int abort_flag;
-};
-
-// Loads tiles as far as the ring reaches (K at even places, V at odd ones): tile t needs tile t - kRing to be consumed by
-// every warp, which is waited for, and all before `consumed` are by this one. One thread.
-template <bool kQ, int MT>
-__device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<kQ, MT>& S, const CUtensorMap* tm_k,
-                                       const CUtensorMap* tm_v, int consumed) {
-  using C = RowCfg<kQ, MT>;
-  int t = S.issued;
-  Cursor c = S.next;
-  while (t < consumed + C::kRing && c.u < c.u1) {
-    const int s = t % C::kRing;
-    if (t >= C::kRing && !wait(&S.empty[s], ((t / C::kRing) - 1) & 1, A.status, &S.abort_flag)) break;
-    const uint32_t half = A.hw * A.unit * 128;   // rows of one head after the other
-    tg::mbar_arrive_expect_tx(&S.full[s], kQ ? half : 2 * half);
-    const CUtensorMap* map = t & 1 ? tm_v : tm_k;
-    const int row = static_cast<int>(static_cast<int64_t>(c.b) * A.cap + c.key0());
-    tg::tma_load_3d(S.tile[s], map, &S.full[s], 0, row, c.kvh);
-    if constexpr (!kQ) tg::tma_load_3d(S.tile[s] + C::kHalf, map, &S.full[s], 64, row, c.kvh);
-    if (t & 1) c.advance(A, S);
-    ++t;
-  }
-  S.issued = t;
-  S.next = c;
-}
-
-// One 16 x 8 x 16 product, bf16 (kF16: fp16) operands, fp32 sums.
-template <bool kF16>
-__device__ __forceinline__ void mma_16816(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
-  if constexpr (kF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
-// Four codes (bytes of w; int8 ones with the sign bit flipped) to four fp16 values, exactly.
-template <bool kE4m3>
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (kE4m3) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  } else {   // 1024 + (code + 128) has the code's bits as its last eight; then less 1152
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
-  }
-}
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// bf16 rows in an fp16 product: a row is multiplied by the power of two that brings its
-// largest value (exponent field e, m the magnitude's bits) to [2^8, 2^9), so that values
-// down to 2^-22 of it stay exact, and the inverse goes where the row's scale goes.
-struct RowScale {
-  float down, up;
-};
-__device__ __forceinline__ RowScale row_scale(uint32_t m) {
-  const int e = max(static_cast<int>(m >> 7), 9);
-  return RowScale{__int_as_float((262 - e) << 23), __int_as_float((e - 8) << 23)};
-}
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float scale) {
-  return pack_f16x2(bf16_lo(w) * scale, bf16_hi(w) * scale);
-}
-
-template <int kType, int MT>
-__global__ void __launch_bounds__(kRowThreads, 1)
-    tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __nv_bfloat16* __restrict__ q, const __grid_constant__ TreeArgs A) {
-  constexpr bool kQ = kType != TG_BF16;
-  constexpr bool kE4m3 = kType == TG_E4M3;
-  using C = RowCfg<kQ, MT>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t pad = (1024u - (tg::smem_u32(smem_raw) & 1023u)) & 1023u;
-  RowSmem<kQ, MT>& S = *reinterpret_cast<RowSmem<kQ, MT>*>(smem_raw + pad);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, i4 = lane & 3;
-  if (tid == 0) {
-    for (int s = 0; s < C::kRing; ++s) {
-      tg::mbar_init(&S.full[s], 1);
-      tg::mbar_init(&S.empty[s], kRowWarps);
-    }
-    S.abort_flag = 0;
-    tg::fence_barrier_init();
-    tg::tma_prefetch_desc(&tm_k);
-    tg::tma_prefetch_desc(&tm_v);
-  }
-  tg::pdl_launch_dependents();
-  tg::pdl_wait();   // global memory only from here on
-  const int64_t W = count_units<kRowThreads>(A, S);
-  const int64_t G = share_ctas(A, W);
-  const int cta = blockIdx.x;
-  const int64_t u0 = cta < G ? mul_div(W, cta, G) : 0, u1 = cta < G ? mul_div(W, cta + 1, G) : 0;
-  const int n = static_cast<int>(u1 - u0);
-  if (n == 0) return;   // uniform: nothing to do here
-  Cursor c;
-  c.start(A, S, u0, u1);
-
-  const bool loader = tid == kRowThreads - 1;   // the last warp's last thread
-  if (loader) {
-    S.issued = 0;
-    S.next = c;
-    row_loads<kQ, MT>(A, S, &tm_k, &tm_v, 0);
-  }
-  __syncwarp();
-
-  // ---------------- the warps: 16 keys of a head of every unit each ----------------
-  // A wait that runs out records itself and sets the abort flag, after which every wait
-  // returns at once: the loops below take the same steps either way.
-  const int rows = A.group * A.tm;
-  const int hd = warp / A.kw, k0 = 16 * (warp - hd * A.kw);   // head of the item, first key of the unit
-  const int off = 2 * i4;                                     // this thread's keys: off + {0, 1} + {0, 8}
-  float o[MT][16][4], m[MT][2], l[MT][2];
-  bool first = true;
-  int r = 0;
-#pragma unroll 1
-  for (int u = 0; u < n; ++u) {
-    const int kvh = c.kvh + hd;
-    const bool head = hd < A.hw && kvh < A.n_hkv;             // else this warp only keeps the ring going
-    if (first && head) {   // a new item
-#pragma unroll 1
-      for (int rr = 0; rr < 2 * MT; ++rr) {   // this thread's rows: its part of their fragments
-        const int row = g + 8 * rr, tok = row / A.group, hq = kvh * A.group + row - tok * A.group;
-        const int64_t bt = static_cast<int64_t>(c.b) * A.n_draft + (tok < c.dl ? tok : 0);   // rows behind the last: any
-        const __nv_bfloat16* p = q + (bt * A.n_hq + hq) * 128;
-        uint2 x[8];
-        uint32_t mx = 0;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {   // dims as the keys' below
-          x[t] = *reinterpret_cast<const uint2*>(
-              p + (kQ ? 32 * i4 + 4 * t : 64 * (t >> 2) + 16 * i4 + 8 * ((t >> 1) & 1) + 4 * (t & 1)));
-          if (kQ) mx = max_u16x2(mx, max_u16x2(x[t].x & 0x7FFF7FFFu, x[t].y & 0x7FFF7FFFu));
-        }
-        float factor = kLog2e / (sqrtf(128.f) * A.tau[hq]);
-        // product t, register e + 2 h: row half e = rr % 2, dims half h; read by this thread only
-        uint32_t* f = reinterpret_cast<uint32_t*>(&S.q[warp][rr >> 1][0][lane]) + (rr & 1);
-        if constexpr (kQ) {
-          mx = max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-          mx = max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-          const RowScale rs = row_scale(max(mx >> 16, mx & 0xFFFFu));
-          factor *= rs.up;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            f[128 * t] = bf16x2_to_f16x2(x[t].x, rs.down);
-            f[128 * t + 2] = bf16x2_to_f16x2(x[t].y, rs.down);
-          }
-        } else {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            f[128 * t] = x[t].x;
-            f[128 * t + 2] = x[t].y;
-          }
-        }
-        if (i4 == 0) S.cg[warp][row] = make_float2(factor, A.gain[hq] * kLog2e);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          m[mt][e] = -INFINITY;
-          l[mt][e] = 0.f;
-        }
-#pragma unroll
-        for (int t = 0; t < 16; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][t][e] = 0.f;
-      }
-    }
-    const int nv = c.keys();
-    const bool any = head && k0 < nv;
-    // what the keys bring besides K and V; keys behind the last one read its place and are
-    // masked below
-    float sk[4], ks[4], vs[4];
-    if (any) {
-      const int64_t row0 = static_cast<int64_t>(c.b) * A.cap + c.key0();
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int64_t row = row0 + min(k0 + off + 8 * (x >> 1) + (x & 1), nv - 1);
-        if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
-        sk[x] = A.sc[row];
-        if constexpr (kQ) {
-          ks[x] = A.ks[row * A.n_hkv + kvh];
-          vs[x] = A.vs[row * A.n_hkv + kvh];
-        }
-      }
-    }
-    // ---- S = Q K^T ----
-    float z[MT][2][4];
-    const int s = r % C::kRing, sv = (r + 1) % C::kRing;
-    wait(&S.full[s], (r / C::kRing) & 1, A.status, &S.abort_flag);
-    __syncwarp();
-    if (any) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        // a head's rows of the tile follow each other; the place among eight is g
-        const uint8_t* p = S.tile[s] + (hd * A.unit + k0 + 8 * j + g) * 128;
-        uint32_t kb[16];   // 32 dims of key k0 + 8 j + g, two a register
-#pragma unroll
-        for (int i = 0; i < (kQ ? 2 : 4); ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(p + (kQ ? 0 : (i >> 1) * C::kHalf) +
-                                                          (((2 * i4 + (i & 1)) ^ g) << 4));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (kQ) widen4<kE4m3>(word_of(x, e) ^ (kE4m3 ? 0u : 0x80808080u), kb[8 * i + 2 * e], kb[8 * i + 2 * e + 1]);
-            else kb[4 * i + e] = word_of(x, e);
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[mt][j][e] = 0.f;
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            mma_16816<kQ>(z[mt][j], S.q[warp][mt][t][lane], kb[2 * t], kb[2 * t + 1]);
-      }
-    }
-    __syncwarp();
-    if (lane == 0) tg::mbar_arrive(&S.empty[s]);
-    // the ring goes on where every warp is through with the unit before
-    if (loader) row_loads<kQ, MT>(A, S, &tm_k, &tm_v, r);
-    __syncwarp();
-    wait(&S.full[sv], ((r + 1) / C::kRing) & 1, A.status, &S.abort_flag);
-    __syncwarp();
-    if (any) {
-      // ---- weights ----
-      // Codes: the value scale v joins the logit, z + log2 v, so that the fp16 weights
-      // 2^(z + log2 v - m) are what the codes are multiplied by and m follows their largest;
-      // the row sum takes them in fp32, divided by v. Where v is 0 all codes are, and any v
-      // small enough not to lead will do.
-      float lv[4], iv[4];
-      if constexpr (kQ) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (vs[x] == 0.f) vs[x] = 0x1p-40f;
-          lv[x] = __log2f(vs[x]);
-          iv[x] = __frcp_rn(vs[x]);
-        }
-      }
-      uint4 pa[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float lm[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 cg = S.cg[warp][16 * mt + g + 8 * e];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float& y = z[mt][x >> 1][2 * e + (x & 1)];
-            y = kQ ? fmaf(y * ks[x], cg.x, fmaf(cg.y, sk[x], lv[x])) : fmaf(y, cg.x, cg.y * sk[x]);
-          }
-        }
-        if (nv - k0 < 16) {   // keys that are not there
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (k0 + off + 8 * (x >> 1) + (x & 1) >= nv) z[mt][x >> 1][x & 1] = z[mt][x >> 1][2 + (x & 1)] = -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          lm[e] = fmaxf(fmaxf(z[mt][0][2 * e], z[mt][0][2 * e + 1]), fmaxf(z[mt][1][2 * e], z[mt][1][2 * e + 1]));
-        // A row's reference moves when a logit exceeds it by more than it may: bf16 weights
-        // stay below 2^8, fp16 ones below 2^14 (and tend to be below 2^6).
-        constexpr float kLift = kQ ? 6.f : 0.f;
-        if (__any_sync(0xFFFFFFFFu, lm[0] > m[mt][0] + (kLift + kRescaleThreshold) ||
-                                        lm[1] > m[mt][1] + (kLift + kRescaleThreshold))) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float t = fmaxf(lm[e], __shfl_xor_sync(0xFFFFFFFFu, lm[e], 1));
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
-            t = t > m[mt][e] + (kLift + kRescaleThreshold) ? ceilf(t) - kLift : m[mt][e];
-            const float alpha = t == m[mt][e] ? 1.f : tg::exp2_approx(m[mt][e] - t);
-            m[mt][e] = t;
-            l[mt][e] *= alpha;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              o[mt][k][2 * e] *= alpha;
-              o[mt][k][2 * e + 1] *= alpha;
-            }
-          }
-        }
-        uint32_t pk[2][2];   // [row half][key half]
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float nm = m[mt][e] == -INFINITY ? 0.f : -m[mt][e];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float p0 = tg::exp2_approx(z[mt][h][2 * e] + nm), p1 = tg::exp2_approx(z[mt][h][2 * e + 1] + nm);
-            if constexpr (kQ) {
-              pk[e][h] = pack_f16x2(p0, p1);
-              l[mt][e] = fmaf(p0, iv[2 * h], fmaf(p1, iv[2 * h + 1], l[mt][e]));
-            } else {   // the sum of the rounded weights: a key that dominates gives its value exactly
-              pk[e][h] = tg::pack_bf16x2(p0, p1);
-              l[mt][e] += bf16_lo(pk[e][h]) + bf16_hi(pk[e][h]);
-            }
-          }
-        }
-        pa[mt] = make_uint4(pk[0][0], pk[1][0], pk[0][1], pk[1][1]);
-      }
-      // ---- O += P V: 16 dims of the thread's four keys, products 2 wi and 2 wi + 1 ----
-      uint4 xv[4][kQ ? 1 : 2];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int key = k0 + off + 8 * (y >> 1) + (y & 1);
-        const uint8_t* p = S.tile[sv] + (hd * A.unit + key) * 128 + ((g ^ (key & 7)) << 4);
-#pragma unroll
-        for (int h = 0; h < (kQ ? 1 : 2); ++h) {
-          xv[y][h] = *reinterpret_cast<const uint4*>(p + h * C::kHalf);
-          if (nv - k0 < 16 && key >= nv) xv[y][h] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
-        }
-      }
-#pragma unroll
-      for (int wi = 0; wi < 8; ++wi) {
-        uint32_t b[2][2];   // [key half][product]
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if constexpr (kQ) {
-            const uint32_t x = word_of(xv[2 * h][0], wi >> 1), y = word_of(xv[2 * h + 1][0], wi >> 1);
-            widen4<kE4m3>(__byte_perm(x, y, wi & 1 ? 0x7362 : 0x5140) ^ (kE4m3 ? 0u : 0x80808080u), b[h][0], b[h][1]);
-          } else {
-            const uint32_t x = word_of(xv[2 * h][wi >> 2], wi & 3), y = word_of(xv[2 * h + 1][wi >> 2], wi & 3);
-            b[h][0] = __byte_perm(x, y, 0x5410);
-            b[h][1] = __byte_perm(x, y, 0x7632);
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma_16816<kQ>(o[mt][2 * wi], pa[mt], b[0][0], b[1][0]);
-          mma_16816<kQ>(o[mt][2 * wi + 1], pa[mt], b[0][1], b[1][1]);
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) tg::mbar_arrive(&S.empty[sv]);
-    r += 2;
-    first = c.run() == 1;   // the last unit of its item here
-    if (first && head) {
-      const int64_t item = static_cast<int64_t>(c.b) * head_groups(A) + c.item;   // one row tile: c.item is the head group
-      const int64_t slot = ((blockIdx.x + item) * A.hw * A.kw + warp) * rows;
-      float* pl = part_ml(A, rows, 128) + slot * 2;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float sum = l[mt][e];
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-          const int row = 16 * mt + g + 8 * e;
-          if (row >= rows) continue;
-          // columns off and off + 1 of every product: eight contiguous dims each
-          float* p = A.part + (slot + row) * 128 + (kQ ? 16 : 8) * off;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-              *reinterpret_cast<float4*>(p + (kQ ? 16 * x + 4 * h : 8 * x + 64 * (h >> 1) + 4 * (h & 1))) =
-                  make_float4(o[mt][4 * h][2 * e + x], o[mt][4 * h + 1][2 * e + x], o[mt][4 * h + 2][2 * e + x],
-                              o[mt][4 * h + 3][2 * e + x]);
-          if (i4 == 0) *reinterpret_cast<float2*>(pl + 2 * row) = make_float2(m[mt][e], sum);
-        }
-    }
-    c.advance(A, S);
-  }
-  if (loader && S.abort_flag)   // let copies in flight land before the CTA exits
-    for (int i = S.issued > C::kRing ? S.issued - C::kRing : 0; i < S.issued; ++i)
-      wait(&S.full[i % C::kRing], (i / C::kRing) & 1, A.status, nullptr);
-}
-
 // Adds up what the CTAs left of every output row, one block a row: the partials of the
 // CTAs c0 .. c1 that share the row's item, kw each, in order, a quarter of them a warp.
 // tree_attn_kernel (kFew false): only items that were cut have partials; CTA c's are in
@@ -1445,43 +905,47 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 constexpr int kCombineWarps = 4;
 
 template <int DH, bool kFew>
-__global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const __grid_constant__ TreeArgs A,
-                                                                          const __nv_bfloat16* __restrict__ q) {
+__global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const __grid_constant__ TreeArgs A) {
   constexpr int kE = DH / 32;
   __shared__ float red[kCombineWarps][DH + 2];
   tg::pdl_launch_dependents();
   tg::pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hq = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-  const int2 sl = seq_lens(A, b, false);
-  if (t >= sl.y) return;
-  const int64_t W = A.base[A.batch], first0 = A.base[b];
+  // what does not wait for anything else is asked for at once
   const int64_t bt = static_cast<int64_t>(b) * A.n_draft + t;
+  const int W = A.base[A.batch], first0 = A.base[b];
+  const int2 sl = tg::seq_lens(A, b, false);
+  uint32_t see = 0;
+  uint2 qw = {};
+  float tau = 1.f, gain = 0.f;
+  if constexpr (kFew) {
+    see = static_cast<uint32_t>(A.mask[bt]);
+    qw = *reinterpret_cast<const uint2*>(A.q + (bt * A.n_hq + hq) * DH + 4 * lane);
+    tau = A.tau[hq];
+    gain = A.gain[hq];
+  }
+  if (t >= sl.y) return;
   const int kvh = hq / A.group;
   float M = -INFINITY, L = 0.f, acc[kE] = {};
-  const int nt = item_units(A, sl.x, sl.y);
+  const int nt = tg::item_units(A, sl.x, sl.y);
   if (nt > 0) {
-    const int64_t G = share_ctas(A, W);
+    const tg::Shares share(A, W);
     const int group = kvh / A.hw, hd = kvh - group * A.hw, mt = t / A.tm;
     const int row = (t - mt * A.tm) * A.group + hq - kvh * A.group, rows = A.group * A.tm;
-    const int64_t first = first0 + (static_cast<int64_t>(group) * row_tiles(A, sl.y) + mt) * nt;
-    // The CTA of unit u is the last c with W c / G <= u: floor(((u + 1) G - 1) / W). With 1/2
-    // for the 1 the quotient stays 1/(2 W) off every whole number, far more than the product
-    // with the rounded 1 / W errs by (148 * 2^-52).
-    const double inv_w = 1.0 / static_cast<double>(W);
-    const int c0 = static_cast<int>((static_cast<double>((first + 1) * G) - 0.5) * inv_w);
-    const int c1 = static_cast<int>((static_cast<double>((first + nt) * G) - 0.5) * inv_w);
+    const int first = first0 + (group * tg::row_tiles(A, sl.y) + mt) * nt;
+    const int c0 = share.cta_of(first), c1 = share.cta_of(first + nt - 1);
     if (!kFew && c0 == c1) return;                        // finished by that CTA
     // the first CTA's place, and the others'
-    const int slot0 = kFew ? c0 + b * head_groups(A) + group : 2 * c0 + (W * c0 < first * G);
+    const int slot0 = kFew ? c0 + b * tg::head_groups(A) + group : 2 * c0 + (share.first(c0) != first);
     const int slot1 = kFew ? slot0 - c0 : 0;
-    const float* ml = part_ml(A, rows, DH);
+    const float* ml = tg::part_ml(A, rows, DH);
     const int n = (c1 - c0 + 1) * A.kw;
     // each warp: partials warp, warp + 4, ..; 32 of them at a time
 #pragma unroll 1
     for (int i0 = warp; i0 < n; i0 += 32 * kCombineWarps) {
       const int i = i0 + kCombineWarps * lane;
-      const int ci = i / A.kw, slot = ci == 0 ? slot0 : kFew ? slot1 + c0 + ci : 2 * (c0 + ci);
+      const int ci = A.kw == 1 ? i : i / A.kw, slot = ci == 0 ? slot0 : kFew ? slot1 + c0 + ci : 2 * (c0 + ci);
       const int64_t at = i < n ? (static_cast<int64_t>(slot) * A.hw * A.kw + hd * A.kw + (i - ci * A.kw)) * rows + row : 0;
       const float2 v = i < n ? *reinterpret_cast<const float2*>(ml + at * 2) : make_float2(-INFINITY, 0.f);
       float mb = v.x;
@@ -1496,32 +960,35 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
       const float wt = tg::exp2_approx(v.x - base);
       const int ns = min(32, (n - i0 + kCombineWarps - 1) / kCombineWarps);
 #pragma unroll 1
-      for (int k0 = 0; k0 < ns; k0 += 4) {   // four rows in flight
-        float x[4][kE], wk[4];
+      for (int k0 = 0; k0 < ns; k0 += 8) {   // eight rows in flight
+        float x[8][kE], wk[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const int k1 = min(k0 + k, ns - 1);
           const int64_t from = __shfl_sync(0xFFFFFFFFu, at, k1);
-          wk[k] = __shfl_sync(0xFFFFFFFFu, wt, k1);
           const float lk = __shfl_sync(0xFFFFFFFFu, v.y, k1);
-          const bool there = k0 + k < ns;
-          L = there ? fmaf(wk[k], lk, L) : L;
+          wk[k] = __shfl_sync(0xFFFFFFFFu, wt, k1);
+          if (k0 + k < ns) {
+            L = fmaf(wk[k], lk, L);
 #pragma unroll
-          for (int e = 0; e < kE; ++e) x[k][e] = there ? A.part[from * DH + lane * kE + e] : 0.f;
+            for (int e = 0; e < kE; ++e) x[k][e] = A.part[from * DH + lane * kE + e];
+          } else {
+            wk[k] = 0.f;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) x[k][e] = 0.f;
+          }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
 #pragma unroll
           for (int e = 0; e < kE; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
       }
     }
   }
   if constexpr (kFew) {
-    uint32_t see = static_cast<uint32_t>(A.mask[bt]);
     if (sl.y < 32) see &= (1u << sl.y) - 1;
-    const uint2 qw = *reinterpret_cast<const uint2*>(q + (bt * A.n_hq + hq) * DH + 4 * lane);
     const float qf[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
-    const float ch = kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]), gh = A.gain[hq] * kLog2e;
+    const float ch = kLog2e / (sqrtf(static_cast<float>(DH)) * tau), gh = gain * kLog2e;
     int place = 0;
 #pragma unroll 1
     for (; see; see &= see - 1, ++place) {
@@ -1571,24 +1038,26 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
 struct Plan {
   bool few;   // tree_rows_kernel
   int tm, unit, hw, kw, n_cta;
-  int64_t slots;
+  int64_t units, slots;
   size_t base_bytes, bytes;
 };
-Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim) {
+Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim, bool codes) {
   Plan p;
   const int group = n_hq / n_hkv;
   p.tm = kBM / group < n_draft ? kBM / group : n_draft;
   const int rows = group * p.tm;
-  p.few = head_dim == 128 && rows <= kRowMax;
-  p.hw = p.few ? (n_hkv < kRowWarps ? n_hkv : kRowWarps) : 1;
-  p.kw = p.few ? kRowWarps / p.hw : 1;
+  p.few = head_dim == 128 && rows <= tg::kTreeRowsMax;
+  const int warps = tg::tree_rows_warps(codes, rows);
+  p.hw = p.few ? (n_hkv < warps ? n_hkv : warps) : 1;
+  p.kw = p.few ? warps / p.hw : 1;
   p.unit = p.few ? 16 * p.kw : kBN;
   auto units_of = [&](int64_t keys) { return (keys + p.unit - 1) / p.unit; };
   const int64_t items = static_cast<int64_t>(batch) * ((n_hkv + p.hw - 1) / p.hw) * ((n_draft + p.tm - 1) / p.tm);
-  const int64_t units = items * (units_of(max_len) + (p.few ? 0 : units_of(n_draft)));
-  p.n_cta = static_cast<int>(units < 1 ? 1 : units < kMaxCtas ? units : kMaxCtas);
+  p.units = items * (units_of(max_len) + (p.few ? 0 : 1));
+  const int64_t most = p.few ? tg::kTreeRowsCtas : kMaxCtas;
+  p.n_cta = static_cast<int>(p.units < 1 ? 1 : p.units < most ? p.units : most);
   p.slots = p.few ? p.n_cta + items : 2 * p.n_cta;
-  p.base_bytes = (static_cast<size_t>(batch) + 1) * sizeof(int64_t);
+  p.base_bytes = (static_cast<size_t>(batch) + 1) * sizeof(int32_t);
   p.base_bytes = (p.base_bytes + 255) / 256 * 256;
   p.bytes = p.base_bytes +
             static_cast<size_t>(p.slots) * p.hw * p.kw * rows * (head_dim + 2) * sizeof(float);
@@ -1596,60 +1065,29 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
 }
 
 template <int DH, bool kFew>
-tg_status launch_combine(const TreeArgs& a, const void* q, tg_status r, cudaStream_t st) {
+tg_status launch_combine(const TreeArgs& a, tg_status r, cudaStream_t st) {
   if (r != TG_OK || (!kFew && a.max_len == 0)) return r;   // there every item is one unit
   return tg::launch(tree_combine_kernel<DH, kFew>, dim3(a.n_hq, a.n_draft, a.batch), dim3(32 * kCombineWarps), 0, st,
-                    0, a, static_cast<const __nv_bfloat16*>(q));
-}
-
-// The map of a K or V cache, rows of dh (bf16: two halves of 64), 128-byte swizzle (64-byte
-// for 64-byte rows): boxes of `keys` rows of `heads` KV heads, one head after the other.
-template <int DH, int kType>
-bool cache_map(const TreeArgs& a, const void* cache, int keys, int heads, CUtensorMap* map) {
-  constexpr bool kQ = kType != TG_BF16;
-  const uint64_t es = kQ ? 1 : 2, rows = static_cast<uint64_t>(a.batch) * a.cap;
-  const uint64_t dims[3] = {DH, rows, static_cast<uint64_t>(a.n_hkv)};
-  const uint64_t str[2] = {a.n_hkv * DH * es, DH * es};
-  const uint32_t box[3] = {kQ ? DH : 64, static_cast<uint32_t>(keys), static_cast<uint32_t>(heads)};
-  return tg::encode_tmap(map, kQ ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, cache,
-                         dims, str, box,
-                         kQ && DH == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-template <int kType, int MT>
-tg_status launch_rows(const TreeArgs& a, const void* q, cudaStream_t st) {
-  CUtensorMap tk, tv;
-  if (!cache_map<128, kType>(a, a.kc, a.unit, a.hw, &tk) || !cache_map<128, kType>(a, a.vc, a.unit, a.hw, &tv))
-    return TG_ERR_CUDA;
-  constexpr int smem = sizeof(RowSmem<kType != TG_BF16, MT>) + 1024;
-  static_assert(smem <= 232448, "the shared memory of one SM");
-  if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_rows_kernel<kType, MT>), smem)) return TG_ERR_CUDA;
-  return launch_combine<128, true>(
-      a, q, tg::launch(tree_rows_kernel<kType, MT>, dim3(a.n_cta), dim3(kRowThreads), smem, st, 0, tk, tv,
-                    static_cast<const __nv_bfloat16*>(q), a), st);
+                    0, a);
 }
 
 template <int DH, int kType>
-tg_status launch_tree(const TreeArgs& a, const void* q, bool few, cudaStream_t st) {
+tg_status launch_tree(const TreeArgs& a, cudaStream_t st) {
   constexpr bool kQ = kType != TG_BF16;
   using C = Cfg<DH, kQ>;
-  if constexpr (DH == 128) {
-    const int rows = a.group * a.tm;
-    if (few) return rows <= 16 ? launch_rows<kType, 1>(a, q, st) : launch_rows<kType, 2>(a, q, st);
-  }
   CUtensorMap tq, tk, tv;
   const uint64_t qdims[3] = {DH, static_cast<uint64_t>(a.n_hq), static_cast<uint64_t>(a.batch) * a.n_draft};
   const uint64_t qstr[2] = {DH * 2, static_cast<uint64_t>(a.n_hq) * DH * 2};
   const uint32_t qbox[3] = {64, static_cast<uint32_t>(a.group), static_cast<uint32_t>(a.tm)};
-  if (!tg::encode_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qdims, qstr, qbox,
+  if (!tg::encode_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, qdims, qstr, qbox,
                        CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !cache_map<DH, kType>(a, a.kc, kBN, 1, &tk) || !cache_map<DH, kType>(a, a.vc, kBN, 1, &tv))
+      !tg::tree_cache_map(a, a.kc, DH, kQ, kBN, 1, &tk) || !tg::tree_cache_map(a, a.vc, DH, kQ, kBN, 1, &tv))
     return TG_ERR_CUDA;
   constexpr int smem = sizeof(TreeSmem<DH, kQ>) + 1024;
   static_assert(smem <= 232448, "the shared memory of one SM");
   if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_attn_kernel<DH, kType>), smem)) return TG_ERR_CUDA;
   return launch_combine<DH, false>(
-      a, q, tg::launch(tree_attn_kernel<DH, kType>, dim3(a.n_cta), dim3(C::kThreads), smem, st, 0, tq, tk, tv, a), st);
+      a, tg::launch(tree_attn_kernel<DH, kType>, dim3(a.n_cta), dim3(C::kThreads), smem, st, 0, tq, tk, tv, a), st);
 }
 
 }  // namespace
@@ -1659,7 +1097,10 @@ extern "C" size_t tg_tree_attention_workspace_size(int batch, int n_draft, int m
   if (batch <= 0 || n_draft <= 0 || max_len < 0 || n_hkv <= 0 || n_hq < n_hkv || n_hq / n_hkv > kBM ||
       head_dim <= 0)
     return 0;
-  return plan(batch, n_draft, max_len, n_hq, n_hkv, head_dim).bytes;
+  // for either kind of cache
+  const size_t a = plan(batch, n_draft, max_len, n_hq, n_hkv, head_dim, false).bytes;
+  const size_t b = plan(batch, n_draft, max_len, n_hq, n_hkv, head_dim, true).bytes;
+  return a > b ? a : b;
 }
 
 extern "C" tg_status tg_tree_attention(
@@ -1682,31 +1123,35 @@ extern "C" tg_status tg_tree_attention(
   const bool quantised = cache_dtype != TG_BF16;
   if (quantised ? !k_scale || !v_scale : k_scale || v_scale) return TG_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || n_draft > kMaxDraft || n_hq / n_hkv > kBM ||
-      batch > kMaxBatch || n_hkv > 1024 || static_cast<int64_t>(batch) * cap > INT32_MAX - kBN)
+      batch > tg::kTreeMaxBatch || n_hkv > 1024 || static_cast<int64_t>(batch) * cap > INT32_MAX - kBN)
     return TG_ERR_UNSUPPORTED;
   if (!tg::aligned16(q) || !tg::aligned16(k_draft) || !tg::aligned16(v_draft) ||
       !tg::aligned16(k_cache) || !tg::aligned16(v_cache) || !tg::aligned16(out))
     return TG_ERR_MISALIGNED;
-  const Plan p = plan(batch, n_draft, max_len, n_hq, n_hkv, head_dim);
-  if (!workspace || workspace_bytes < p.bytes) return TG_ERR_WORKSPACE;
+  const Plan p = plan(batch, n_draft, max_len, n_hq, n_hkv, head_dim, quantised);
+  if (p.units > INT32_MAX / 2) return TG_ERR_UNSUPPORTED;   // far more keys than a GPU holds
+  if (!workspace || workspace_bytes < tg_tree_attention_workspace_size(batch, n_draft, max_len, n_hq, n_hkv, head_dim))
+    return TG_ERR_WORKSPACE;
   if (!tg::aligned16(workspace)) return TG_ERR_MISALIGNED;
   TreeArgs a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
   a.kd = static_cast<const __nv_bfloat16*>(k_draft), a.vd = static_cast<const __nv_bfloat16*>(v_draft);
   a.sd = s_draft, a.mask = tree_mask, a.draft_len = draft_len;
   a.kc = static_cast<const uint8_t*>(k_cache), a.vc = static_cast<const uint8_t*>(v_cache);
   a.ks = k_scale, a.vs = v_scale, a.sc = s_cache, a.cache_len = cache_len;
   a.gain = gain, a.tau = tau, a.out = static_cast<__nv_bfloat16*>(out);
-  a.base = static_cast<int64_t*>(workspace);
+  a.base = static_cast<int32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.base_bytes);
   a.batch = batch, a.n_draft = n_draft, a.cap = cap, a.max_len = max_len, a.n_hq = n_hq, a.n_hkv = n_hkv;
-  a.group = n_hq / n_hkv, a.tm = p.tm, a.unit = p.unit, a.hw = p.hw, a.kw = p.kw, a.n_cta = p.n_cta;
+  a.group = n_hq / n_hkv, a.group_inv = (65536 + a.group - 1) / a.group, a.tm = p.tm, a.unit = p.unit, a.hw = p.hw, a.kw = p.kw, a.n_cta = p.n_cta;
   a.few = p.few, a.slots = p.slots;
   a.status = tg::status_word();
   if (!a.status) return TG_ERR_CUDA;
+  if (p.few) return launch_combine<128, true>(a, tg::launch_tree_rows(a, cache_dtype, stream), stream);
   if (head_dim == 128) {
-    if (cache_dtype == TG_BF16) return launch_tree<128, TG_BF16>(a, q, p.few, stream);
-    return cache_dtype == TG_I8 ? launch_tree<128, TG_I8>(a, q, p.few, stream) : launch_tree<128, TG_E4M3>(a, q, p.few, stream);
+    if (cache_dtype == TG_BF16) return launch_tree<128, TG_BF16>(a, stream);
+    return cache_dtype == TG_I8 ? launch_tree<128, TG_I8>(a, stream) : launch_tree<128, TG_E4M3>(a, stream);
   }
-  if (cache_dtype == TG_BF16) return launch_tree<64, TG_BF16>(a, q, p.few, stream);
-  return cache_dtype == TG_I8 ? launch_tree<64, TG_I8>(a, q, p.few, stream) : launch_tree<64, TG_E4M3>(a, q, p.few, stream);
+  if (cache_dtype == TG_BF16) return launch_tree<64, TG_BF16>(a, stream);
+  return cache_dtype == TG_I8 ? launch_tree<64, TG_I8>(a, stream) : launch_tree<64, TG_E4M3>(a, stream);
 }

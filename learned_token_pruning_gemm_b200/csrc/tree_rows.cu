@@ -1,0 +1,496 @@
+// tg_tree_attention for few rows (drafted tokens x query heads of a KV head, up to 32, head
+// dim 128): the part over the cache. There is little to multiply per byte of cache then,
+// and the 128-row tiles of tree_attn_kernel spend their time in the hand-over between its
+// roles. Here all warps run the same code, straight from a TMA ring into the register
+// fragments of m16n8k16 products, each with its own running reference, sums and O, so
+// nothing joins them but the ring.
+//
+// A unit is 16 keys a warp: the warps share hw KV heads of the same cache rows (all of them
+// up to four or eight, so that a tile is one contiguous piece of the cache or nearly) and, where there are
+// fewer heads, split the keys in kw parts. Every warp leaves a partial (max, sum, O) per
+// item, and the second kernel adds those up and brings in the drafted rows.
+//
+// Products are taken as S^T = K Q^T (16 keys x 8 rows at a time) and O^T = V^T P^T: rows
+// are the short side of a product, so eight rows cost half of sixteen. The weights change
+// from one product's result to the other's operand by a transpose of 8 x 8 in the warp.
+// Any dim may take any place of an inner index or of the 16-high side, as long as both
+// operands agree, so that every thread (g = lane / 4, i = lane % 4) reads 16-byte pieces:
+//   S^T: dims 32 i .. 32 i + 31 of keys g and g + 8 (codes; of a bf16 cache the 8-dim
+//        columns 2 i and 2 i + 1 of both 64-dim halves);
+//   O^T: dims 16 g .. 16 g + 15 (bf16: 8 g .. 8 g + 7 of both halves) of keys 2 i, 2 i + 1,
+//        2 i + 8 and 2 i + 9: product t holds the dims at places 2 t and 2 t + 1 of these.
+// Codes are widened to fp16, which holds them exactly at half the instructions that bf16
+// takes; the queries are then fp16 too, after their largest value is brought near 2^8.
+#include <cuda_fp16.h>
+
+#include "tree.cuh"
+
+namespace {
+
+using tg::TreeArgs;
+using tg::bf16_hi;
+using tg::bf16_lo;
+using tg::wait;
+
+// NT: tiles of eight rows. Two CTAs share an SM, so that one's start and end of an item pass
+// under the other's work; eight warps each where half of the registers are enough for that,
+// four otherwise, and for bf16 tiles, whose ring would be too short with eight.
+constexpr int warps_of(bool codes, int n_tiles) { return codes && n_tiles == 1 ? 8 : 4; }
+template <bool kQ, int NT>
+struct Cfg {
+  static constexpr int kWarps = warps_of(kQ, NT);
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kHalf = 16 * kWarps * 128;      // 128-byte rows of a tile (bf16: of one half of it)
+  static constexpr int kTile = kHalf * (kQ ? 1 : 2);   // bytes of a K or V tile, at most
+  static constexpr int kRing = kQ ? (NT == 1 ? 5 : NT == 2 ? 10 : 8) : (NT == 4 ? 4 : 5);
+  static_assert(kRing >= 4, "a unit's tiles are asked for while the one before is in use");
+};
+
+// Places in the walk over a CTA's units.
+struct Cursor {
+  int u, u1, b, group, j, nt, len;
+  template <class S>
+  __device__ __forceinline__ void start(const TreeArgs& A, const S& s, int first, int n) {
+    u = first;
+    u1 = first + n;
+    b = tg::sequence_of(A, s, u);
+    len = s.len[b];
+    nt = tg::key_units(A, len);
+    group = (u - s.base[b]) / nt;
+    j = u - s.base[b] - group * nt;
+  }
+  template <class S>
+  __device__ __forceinline__ void advance(const TreeArgs& A, const S& s) {
+    ++u;
+    if (++j < nt || u >= u1) return;
+    j = 0;
+    if (++group < tg::head_groups(A)) return;
+    group = 0;
+    do ++b;
+    while (s.base[b + 1] == s.base[b]);   // sequences without units
+    len = s.len[b];
+    nt = tg::key_units(A, len);
+  }
+};
+
+template <bool kQ, int NT>
+struct RowSmem {
+  using C = Cfg<kQ, NT>;
+  uint8_t tile[C::kRing][C::kTile];
+  uint2 q[C::kWarps][NT][8][32];       // B fragments of each warp's queries
+  float2 cg[C::kWarps][8 * NT];        // each row's logit factor and gain, log2 domain
+  int base[tg::kTreeMaxBatch + 1];
+  int len[tg::kTreeMaxBatch];
+  uint8_t dl[tg::kTreeMaxBatch];
+  uint64_t full[C::kRing], empty[C::kRing];
+  Cursor next;                      // the unit that is loaded next, and
+  int issued;                       // the tiles that are on their way or here
+  int abort_flag;
+};
+
+// Loads tiles as far as the ring reaches (K at even places, V at odd ones): tile t needs
+// tile t - kRing to be consumed by every warp, which is waited for, and all before
+// `consumed` are by this one. One thread.
+template <bool kQ, int NT>
+__device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<kQ, NT>& S, const CUtensorMap* tm_k,
+                                       const CUtensorMap* tm_v, int consumed) {
+  using C = Cfg<kQ, NT>;
+  int t = S.issued;
+  Cursor c = S.next;
+  while (t < consumed + C::kRing && c.u < c.u1) {
+    const int s = t % C::kRing;
+    if (t >= C::kRing && !wait(&S.empty[s], ((t / C::kRing) - 1) & 1, A.status, &S.abort_flag)) break;
+    const uint32_t half = A.hw * A.unit * 128;
+    tg::mbar_arrive_expect_tx(&S.full[s], kQ ? half : 2 * half);
+    const CUtensorMap* map = t & 1 ? tm_v : tm_k;
+    const int row = c.b * A.cap + c.j * A.unit, kvh = c.group * A.hw;
+    tg::tma_load_3d(S.tile[s], map, &S.full[s], 0, row, kvh);
+    if constexpr (!kQ) tg::tma_load_3d(S.tile[s] + C::kHalf, map, &S.full[s], 64, row, kvh);
+    if (t & 1) c.advance(A, S);
+    ++t;
+  }
+  S.issued = t;
+  S.next = c;
+}
+
+// One 16 x 8 x 16 product, bf16 (kF16: fp16) operands, fp32 sums.
+template <bool kF16>
+__device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (kF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values held as product fragments.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Four codes (bytes of w; int8 ones with the sign bit flipped) to four fp16 values, exactly.
+template <bool kE4m3>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kE4m3) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {   // 1024 + (code + 128) has the code's bits as its last eight; then less 1152
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
+  }
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float scale) {
+  return pack_f16x2(bf16_lo(w) * scale, bf16_hi(w) * scale);
+}
+// 8 bytes global -> shared, asynchronously
+__device__ __forceinline__ void cp8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tg::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <int kType, int NT>
+__global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, 2)
+    tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ TreeArgs A) {
+  constexpr bool kQ = kType != TG_BF16;
+  constexpr bool kE4m3 = kType == TG_E4M3;
+  constexpr uint32_t kFlip = kType == TG_I8 ? 0x80808080u : 0u;
+  using C = Cfg<kQ, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (tg::smem_u32(smem_raw) & 1023u)) & 1023u;
+  RowSmem<kQ, NT>& S = *reinterpret_cast<RowSmem<kQ, NT>*>(smem_raw + pad);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, i4 = lane & 3;
+  if (tid == 0) {
+    for (int s = 0; s < C::kRing; ++s) {
+      tg::mbar_init(&S.full[s], 1);
+      tg::mbar_init(&S.empty[s], C::kWarps);
+    }
+    S.abort_flag = 0;
+    tg::fence_barrier_init();
+    tg::tma_prefetch_desc(&tm_k);
+    tg::tma_prefetch_desc(&tm_v);
+  }
+  tg::pdl_launch_dependents();
+  tg::pdl_wait();   // global memory only from here on
+  const tg::Shares share(A, tg::count_units<C::kThreads>(A, S));
+  const int n = share.size(blockIdx.x);
+  if (n == 0) return;   // uniform: nothing to do here
+  Cursor c;
+  c.start(A, S, share.first(blockIdx.x), n);
+  const bool loader = tid == C::kThreads - 1;   // the last warp's last thread
+  if (loader) {
+    S.issued = 0;
+    S.next = c;
+    row_loads<kQ, NT>(A, S, &tm_k, &tm_v, 0);
+  }
+  __syncwarp();
+
+  // A wait that runs out records itself and sets the abort flag, after which every wait
+  // returns at once: the loops below take the same steps either way.
+  const int rows = A.group * A.n_draft;
+  const int hd = warp / A.kw, k0 = 16 * (warp - hd * A.kw);   // head of the item, first key of the unit
+  float o[NT][8][4];                  // product t: dims at places 2t, 2t + 1 x rows 2 i4, 2 i4 + 1
+  float m[NT][2], l[NT][2];           // of rows 2 i4 and 2 i4 + 1 of every tile
+  bool first = true;
+  int r = 0;
+#pragma unroll 1
+  for (int u = 0; u < n; ++u) {
+    const int kvh = c.group * A.hw + hd;
+    const bool head = hd < A.hw && kvh < A.n_hkv;   // else this warp only keeps the ring going
+    const int nv = min(A.unit, c.len - c.j * A.unit);
+    const bool any = head && k0 < nv;
+    // what the thread's keys g and g + 8 bring besides K and V; keys behind the last one
+    // read its place and are masked below
+    float sk[2], ks[2], vs[2];
+    if (any) {
+      const int64_t row0 = static_cast<int64_t>(c.b) * A.cap + c.j * A.unit;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int64_t row = row0 + min(k0 + g + 8 * x, nv - 1);
+        sk[x] = ks[x] = vs[x] = 0.f;
+        if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
+        sk[x] = A.sc[row];
+        if constexpr (kQ) {
+          ks[x] = A.ks[row * A.n_hkv + kvh];
+          vs[x] = A.vs[row * A.n_hkv + kvh];
+        }
+      }
+    }
+    if (first && head) {   // a new item: its queries, and nothing seen yet
+      __syncwarp();
+      const int64_t row_q = static_cast<int64_t>(c.b) * A.n_draft * A.n_hq + kvh * A.group;
+#pragma unroll 1
+      for (int nt = 0; nt < NT; ++nt) {   // rows behind the last: any row that is there
+        const int row = min(8 * nt + g, rows - 1), tok = tg::token_of(A, row);
+        const __nv_bfloat16* p = A.q + (row_q + tok * A.n_hq + row - tok * A.group) * 128;
+#pragma unroll
+        for (int t = 0; t < 8; ++t)   // dims as the keys' below
+          cp8(&S.q[warp][nt][t][lane],
+              p + (kQ ? 32 * i4 + 4 * t : 64 * (t >> 2) + 16 * i4 + 8 * ((t >> 1) & 1) + 4 * (t & 1)));
+      }
+      if (lane < 8 * NT) {
+        const int row = min(lane, rows - 1), hq = kvh * A.group + row - tg::token_of(A, row) * A.group;
+        S.cg[warp][lane] = make_float2(tg::kLog2e / (sqrtf(128.f) * A.tau[hq]), A.gain[hq] * tg::kLog2e);
+      }
+      cp_wait_all();
+      __syncwarp();
+      if constexpr (kQ) {
+        // to fp16: the row is multiplied by the power of two that brings its largest value
+        // (exponent field e) to [2^8, 2^9), so that values down to 2^-22 of it stay exact
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt) {
+          uint2 x[8];
+          uint32_t mx = 0;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            x[t] = S.q[warp][nt][t][lane];
+            mx = max_u16x2(mx, max_u16x2(x[t].x & 0x7FFF7FFFu, x[t].y & 0x7FFF7FFFu));
+          }
+          mx = max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+          mx = max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+          const int e = max(static_cast<int>(max(mx >> 16, mx & 0xFFFFu) >> 7), 9);
+          const float down = __int_as_float((262 - e) << 23);
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            S.q[warp][nt][t][lane] = make_uint2(bf16x2_to_f16x2(x[t].x, down), bf16x2_to_f16x2(x[t].y, down));
+          if (i4 == 0) S.cg[warp][8 * nt + g].x *= __int_as_float((e - 8) << 23);
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.f;
+      }
+    }
+    // ---- S^T = K Q^T ----
+    float z[NT][4];   // key g: rows 2 i4, 2 i4 + 1; key g + 8: the same
+    const int s = r % C::kRing, sv = (r + 1) % C::kRing;
+    wait(&S.full[s], (r / C::kRing) & 1, A.status, &S.abort_flag);
+    __syncwarp();
+    if (any) {
+      // a head's rows of the tile follow each other; the places of both keys among eight are g
+      const uint8_t* p = S.tile[s] + (hd * A.unit + k0 + g) * 128;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[nt][e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < (kQ ? 2 : 4); ++i) {
+        const uint8_t* at = p + (kQ ? 0 : (i >> 1) * C::kHalf) + (((2 * i4 + (i & 1)) ^ g) << 4);
+        const uint4 x0 = *reinterpret_cast<const uint4*>(at), x1 = *reinterpret_cast<const uint4*>(at + 8 * 128);
+#pragma unroll
+        for (int e = 0; e < (kQ ? 4 : 2); ++e) {   // product t: four dims of the thread's part
+          const int t = (kQ ? 4 : 2) * i + e;
+          uint32_t a0, a1, a2, a3;
+          if constexpr (kQ) {
+            widen4<kE4m3>(word_of(x0, e) ^ kFlip, a0, a2);
+            widen4<kE4m3>(word_of(x1, e) ^ kFlip, a1, a3);
+          } else {
+            a0 = word_of(x0, 2 * e), a2 = word_of(x0, 2 * e + 1);
+            a1 = word_of(x1, 2 * e), a3 = word_of(x1, 2 * e + 1);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 b = S.q[warp][nt][t][lane];
+            mma_16816<kQ>(z[nt], a0, a1, a2, a3, b.x, b.y);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tg::mbar_arrive(&S.empty[s]);
+    // the ring goes on where every warp is through with the unit before
+    if (loader) row_loads<kQ, NT>(A, S, &tm_k, &tm_v, r);
+    __syncwarp();
+    uint32_t b[NT][2];   // the weights as fragments
+    if (any) {
+      // ---- weights ----
+      // Codes: the value scale v joins the logit, z + log2 v, so that the fp16 weights
+      // 2^(z + log2 v - m) are what the codes are multiplied by and m follows their largest;
+      // the row sum takes them in fp32, divided by v. Where v is 0 all codes are, and any v
+      // small enough not to lead will do.
+      float lv[2] = {}, iv[2] = {1.f, 1.f};
+      if constexpr (kQ) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (vs[x] == 0.f) vs[x] = 0x1p-40f;
+          lv[x] = __log2f(vs[x]);
+          iv[x] = __frcp_rn(vs[x]);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float4 cg = *reinterpret_cast<const float4*>(&S.cg[warp][8 * nt + 2 * i4]);   // two rows
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float &y0 = z[nt][2 * x], &y1 = z[nt][2 * x + 1];
+          if constexpr (kQ) {
+            y0 = fmaf(y0 * ks[x], cg.x, fmaf(cg.y, sk[x], lv[x]));
+            y1 = fmaf(y1 * ks[x], cg.z, fmaf(cg.w, sk[x], lv[x]));
+          } else {
+            y0 = fmaf(y0, cg.x, cg.y * sk[x]);
+            y1 = fmaf(y1, cg.z, cg.w * sk[x]);
+          }
+          if (k0 + g + 8 * x >= nv) y0 = y1 = -INFINITY;   // a key that is not there
+        }
+        // A row's reference is a whole number at or above its largest logit (fp16 weights: 6
+        // below that, to keep small ones exact) when it is set, and moves when a logit exceeds
+        // it by 2^8 more, so that bf16 weights stay below 2^8 and fp16 ones below 2^14.
+        constexpr float kLift = kQ ? 6.f : 0.f, kMost = kLift + tg::kRescaleThreshold;
+        const float m0 = fmaxf(z[nt][0], z[nt][2]), m1 = fmaxf(z[nt][1], z[nt][3]);
+        if (__any_sync(0xFFFFFFFFu, m0 > m[nt][0] + kMost || m1 > m[nt][1] + kMost)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = e ? m1 : m0;
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, x));
+            t = t > m[nt][e] + kMost ? ceilf(t) - kLift : m[nt][e];
+            const float alpha = t == m[nt][e] ? 1.f : tg::exp2_approx(m[nt][e] - t);
+            m[nt][e] = t;
+            l[nt][e] *= alpha;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              o[nt][k][e] *= alpha;
+              o[nt][k][2 + e] *= alpha;
+            }
+          }
+        }
+        const float n0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0], n1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float p0 = tg::exp2_approx(z[nt][2 * x] + n0), p1 = tg::exp2_approx(z[nt][2 * x + 1] + n1);
+          uint32_t w;
+          if constexpr (kQ) {
+            w = pack_f16x2(p0, p1);
+            l[nt][0] = fmaf(p0, iv[x], l[nt][0]);
+            l[nt][1] = fmaf(p1, iv[x], l[nt][1]);
+          } else {   // the sum of the rounded weights: a key that dominates gives its value exactly
+            w = tg::pack_bf16x2(p0, p1);
+            l[nt][0] += bf16_lo(w);
+            l[nt][1] += bf16_hi(w);
+          }
+          b[nt][x] = transpose8(w);
+        }
+      }
+    }
+    wait(&S.full[sv], ((r + 1) / C::kRing) & 1, A.status, &S.abort_flag);
+    __syncwarp();
+    if (any) {
+      // ---- O^T += V^T P^T ----
+      uint4 xv[4][kQ ? 1 : 2];   // keys 2 i4 + {0, 1, 8, 9}
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int key = k0 + 2 * i4 + (y & 1) + 8 * (y >> 1);
+        const uint8_t* p = S.tile[sv] + (hd * A.unit + key) * 128 + ((g ^ (key & 7)) << 4);
+#pragma unroll
+        for (int h = 0; h < (kQ ? 1 : 2); ++h) {
+          xv[y][h] = *reinterpret_cast<const uint4*>(p + h * C::kHalf);
+          if (nv - k0 < 16 && key >= nv) xv[y][h] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        uint32_t a[4];   // [key half][place]
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (kQ) {
+            const uint32_t x = word_of(xv[2 * h][0], t >> 1), y = word_of(xv[2 * h + 1][0], t >> 1);
+            widen4<kE4m3>(__byte_perm(x, y, t & 1 ? 0x7362 : 0x5140) ^ kFlip, a[2 * h], a[2 * h + 1]);
+          } else {
+            const uint32_t x = word_of(xv[2 * h][t >> 2], t & 3), y = word_of(xv[2 * h + 1][t >> 2], t & 3);
+            a[2 * h] = __byte_perm(x, y, 0x5410);
+            a[2 * h + 1] = __byte_perm(x, y, 0x7632);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16816<kQ>(o[nt][t], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tg::mbar_arrive(&S.empty[sv]);
+    r += 2;
+    first = c.j + 1 == c.nt || u + 1 == n;   // the last unit of its item here
+    if (first && head) {
+      // CTA c and item i (numbered over all sequences): slot c + i grows along the units
+      const int64_t slot = (static_cast<int64_t>(blockIdx.x + c.b * tg::head_groups(A) + c.group) * A.hw * A.kw + warp) * rows;
+      float* pl = tg::part_ml(A, rows, 128) + slot * 2;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float sum = l[nt][e];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+          const int row = 8 * nt + 2 * i4 + e;
+          if (row >= rows) continue;
+          // the thread's 16 dims: contiguous (bf16: eight of both halves)
+          float* p = A.part + (slot + row) * 128 + (kQ ? 16 : 8) * g;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            *reinterpret_cast<float4*>(p + (kQ ? 4 * h : 64 * (h >> 1) + 4 * (h & 1))) =
+                make_float4(o[nt][2 * h][e], o[nt][2 * h][2 + e], o[nt][2 * h + 1][e], o[nt][2 * h + 1][2 + e]);
+          if (g == 0) *reinterpret_cast<float2*>(pl + 2 * row) = make_float2(m[nt][e], sum);
+        }
+    }
+    c.advance(A, S);
+  }
+  if (loader && S.abort_flag)   // let copies in flight land before the CTA exits
+    for (int i = S.issued > C::kRing ? S.issued - C::kRing : 0; i < S.issued; ++i)
+      wait(&S.full[i % C::kRing], (i / C::kRing) & 1, A.status, nullptr);
+}
+
+template <int kType, int NT>
+tg_status launch(const TreeArgs& a, cudaStream_t st) {
+  constexpr bool kQ = kType != TG_BF16;
+  CUtensorMap tk, tv;
+  if (!tg::tree_cache_map(a, a.kc, 128, kQ, a.unit, a.hw, &tk) ||
+      !tg::tree_cache_map(a, a.vc, 128, kQ, a.unit, a.hw, &tv))
+    return TG_ERR_CUDA;
+  constexpr int smem = sizeof(RowSmem<kQ, NT>) + 1024;
+  static_assert(smem <= 115712, "half of an SM's shared memory");
+  if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_rows_kernel<kType, NT>), smem)) return TG_ERR_CUDA;
+  return tg::launch(tree_rows_kernel<kType, NT>, dim3(a.n_cta), dim3(Cfg<kQ, NT>::kThreads), smem, st, 0, tk, tv, a);
+}
+
+template <int kType>
+tg_status launch_type(const TreeArgs& a, cudaStream_t st) {
+  const int rows = a.group * a.n_draft;
+  if (rows <= 8) return launch<kType, 1>(a, st);
+  return rows <= 16 ? launch<kType, 2>(a, st) : launch<kType, 4>(a, st);
+}
+
+}  // namespace
+
+int tg::tree_rows_warps(bool codes, int rows) { return warps_of(codes, rows <= 8 ? 1 : rows <= 16 ? 2 : 4); }
+
+tg_status tg::launch_tree_rows(const TreeArgs& a, tg_dtype cache_dtype, cudaStream_t stream) {
+  if (cache_dtype == TG_BF16) return launch_type<TG_BF16>(a, stream);
+  return cache_dtype == TG_I8 ? launch_type<TG_I8>(a, stream) : launch_type<TG_E4M3>(a, stream);
+}
