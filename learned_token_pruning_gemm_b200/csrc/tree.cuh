@@ -81,11 +81,17 @@ struct Shares {
   }
 };
 
+// Per sequence, in shared memory: first unit (one more: the end), cache length, drafted tokens.
+struct TreeSeqs {
+  int *base, *len;
+  uint8_t* dl;
+};
+
 // Every sequence's lengths and first unit into shared memory (CTA 0: the units also to the
 // workspace, for the second kernel); all threads of the block, with barriers. Returns the
 // number of units, below 2^31 (the host sees to it).
-template <int kThreads, class Smem>
-__device__ __forceinline__ int count_units(const TreeArgs& A, Smem& S) {
+template <int kThreads>
+__device__ __forceinline__ int count_units(const TreeArgs& A, const TreeSeqs& S) {
   const int tid = threadIdx.x, lane = tid & 31;
   for (int b = tid; b < A.batch; b += kThreads) {
     const int2 l = seq_lens(A, b, blockIdx.x == 0);
@@ -116,8 +122,7 @@ __device__ __forceinline__ int count_units(const TreeArgs& A, Smem& S) {
 }
 
 // The last sequence whose first unit is at most u.
-template <class Smem>
-__device__ __forceinline__ int sequence_of(const TreeArgs& A, const Smem& S, int u) {
+__device__ __forceinline__ int sequence_of(const TreeArgs& A, const TreeSeqs& S, int u) {
   int lo = 0, hi = A.batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -154,8 +159,8 @@ inline bool tree_cache_map(const TreeArgs& a, const void* cache, int dh, bool co
 
 // tree_rows.cu: the part over the cache for up to kTreeRowsMax rows of head_dim 128.
 constexpr int kTreeRowsMax = 32;
-constexpr int kTreeRowsCtas = 2 * 148;            // two per SM
-int tree_rows_warps(bool codes, int rows);        // warps of a CTA: hw * kw is at most these
+int tree_rows_ctas(bool codes, int rows);    // CTAs that fill the machine
+int tree_rows_warps(bool codes, int rows);   // warps of a CTA: hw * kw is at most these
 tg_status launch_tree_rows(const TreeArgs& a, tg_dtype cache_dtype, cudaStream_t stream);
 
 }  // namespace tg

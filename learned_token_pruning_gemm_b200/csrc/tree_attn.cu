@@ -42,7 +42,7 @@
 // Values of drafted rows that are not finite never enter the products (0 * inf would
 // reach tokens that do not see the row): they are zero in the operand tile, their rows
 // are noted, and the epilogue adds them to the rows that see them.
-#include <cuda_fp16.h>
+#include <type_traits>
 
 #include "tree.cuh"
 
@@ -112,8 +112,7 @@ __device__ __forceinline__ bool value_turn(int i, int n) {
 // item's units, those of the cache before the one of the drafted rows.
 struct Cursor {
   int u, u1, b, item, n_items, kvh, mt, j, nk, nt, len, dl;
-  template <class S>
-  __device__ __forceinline__ void load_seq(const TreeArgs& A, const S& s) {
+  __device__ __forceinline__ void load_seq(const TreeArgs& A, const tg::TreeSeqs& s) {
     len = s.len[b];
     dl = s.dl[b];
     nk = (len + kBN - 1) / kBN;
@@ -125,8 +124,7 @@ struct Cursor {
     kvh = item / amt;
     mt = item - kvh * amt;
   }
-  template <class S>
-  __device__ __forceinline__ void start(const TreeArgs& A, const S& s, int first, int n) {
+  __device__ __forceinline__ void start(const TreeArgs& A, const tg::TreeSeqs& s, int first, int n) {
     u = first;
     u1 = first + n;
     b = tg::sequence_of(A, s, u);
@@ -135,8 +133,7 @@ struct Cursor {
     j = u - s.base[b] - item * nt;
     split_item(A);
   }
-  template <class S>
-  __device__ __forceinline__ void advance(const TreeArgs& A, const S& s) {
+  __device__ __forceinline__ void advance(const TreeArgs& A, const tg::TreeSeqs& s) {
     ++u;
     if (++j < nt || u >= u1) return;
     j = 0;
@@ -363,7 +360,8 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
   tg::pdl_launch_dependents();
   tg::pdl_wait();   // global memory only from here on
   tg::tc_fence_before();
-  const tg::Shares share(A, tg::count_units<C::kThreads>(A, S));
+  const tg::TreeSeqs Q{S.base, S.len, S.dl};
+  const tg::Shares share(A, tg::count_units<C::kThreads>(A, Q));
   tg::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   const int n = share.size(blockIdx.x);
@@ -372,7 +370,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     return;
   }
   Cursor c;
-  c.start(A, S, share.first(blockIdx.x), n);
+  c.start(A, Q, share.first(blockIdx.x), n);
 
   if (!kQ && (warp == 0 || warp == 3)) {
     // ---------------- K (warp 0) or V (warp 3) tiles of a bf16 cache ----------------
@@ -384,7 +382,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     const CUtensorMap* map = val ? &tm_v : &tm_k;
     const __nv_bfloat16* cache = reinterpret_cast<const __nv_bfloat16*>(val ? A.vc : A.kc);
     int n_draft = 0, g = 0;
-    for (; g < n; ++g, c.advance(A, S)) {
+    for (; g < n; ++g, c.advance(A, Q)) {
       const int s = g % n_st;
       if (g >= n_st &&
           !all_alive(wait(&empty[s], ((g / n_st) - 1) & 1, A.status, &S.abort_flag)))
@@ -435,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         if (!val) {
           prev = cur;
           cur = tile_of(c);
-          c.advance(A, S);
+          c.advance(A, Q);
         }
         const Tile t = val && i < 2 * n - 1 ? prev : cur;
         if (t.draft) continue;   // drafted rows are bf16: the converters read them
@@ -484,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
             x[kAhead][2][i] = there && !draft ? A.vs[hr] : 1.f;
           }
         }
-        la.advance(A, S);
+        la.advance(A, Q);
       }
       if (g < 0) continue;
       if (g == 0 || c.j == 0) {   // a new item: its queries, once the last one's S are done
@@ -516,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         }
       }
       tg::mbar_arrive(&S.b_full[s]);
-      c.advance(A, S);
+      c.advance(A, Q);
     }
     if (S.abort_flag && n_q > 0 && lane == 0)
       wait(&S.q_full, (n_q - 1) & 1, A.status, nullptr);
@@ -570,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
             alive = issue_s(g + C::kS);
             if (alive && j + C::kS + 1 == nt) tg::mma_commit(&S.q_empty);
           }
-          c.advance(A, S);
+          c.advance(A, Q);
         }
         g0 += nt;
       }
@@ -816,7 +814,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           if (with_draft) ++n_draft;
           ++seg;
         }
-        c.advance(A, S);
+        c.advance(A, Q);
       }
     }
   } else if (kQ && warp >= 4 + kSoftmaxWarps) {
@@ -837,7 +835,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       if (!val) {
         prev = cur;
         cur = tile_of(c);
-        c.advance(A, S);
+        c.advance(A, Q);
       }
       const Tile t = val && i < 2 * n - 1 ? prev : cur;
       const int g = val ? gv++ : gk++;
@@ -907,26 +905,35 @@ constexpr int kCombineWarps = 4;
 template <int DH, bool kFew>
 __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const __grid_constant__ TreeArgs A) {
   constexpr int kE = DH / 32;
+  using Vec = typename std::conditional<DH == 128, float4, float2>::type;
   __shared__ float red[kCombineWarps][DH + 2];
   tg::pdl_launch_dependents();
   tg::pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hq = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-  // what does not wait for anything else is asked for at once
+  const int kvh = hq / A.group;
+  // what does not wait for anything else is asked for at once, the warp's first drafted row
+  // among it
   const int64_t bt = static_cast<int64_t>(b) * A.n_draft + t;
   const int W = A.base[A.batch], first0 = A.base[b];
   const int2 sl = tg::seq_lens(A, b, false);
   uint32_t see = 0;
-  uint2 qw = {};
-  float tau = 1.f, gain = 0.f;
+  uint2 qw = {}, kw = {}, vw = {};
+  float tau = 1.f, gain = 0.f, sd = 0.f;
+  auto drafted = [&](int i) {
+    const int64_t at = static_cast<int64_t>(b) * A.n_draft + min(i, A.n_draft - 1);
+    kw = *reinterpret_cast<const uint2*>(A.kd + (at * A.n_hkv + kvh) * DH + 4 * lane);
+    vw = *reinterpret_cast<const uint2*>(A.vd + (at * A.n_hkv + kvh) * DH + 4 * lane);
+    sd = A.sd[at];
+  };
   if constexpr (kFew) {
     see = static_cast<uint32_t>(A.mask[bt]);
     qw = *reinterpret_cast<const uint2*>(A.q + (bt * A.n_hq + hq) * DH + 4 * lane);
     tau = A.tau[hq];
     gain = A.gain[hq];
+    drafted(warp);
   }
   if (t >= sl.y) return;
-  const int kvh = hq / A.group;
   float M = -INFINITY, L = 0.f, acc[kE] = {};
   const int nt = tg::item_units(A, sl.x, sl.y);
   if (nt > 0) {
@@ -938,50 +945,39 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     if (!kFew && c0 == c1) return;                        // finished by that CTA
     // the first CTA's place, and the others'
     const int slot0 = kFew ? c0 + b * tg::head_groups(A) + group : 2 * c0 + (share.first(c0) != first);
-    const int slot1 = kFew ? slot0 - c0 : 0;
+    const int parts = A.hw * A.kw, n = (c1 - c0 + 1) * A.kw;
     const float* ml = tg::part_ml(A, rows, DH);
-    const int n = (c1 - c0 + 1) * A.kw;
-    // each warp: partials warp, warp + 4, ..; 32 of them at a time
+    // each warp: partials warp, warp + 4, ..; eight of them at a time, sums and O together
 #pragma unroll 1
-    for (int i0 = warp; i0 < n; i0 += 32 * kCombineWarps) {
-      const int i = i0 + kCombineWarps * lane;
-      const int ci = A.kw == 1 ? i : i / A.kw, slot = ci == 0 ? slot0 : kFew ? slot1 + c0 + ci : 2 * (c0 + ci);
-      const int64_t at = i < n ? (static_cast<int64_t>(slot) * A.hw * A.kw + hd * A.kw + (i - ci * A.kw)) * rows + row : 0;
-      const float2 v = i < n ? *reinterpret_cast<const float2*>(ml + at * 2) : make_float2(-INFINITY, 0.f);
-      float mb = v.x;
+    for (int i0 = warp; i0 < n; i0 += 8 * kCombineWarps) {
+      float2 v[8];
+      Vec x[8];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
-      mb = fmaxf(mb, M);
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + kCombineWarps * k, ci = A.kw == 1 ? i : i / A.kw;
+        const int slot = ci == 0 ? slot0 : kFew ? slot0 + ci : 2 * (c0 + ci);
+        const int64_t at = (static_cast<int64_t>(slot) * parts + hd * A.kw + (i - ci * A.kw)) * rows + row;
+        v[k] = make_float2(-INFINITY, 0.f);
+        x[k] = Vec{};
+        if (i < n) {
+          v[k] = *reinterpret_cast<const float2*>(ml + at * 2);
+          x[k] = *reinterpret_cast<const Vec*>(A.part + at * DH + lane * kE);
+        }
+      }
+      float mb = M;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mb = fmaxf(mb, v[k].x);
       const float base = mb == -INFINITY ? 0.f : mb, scale = tg::exp2_approx(M - base);
       M = mb;
       L *= scale;
 #pragma unroll
       for (int e = 0; e < kE; ++e) acc[e] *= scale;
-      const float wt = tg::exp2_approx(v.x - base);
-      const int ns = min(32, (n - i0 + kCombineWarps - 1) / kCombineWarps);
-#pragma unroll 1
-      for (int k0 = 0; k0 < ns; k0 += 8) {   // eight rows in flight
-        float x[8][kE], wk[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int k1 = min(k0 + k, ns - 1);
-          const int64_t from = __shfl_sync(0xFFFFFFFFu, at, k1);
-          const float lk = __shfl_sync(0xFFFFFFFFu, v.y, k1);
-          wk[k] = __shfl_sync(0xFFFFFFFFu, wt, k1);
-          if (k0 + k < ns) {
-            L = fmaf(wk[k], lk, L);
+      for (int k = 0; k < 8; ++k) {
+        const float wk = tg::exp2_approx(v[k].x - base);
+        L = fmaf(wk, v[k].y, L);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) x[k][e] = A.part[from * DH + lane * kE + e];
-          } else {
-            wk[k] = 0.f;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) x[k][e] = 0.f;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int e = 0; e < kE; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
+        for (int e = 0; e < kE; ++e) acc[e] = fmaf(wk, reinterpret_cast<const float*>(&x[k])[e], acc[e]);
       }
     }
   }
@@ -989,22 +985,21 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     if (sl.y < 32) see &= (1u << sl.y) - 1;
     const float qf[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
     const float ch = kLog2e / (sqrtf(static_cast<float>(DH)) * tau), gh = gain * kLog2e;
-    int place = 0;
 #pragma unroll 1
-    for (; see; see &= see - 1, ++place) {
-      if ((place & (kCombineWarps - 1)) != warp) continue;
-      const int64_t at = static_cast<int64_t>(b) * A.n_draft + __ffs(static_cast<int>(see)) - 1;
-      const uint2 kw = *reinterpret_cast<const uint2*>(A.kd + (at * A.n_hkv + kvh) * DH + 4 * lane);
-      const uint2 vw = *reinterpret_cast<const uint2*>(A.vd + (at * A.n_hkv + kvh) * DH + 4 * lane);
-      float z = fmaf(qf[0], bf16_lo(kw.x), fmaf(qf[1], bf16_hi(kw.x), fmaf(qf[2], bf16_lo(kw.y), qf[3] * bf16_hi(kw.y))));
+    for (int i = warp; i < sl.y; i += kCombineWarps) {
+      const uint2 k1 = kw, v1 = vw;
+      const float s1 = sd;
+      drafted(i + kCombineWarps);
+      if (!((see >> i) & 1)) continue;
+      float z = fmaf(qf[0], bf16_lo(k1.x), fmaf(qf[1], bf16_hi(k1.x), fmaf(qf[2], bf16_lo(k1.y), qf[3] * bf16_hi(k1.y))));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-      z = fmaf(z, ch, gh * A.sd[at]);
+      z = fmaf(z, ch, gh * s1);
       if (z == -INFINITY) continue;   // a weight of zero
       const float mn = fmaxf(M, z), scale = tg::exp2_approx(M - mn), p = tg::exp2_approx(z - mn);
       M = mn;
       L = fmaf(L, scale, p);
-      const float vf[4] = {bf16_lo(vw.x), bf16_hi(vw.x), bf16_lo(vw.y), bf16_hi(vw.y)};
+      const float vf[4] = {bf16_lo(v1.x), bf16_hi(v1.x), bf16_lo(v1.y), bf16_hi(v1.y)};
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = fmaf(acc[e], scale, p * vf[e]);
     }
@@ -1033,6 +1028,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   A.out[at * DH + d] = __float2bfloat16_rn(y * (Lx == 0.f ? 0.f : 1.f / Lx));   // nothing seen: zeros
 }
 
+constexpr int kMinUnits = 2;
+
 // How a call is laid out: which kernel, tokens per row tile, units, CTAs and the
 // workspace's two parts.
 struct Plan {
@@ -1054,8 +1051,10 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
   auto units_of = [&](int64_t keys) { return (keys + p.unit - 1) / p.unit; };
   const int64_t items = static_cast<int64_t>(batch) * ((n_hkv + p.hw - 1) / p.hw) * ((n_draft + p.tm - 1) / p.tm);
   p.units = items * (units_of(max_len) + (p.few ? 0 : 1));
-  const int64_t most = p.few ? tg::kTreeRowsCtas : kMaxCtas;
-  p.n_cta = static_cast<int>(p.units < 1 ? 1 : p.units < most ? p.units : most);
+  const int64_t most = p.few ? tg::tree_rows_ctas(codes, rows) : kMaxCtas;
+  // few rows: no fewer than kMinUnits units a CTA, since every CTA leaves a partial
+  const int64_t want = p.few ? (p.units + kMinUnits - 1) / kMinUnits : p.units;
+  p.n_cta = static_cast<int>(want < 1 ? 1 : want < most ? want : most);
   p.slots = p.few ? p.n_cta + items : 2 * p.n_cta;
   p.base_bytes = (static_cast<size_t>(batch) + 1) * sizeof(int32_t);
   p.base_bytes = (p.base_bytes + 255) / 256 * 256;

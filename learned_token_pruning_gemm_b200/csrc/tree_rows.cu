@@ -32,25 +32,31 @@ using tg::bf16_hi;
 using tg::bf16_lo;
 using tg::wait;
 
-// NT: tiles of eight rows. Two CTAs share an SM, so that one's start and end of an item pass
-// under the other's work; eight warps each where half of the registers are enough for that,
-// four otherwise, and for bf16 tiles, whose ring would be too short with eight.
-constexpr int warps_of(bool codes, int n_tiles) { return codes && n_tiles == 1 ? 8 : 4; }
+// NT: tiles of eight rows. Several CTAs share an SM, so that one's start and end of an item
+// pass under the others' work; how many goes by registers, then the ring takes the rest of
+// the shared memory.
+struct Shape {
+  int warps, ctas, ring;   // of a CTA; CTAs an SM; tiles
+};
+constexpr Shape shape_of(bool codes, int n_tiles) {
+  if (codes) return n_tiles == 1 ? Shape{8, 2, 5} : n_tiles == 2 ? Shape{4, 3, 7} : Shape{4, 2, 9};
+  return Shape{4, 2, n_tiles == 1 ? 6 : n_tiles == 2 ? 5 : 4};
+}
 template <bool kQ, int NT>
 struct Cfg {
-  static constexpr int kWarps = warps_of(kQ, NT);
+  static constexpr Shape kShape = shape_of(kQ, NT);
+  static constexpr int kWarps = kShape.warps;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kHalf = 16 * kWarps * 128;      // 128-byte rows of a tile (bf16: of one half of it)
   static constexpr int kTile = kHalf * (kQ ? 1 : 2);   // bytes of a K or V tile, at most
-  static constexpr int kRing = kQ ? (NT == 1 ? 5 : NT == 2 ? 10 : 8) : (NT == 4 ? 4 : 5);
+  static constexpr int kRing = kShape.ring;
   static_assert(kRing >= 4, "a unit's tiles are asked for while the one before is in use");
 };
 
 // Places in the walk over a CTA's units.
 struct Cursor {
   int u, u1, b, group, j, nt, len;
-  template <class S>
-  __device__ __forceinline__ void start(const TreeArgs& A, const S& s, int first, int n) {
+  __device__ __forceinline__ void start(const TreeArgs& A, const tg::TreeSeqs& s, int first, int n) {
     u = first;
     u1 = first + n;
     b = tg::sequence_of(A, s, u);
@@ -59,8 +65,7 @@ struct Cursor {
     group = (u - s.base[b]) / nt;
     j = u - s.base[b] - group * nt;
   }
-  template <class S>
-  __device__ __forceinline__ void advance(const TreeArgs& A, const S& s) {
+  __device__ __forceinline__ void advance(const TreeArgs& A, const tg::TreeSeqs& s) {
     ++u;
     if (++j < nt || u >= u1) return;
     j = 0;
@@ -79,13 +84,15 @@ struct RowSmem {
   uint8_t tile[C::kRing][C::kTile];
   uint2 q[C::kWarps][NT][8][32];       // B fragments of each warp's queries
   float2 cg[C::kWarps][8 * NT];        // each row's logit factor and gain, log2 domain
-  int base[tg::kTreeMaxBatch + 1];
-  int len[tg::kTreeMaxBatch];
-  uint8_t dl[tg::kTreeMaxBatch];
   uint64_t full[C::kRing], empty[C::kRing];
   Cursor next;                      // the unit that is loaded next, and
   int issued;                       // the tiles that are on their way or here
   int abort_flag;
+  // behind it, by the batch: first units, cache lengths, drafted tokens
+  __device__ __forceinline__ tg::TreeSeqs seqs(int batch) {
+    int* p = reinterpret_cast<int*>(this + 1);
+    return tg::TreeSeqs{p, p + batch + 1, reinterpret_cast<uint8_t*>(p + 2 * batch + 1)};
+  }
 };
 
 // Loads tiles as far as the ring reaches (K at even places, V at odd ones): tile t needs
@@ -95,6 +102,7 @@ template <bool kQ, int NT>
 __device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<kQ, NT>& S, const CUtensorMap* tm_k,
                                        const CUtensorMap* tm_v, int consumed) {
   using C = Cfg<kQ, NT>;
+  const tg::TreeSeqs Q = S.seqs(A.batch);
   int t = S.issued;
   Cursor c = S.next;
   while (t < consumed + C::kRing && c.u < c.u1) {
@@ -106,7 +114,7 @@ __device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<kQ, NT>& S, co
     const int row = c.b * A.cap + c.j * A.unit, kvh = c.group * A.hw;
     tg::tma_load_3d(S.tile[s], map, &S.full[s], 0, row, kvh);
     if constexpr (!kQ) tg::tma_load_3d(S.tile[s] + C::kHalf, map, &S.full[s], 64, row, kvh);
-    if (t & 1) c.advance(A, S);
+    if (t & 1) c.advance(A, Q);
     ++t;
   }
   S.issued = t;
@@ -170,7 +178,7 @@ __device__ __forceinline__ void cp8(void* dst, const void* src) {
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <int kType, int NT>
-__global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, 2)
+__global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType != TG_BF16, NT>::kShape.ctas)
     tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ TreeArgs A) {
   constexpr bool kQ = kType != TG_BF16;
@@ -194,11 +202,12 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, 2)
   }
   tg::pdl_launch_dependents();
   tg::pdl_wait();   // global memory only from here on
-  const tg::Shares share(A, tg::count_units<C::kThreads>(A, S));
+  const tg::TreeSeqs Q = S.seqs(A.batch);
+  const tg::Shares share(A, tg::count_units<C::kThreads>(A, Q));
   const int n = share.size(blockIdx.x);
   if (n == 0) return;   // uniform: nothing to do here
   Cursor c;
-  c.start(A, S, share.first(blockIdx.x), n);
+  c.start(A, Q, share.first(blockIdx.x), n);
   const bool loader = tid == C::kThreads - 1;   // the last warp's last thread
   if (loader) {
     S.issued = 0;
@@ -213,6 +222,25 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, 2)
   const int hd = warp / A.kw, k0 = 16 * (warp - hd * A.kw);   // head of the item, first key of the unit
   float o[NT][8][4];                  // product t: dims at places 2t, 2t + 1 x rows 2 i4, 2 i4 + 1
   float m[NT][2], l[NT][2];           // of rows 2 i4 and 2 i4 + 1 of every tile
+  // What the thread's keys g and g + 8 of a unit bring besides K and V. Keys behind the last
+  // one read its place and are masked below, as are units without keys for this warp.
+  float next_s[2], next_k[2], next_v[2];
+  auto key_data = [&](const Cursor& t) {
+    const int64_t row0 = static_cast<int64_t>(t.b) * A.cap;
+    const int kvh = min(t.group * A.hw + hd, A.n_hkv - 1);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int64_t row = row0 + min(t.j * A.unit + k0 + g + 8 * x, t.len - 1);
+      next_s[x] = next_k[x] = next_v[x] = 0.f;
+      if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
+      next_s[x] = A.sc[row];
+      if constexpr (kQ) {
+        next_k[x] = A.ks[row * A.n_hkv + kvh];
+        next_v[x] = A.vs[row * A.n_hkv + kvh];
+      }
+    }
+  };
+  key_data(c);
   bool first = true;
   int r = 0;
 #pragma unroll 1
@@ -221,23 +249,12 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, 2)
     const bool head = hd < A.hw && kvh < A.n_hkv;   // else this warp only keeps the ring going
     const int nv = min(A.unit, c.len - c.j * A.unit);
     const bool any = head && k0 < nv;
-    // what the thread's keys g and g + 8 bring besides K and V; keys behind the last one
-    // read its place and are masked below
-    float sk[2], ks[2], vs[2];
-    if (any) {
-      const int64_t row0 = static_cast<int64_t>(c.b) * A.cap + c.j * A.unit;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int64_t row = row0 + min(k0 + g + 8 * x, nv - 1);
-        sk[x] = ks[x] = vs[x] = 0.f;
-        if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
-        sk[x] = A.sc[row];
-        if constexpr (kQ) {
-          ks[x] = A.ks[row * A.n_hkv + kvh];
-          vs[x] = A.vs[row * A.n_hkv + kvh];
-        }
-      }
-    }
+    // the next unit's scores and scales are on their way while this one is worked on
+    const float sk[2] = {next_s[0], next_s[1]}, ks[2] = {next_k[0], next_k[1]};
+    float vs[2] = {next_v[0], next_v[1]};
+    Cursor next = c;
+    next.advance(A, Q);
+    if (u + 1 < n) key_data(next);
     if (first && head) {   // a new item: its queries, and nothing seen yet
       __syncwarp();
       const int64_t row_q = static_cast<int64_t>(c.b) * A.n_draft * A.n_hq + kvh * A.group;
@@ -459,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, 2)
           if (g == 0) *reinterpret_cast<float2*>(pl + 2 * row) = make_float2(m[nt][e], sum);
         }
     }
-    c.advance(A, S);
+    c = next;
   }
   if (loader && S.abort_flag)   // let copies in flight land before the CTA exits
     for (int i = S.issued > C::kRing ? S.issued - C::kRing : 0; i < S.issued; ++i)
@@ -473,8 +490,9 @@ tg_status launch(const TreeArgs& a, cudaStream_t st) {
   if (!tg::tree_cache_map(a, a.kc, 128, kQ, a.unit, a.hw, &tk) ||
       !tg::tree_cache_map(a, a.vc, 128, kQ, a.unit, a.hw, &tv))
     return TG_ERR_CUDA;
-  constexpr int smem = sizeof(RowSmem<kQ, NT>) + 1024;
-  static_assert(smem <= 115712, "half of an SM's shared memory");
+  constexpr int fixed = sizeof(RowSmem<kQ, NT>) + 1024;
+  static_assert((fixed + 1024 + 512) * Cfg<kQ, NT>::kShape.ctas <= 233472, "an SM's shared memory");
+  const int smem = fixed + 9 * a.batch + 8;
   if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_rows_kernel<kType, NT>), smem)) return TG_ERR_CUDA;
   return tg::launch(tree_rows_kernel<kType, NT>, dim3(a.n_cta), dim3(Cfg<kQ, NT>::kThreads), smem, st, 0, tk, tv, a);
 }
@@ -488,7 +506,12 @@ tg_status launch_type(const TreeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-int tg::tree_rows_warps(bool codes, int rows) { return warps_of(codes, rows <= 8 ? 1 : rows <= 16 ? 2 : 4); }
+namespace {
+Shape shape_for(bool codes, int rows) { return shape_of(codes, rows <= 8 ? 1 : rows <= 16 ? 2 : 4); }
+}  // namespace
+
+int tg::tree_rows_ctas(bool codes, int rows) { return 148 * shape_for(codes, rows).ctas; }
+int tg::tree_rows_warps(bool codes, int rows) { return shape_for(codes, rows).warps; }
 
 tg_status tg::launch_tree_rows(const TreeArgs& a, tg_dtype cache_dtype, cudaStream_t stream) {
   if (cache_dtype == TG_BF16) return launch_type<TG_BF16>(a, stream);
