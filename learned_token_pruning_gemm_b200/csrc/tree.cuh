@@ -1,11 +1,13 @@
 // What the kernels of tg_tree_attention share: their arguments, and the split of all work
 // into equal shares.
 //
-// Work units are pieces of `unit` cache rows. An item (a sequence's KV heads, `hw` at a
-// time, and a tile of its rows) has the units of its cache and, in tree_attn_kernel, one
-// more of drafted rows. All units of all items are numbered in a row, and every CTA takes
-// an equal share of that row, so ragged lengths and few heads fill the machine alike.
+// Work units are pieces of `unit` cache rows. An item is a sequence's KV heads, `hw` at a
+// time, and a tile of its query rows; it has the units of its cache. All units of all items
+// are numbered in a row, and every CTA takes an equal share of that row, so ragged lengths
+// and few heads fill the machine alike.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 
@@ -32,7 +34,6 @@ struct TreeArgs {
   int group, group_inv;   // query heads per KV head; ceil(2^16 / group)
   int tm;             // tokens of a row tile
   int unit;           // keys of a unit
-  int few;            // tree_rows_kernel: units of the cache only
   int hw, kw;         // KV heads of an item, and warps that share a head's keys of a unit
   int n_cta;
   int* status;
@@ -53,10 +54,6 @@ __device__ __forceinline__ int2 seq_lens(const TreeArgs& A, int b, bool record) 
 }
 __device__ __forceinline__ int row_tiles(const TreeArgs& A, int dl) { return (dl + A.tm - 1) / A.tm; }
 __device__ __forceinline__ int key_units(const TreeArgs& A, int keys) { return (keys + A.unit - 1) / A.unit; }
-// units of an item: those of the cache, then those of the drafted rows
-__device__ __forceinline__ int item_units(const TreeArgs& A, int len, int dl) {
-  return key_units(A, len) + (A.few ? 0 : key_units(A, dl));
-}
 __device__ __forceinline__ int head_groups(const TreeArgs& A) { return (A.n_hkv + A.hw - 1) / A.hw; }
 // Where the maxima and sums of the partials begin.
 __device__ __forceinline__ float* part_ml(const TreeArgs& A, int rows, int dh) {
@@ -97,7 +94,7 @@ __device__ __forceinline__ int count_units(const TreeArgs& A, const TreeSeqs& S)
     const int2 l = seq_lens(A, b, blockIdx.x == 0);
     S.len[b] = l.x;
     S.dl[b] = static_cast<uint8_t>(l.y);
-    S.base[b + 1] = l.y ? head_groups(A) * row_tiles(A, l.y) * item_units(A, l.x, l.y) : 0;
+    S.base[b + 1] = l.y ? head_groups(A) * row_tiles(A, l.y) * key_units(A, l.x) : 0;
   }
   __syncthreads();
   if (tid < 32) {
@@ -143,6 +140,36 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status
 
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// Four codes (bytes of w; int8 ones with the sign bit flipped) to four fp16 values, exactly.
+template <bool kE4m3>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kE4m3) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {   // 1024 + (code + 128) has the code's bits as its last eight; then less 1152
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
+  }
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float scale) {
+  return pack_f16x2(bf16_lo(w) * scale, bf16_hi(w) * scale);
+}
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 
 // The map of a K or V cache, rows of dh (bf16: halves of 64), 128-byte swizzle (64-byte for
 // 64-byte rows): boxes of `keys` rows of `heads` KV heads, one head after the other.

@@ -6,42 +6,30 @@
 // is set in tree_mask[b][t]:
 //     z_j = q . k_j / (sqrt(dh) tau_h) + g_h s_j,   O = sum_j softmax_j(z) v_j.
 //
-// The cache is read once per KV head and serves all drafted tokens and query heads of
-// the group: with R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product
-// and back, so rows are packed into M = 128 tiles (row r is token r / G, head r % G)
-// and both products run on the tensor cores with accumulators in TMEM. Up to some 100
-// rows the work is bound by the bytes of the cache; beyond, by the products.
-//
-// Work units are tiles of 128 keys. The items (sequence, KV head, row tile) have
-// ceil(len / 128) cache tiles and one tile of drafted rows each; all units of all items
-// are numbered in a row and every CTA (one per SM) takes an equal share of that row, so
-// ragged lengths and few heads fill the machine alike. An item that lies inside one
-// CTA's share is finished there; one that is cut leaves a partial (max, sum, O) per
-// CTA, which a second kernel adds up in CTA order: results do not depend on timing.
+// The cache is read once per KV head and serves all drafted tokens and query heads of the
+// group: with R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product and back.
+// Here the rows are packed into M = 128 tiles (row r is token r / G, head r % G) and both
+// products run on the tensor cores with accumulators in TMEM; up to 32 rows of head dim 128
+// take the kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128
+// cache rows; what a CTA has of an item it leaves as a partial (max, sum, O), and the
+// kernel at the end adds the partials up in CTA order, so results do not depend on timing,
+// and brings in the drafted rows that each token sees.
 //
 // Per CTA, pipelines run over the units:
-//   warp 0       K tiles by TMA (bf16: into the operand ring; codes: K and V codes into
-//                a raw ring). A tile that ends inside (the last of a cache, the drafted
-//                rows) is copied row by row with the rest of it zero.
+//   warp 0       K tiles by TMA (bf16: into the operand ring; codes: K and V codes into a
+//                raw ring). A bf16 tile that ends inside is copied row by row.
 //   warp 3       V tiles likewise (bf16 cache)
 //   warp 2       the rows' queries, and per key: score, scales (a ring of four tiles)
-//   warps 12-19  codes only: widen the raw tiles into bf16 operand tiles. Codes are exact
-//                in bf16, so scales are applied in fp32: the key's to the logit, the
-//                value's to the weight.
-//   warp 1       MMA issuer (one thread): S_0, .., PV_0, S_n, PV_1, ...; S_j = Q K_j^T into
-//                one of kS 128-column TMEM buffers, O += P_j V_j with P_j read from TMEM
-//                (it overwrites S_j) and V_j as an MN-major shared-memory operand.
-//   warps 4-11   softmax, 16 rows each, those with rows only: logits in the log2 domain,
-//                masks in the tiles that need them, a running reference that moves only
-//                when a logit exceeds it by more than 2^8 (O is then rescaled in TMEM), P in
-//                bf16. The row sum adds the rounded weights, so that a key which dominates
-//                its row gives its value exactly.
-// The parity waits are exact for the reasons given at the gated attention's kernel:
-// S_g is issued after PV_{g - kS}, and a softmax warp is never more than kS tiles ahead.
-//
-// Values of drafted rows that are not finite never enter the products (0 * inf would
-// reach tokens that do not see the row): they are zero in the operand tile, their rows
-// are noted, and the epilogue adds them to the rows that see them.
+//   warps 12-19  codes only: widen the raw tiles into fp16 operand tiles. Codes are exact in
+//                fp16, so scales are applied in fp32, to logits and weights.
+//   warp 1       MMA issuer (one thread): S_0, .., PV_0, S_n, PV_1, ...; S_j = Q K_j^T into one
+//                of kS 128-column TMEM buffers, O += P_j V_j with P_j read from TMEM (it
+//                overwrites S_j) and V_j as an MN-major shared-memory operand.
+//   warps 4-11   softmax, 16 rows each, those with rows only: logits in the log2 domain less
+//                the row's running reference, which moves only when one exceeds it by more
+//                than it may (O is then rescaled in TMEM).
+// The parity waits are exact for the reasons given at the gated attention's kernel: S_g is
+// issued after PV_{g - kS}, and a softmax warp is never more than kS tiles ahead.
 #include <type_traits>
 
 #include "tree.cuh"
@@ -58,7 +46,6 @@ constexpr int kBM = 128;           // rows of a row tile
 constexpr int kBN = 128;           // keys of a unit
 constexpr int kMaxDraft = 64;
 constexpr int kKeyStages = 4;
-constexpr int kBadRing = 8;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kConvWarps = 8;
 constexpr int kMaxCtas = 148;      // one per SM
@@ -70,8 +57,8 @@ struct Cfg {
   static constexpr int kHalves = DH / 64;
   static constexpr int kS = kQ ? 2 : 3;                                  // S/P buffers in TMEM
   static constexpr int kK = kQ ? (DH == 128 ? 2 : 3) : (DH == 128 ? 3 : 5);   // K operand tiles
-  static constexpr int kV = kQ ? (DH == 128 ? 1 : 2) : (DH == 128 ? 2 : 4);   // V operand tiles
-  static constexpr int kRaw = kQ ? (DH == 128 ? 4 : 8) : 1;              // raw tiles of codes
+  static constexpr int kV = kQ ? 2 : DH == 128 ? 2 : 4;                  // V operand tiles
+  static constexpr int kRaw = kQ ? (DH == 128 ? 3 : 8) : 1;              // raw tiles of codes
   static constexpr int kRawBytes = kQ ? kBN * DH : 16;
   static constexpr int kThreads = 128 + kSoftmaxWarps * 32 + (kQ ? kConvWarps * 32 : 0);
   static constexpr int kFullArrivals = kQ ? kConvWarps : 1;              // a K or V tile is ready
@@ -84,12 +71,11 @@ struct TreeSmem {
   uint8_t k[C::kK][C::kHalves][kHalfBytes];
   uint8_t v[C::kV][C::kHalves][kHalfBytes];
   uint8_t raw[C::kRaw][C::kRawBytes];
-  float key[kKeyStages][kQ ? 4 : 1][kBN];   // score, then (codes) key scale, value scale and its inverse
-  uint16_t bad[kBadRing][4];                // drafted rows with values that are not finite, 16 rows a word
+  float key[kKeyStages][kQ ? 4 : 1][kBN];   // score, then (codes) key scale, log2 of the value scale, its inverse
   int base[tg::kTreeMaxBatch + 1];
   int len[tg::kTreeMaxBatch];
   uint8_t dl[tg::kTreeMaxBatch];
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_ready, q_empty;   // landed; in fp16 (codes); every S of the item done
   uint64_t k_full[C::kK], k_empty[C::kK];
   uint64_t v_full[C::kV], v_empty[C::kV];
   uint64_t raw_full[C::kRaw], raw_empty[C::kRaw];
@@ -109,14 +95,13 @@ __device__ __forceinline__ bool value_turn(int i, int n) {
 }
 
 // Walks a CTA's units in order: the unit's sequence, KV head, row tile and place among its
-// item's units, those of the cache before the one of the drafted rows.
+// item's units.
 struct Cursor {
-  int u, u1, b, item, n_items, kvh, mt, j, nk, nt, len, dl;
+  int u, u1, b, item, n_items, kvh, mt, j, nt, len, dl;
   __device__ __forceinline__ void load_seq(const TreeArgs& A, const tg::TreeSeqs& s) {
     len = s.len[b];
     dl = s.dl[b];
-    nk = (len + kBN - 1) / kBN;
-    nt = nk + 1;
+    nt = (len + kBN - 1) / kBN;
     n_items = A.n_hkv * tg::row_tiles(A, dl);
   }
   __device__ __forceinline__ void split_item(const TreeArgs& A) {
@@ -145,8 +130,7 @@ struct Cursor {
     }
     split_item(A);
   }
-  __device__ __forceinline__ bool draft() const { return j == nk; }
-  __device__ __forceinline__ int keys() const { return draft() ? dl : min(kBN, len - j * kBN); }
+  __device__ __forceinline__ int keys() const { return min(kBN, len - j * kBN); }
   // units of the current item from here on within the CTA's share
   __device__ __forceinline__ int run() const { return min(nt - j, u1 - u); }
 };
@@ -154,10 +138,9 @@ struct Cursor {
 // What the copy of one unit needs to know of it.
 struct Tile {
   int b, kvh, j, nv;
-  bool draft;
 };
 __device__ __forceinline__ Tile tile_of(const Cursor& c) {
-  return Tile{c.b, c.kvh, c.j, c.keys(), c.draft()};
+  return Tile{c.b, c.kvh, c.j, c.keys()};
 }
 
 // 16 bytes global -> shared, or 16 zero bytes when !ok (src is not read then)
@@ -216,95 +199,24 @@ __device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Two codes (bytes of a and b, as __byte_perm selects them into the low bytes of the two
-// halves for int8 and into the high ones for e4m3) to two bf16 values, exactly.
-// int8: with the low seven bits as mantissa over 128, (128 + low) - (128 or 256 by the
-// sign bit). e4m3: its exponent and mantissa bits sit in place in a bf16 whose exponent
-// is 120 too small, which a product with 2^120 restores (subnormals too).
-template <bool kE4m3>
-__device__ __forceinline__ uint32_t widen2(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  if constexpr (kE4m3) {
-    const uint32_t x = __byte_perm(a, b, sel);   // the codes in the high bytes
-    const uint32_t y = (x & 0x80008000u) | ((x & 0x7F007F00u) >> 4);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(y), "r"(0x7B807B80u));
-  } else {
-    const uint32_t x = __byte_perm(a, b, sel);   // the codes in the low bytes
-    asm("sub.rn.bf16x2 %0, %1, %2;"
-        : "=r"(d)
-        : "r"((x & 0x007F007Fu) | 0x43004300u), "r"((x & 0x00800080u) | 0x43004300u));
-  }
-  return d;
+// acc += the low (lo) or high (hi) bf16 half of a packed pair, widened exactly
+__device__ __forceinline__ void add_bf16_lo(float& acc, uint32_t u) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, l, %0;\n\t}" : "+f"(acc) : "r"(u));
 }
-
-// A bf16 pair with values that are not finite replaced by 0; *bad is set if there were any.
-__device__ __forceinline__ uint32_t finite2(uint32_t u, bool* bad) {
-  if ((u & 0x7F80u) == 0x7F80u) u &= 0xFFFF0000u, *bad = true;
-  if ((u & 0x7F800000u) == 0x7F800000u) u &= 0x0000FFFFu, *bad = true;
-  return u;
+__device__ __forceinline__ void add_bf16_hi(float& acc, uint32_t u) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, h, %0;\n\t}" : "+f"(acc) : "r"(u));
 }
-
-// Rows r0, r0 + step, .. below r1 of the drafted keys of (b, kvh) into an operand tile.
-template <int DH>
-__device__ __noinline__ void draft_keys(const TreeArgs& A, int b, int kvh, int dl, uint8_t* dst, int r0,
-                                        int r1, int lane) {
-  constexpr int kC = DH / 8;   // 16-byte columns of a row
-  r1 = min(r1, dl);
-#pragma unroll 1
-  for (int i = r0 * kC + lane; i < r1 * kC; i += 32) {
-    const int r = i / kC, cc = i % kC;
-    const int64_t hr = (static_cast<int64_t>(b) * A.n_draft + r) * A.n_hkv + kvh;
-    if (!tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hkv, A.status)) continue;
-    cp16(tg::smem_u32(dst) + tile_off(r, cc), A.kd + hr * DH + 8 * cc, true);
-  }
-  cp_wait_all();
+__device__ __forceinline__ void cp4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tg::smem_u32(dst)), "l"(src) : "memory");
 }
+template <int N>
+__device__ __forceinline__ void cp_wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// The same for drafted values: zeros behind the last one up to a multiple of 16 rows and
-// in place of what is not finite. Rows r0 .. r1 - 1 lie in 16-row words r0 / 16, ...
-template <int DH>
-__device__ __noinline__ void draft_values(const TreeArgs& A, int b, int kvh, int dl, uint8_t* dst,
-                                          uint16_t* bad, int r0, int r1, int lane) {
-  constexpr int kC = DH / 8;
-  for (int w = r0; w < r1; w += 16) {   // one word of `bad` at a time
-    uint32_t word = 0;
-#pragma unroll 2
-    for (int i = w * kC + lane; i < (w + 16) * kC; i += 32) {
-      const int r = i / kC, cc = i % kC;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      const int64_t hr = (static_cast<int64_t>(b) * A.n_draft + r) * A.n_hkv + kvh;
-      if (r < dl && tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hkv, A.status))
-        x = *reinterpret_cast<const uint4*>(A.vd + hr * DH + 8 * cc);
-      bool inf = false;
-      x.x = finite2(x.x, &inf);
-      x.y = finite2(x.y, &inf);
-      x.z = finite2(x.z, &inf);
-      x.w = finite2(x.w, &inf);
-      if (inf) word |= 1u << (r - w);
-      *reinterpret_cast<uint4*>(dst + tile_off(r, cc)) = x;
-    }
-    word = __reduce_or_sync(0xFFFFFFFFu, word);
-    if (lane == 0) bad[w >> 4] = static_cast<uint16_t>(word);
-  }
-}
-
-// The values that are not finite of the drafted rows in `rows` join a token's output
-// (out, or its partial) at this thread's elements: columns cq and cq + 1 of each 8.
-template <int DH>
-__device__ __noinline__ void add_infinite(const TreeArgs& A, int b, int kvh, uint64_t rows,
-                                          __nv_bfloat16* out, float* part, int cq) {
-  for (; rows; rows &= rows - 1) {
-    const int r = __ffsll(static_cast<long long>(rows)) - 1;
-    const __nv_bfloat16* v = A.vd + ((static_cast<int64_t>(b) * A.n_draft + r) * A.n_hkv + kvh) * DH + cq;
-#pragma unroll 1
-    for (int i = 0; i < DH / 4; ++i) {
-      const int at = 8 * (i >> 1) + (i & 1);
-      const float x = __bfloat162float(v[at]);
-      if (isfinite(x)) continue;
-      if (out) out[at] = __float2bfloat16_rn(__bfloat162float(out[at]) + x);
-      else part[at] += x;
-    }
-  }
+// Instruction descriptor of an fp16 (kF16) or bf16 product: the format fields are 0 for fp16.
+template <bool kF16>
+constexpr uint32_t idesc(int M, int N, bool b_mn) {
+  return tg::idesc_bf16_f32(M, N, false, b_mn) & (kF16 ? ~((1u << 7) | (1u << 10)) : ~0u);
 }
 
 template <int DH, int kType>
@@ -324,6 +236,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
 
   if (tid == 0) {
     tg::mbar_init(&S.q_full, 1);
+    tg::mbar_init(&S.q_ready, n_act);
     tg::mbar_init(&S.q_empty, 1);
     for (int s = 0; s < C::kK; ++s) {
       tg::mbar_init(&S.k_full[s], C::kFullArrivals);
@@ -381,7 +294,8 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     uint64_t* empty = val ? S.v_empty : S.k_empty;
     const CUtensorMap* map = val ? &tm_v : &tm_k;
     const __nv_bfloat16* cache = reinterpret_cast<const __nv_bfloat16*>(val ? A.vc : A.kc);
-    int n_draft = 0, g = 0;
+    int g = 0;
+#pragma unroll 1
     for (; g < n; ++g, c.advance(A, Q)) {
       const int s = g % n_st;
       if (g >= n_st &&
@@ -389,22 +303,16 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         break;
       uint8_t* dst = val ? S.v[s % C::kV][0] : S.k[s % C::kK][0];
       const int nv = c.keys();
-      if (c.draft() || nv < kBN) {
-        if (!c.draft()) {
-          const int r1 = val ? (nv + 15) & ~15 : nv;
+      if (nv < kBN) {   // V: rows behind the end are zero up to a multiple of 16, as P's columns are
+        const int r1 = val ? (nv + 15) & ~15 : nv;
 #pragma unroll 1
-          for (int i = lane; i < r1 * kC; i += 32) {
-            const int r = i / kC, cc = i % kC;
-            const int64_t hr = (static_cast<int64_t>(c.b) * A.cap + c.j * kBN + min(r, nv - 1)) * A.n_hkv + c.kvh;
-            const bool ok = r < nv && tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.cap * A.n_hkv, A.status);
-            cp16(tg::smem_u32(dst) + tile_off(r, cc), cache + hr * DH + 8 * cc, ok);
-          }
-          cp_wait_all();
-        } else if (val) {
-          draft_values<DH>(A, c.b, c.kvh, c.dl, dst, S.bad[n_draft % kBadRing], 0, kMaxDraft, lane);
-        } else {
-          draft_keys<DH>(A, c.b, c.kvh, c.dl, dst, 0, kMaxDraft, lane);
+        for (int i = lane; i < r1 * kC; i += 32) {
+          const int r = i / kC, cc = i % kC;
+          const int64_t hr = (static_cast<int64_t>(c.b) * A.cap + c.j * kBN + min(r, nv - 1)) * A.n_hkv + c.kvh;
+          const bool ok = r < nv && tg::in_bounds(hr, static_cast<int64_t>(A.batch) * A.cap * A.n_hkv, A.status);
+          cp16(tg::smem_u32(dst) + tile_off(r, cc), cache + hr * DH + 8 * cc, ok);
         }
+        cp_wait_all();
         tg::fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) tg::mbar_arrive(&full[s]);
@@ -415,7 +323,6 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         for (int h = 0; h < C::kHalves; ++h)
           tg::tma_load_3d(dst + h * kHalfBytes, map, &full[s], 64 * h, row, c.kvh);
       }
-      if (c.draft()) ++n_draft;
       __syncwarp();
     }
     if (S.abort_flag && lane == 0)   // let copies in flight land before the CTA exits
@@ -436,7 +343,6 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           c.advance(A, Q);
         }
         const Tile t = val && i < 2 * n - 1 ? prev : cur;
-        if (t.draft) continue;   // drafted rows are bf16: the converters read them
         const int s = r % C::kRaw;
         if (r >= C::kRaw && !wait(&S.raw_empty[s], ((r / C::kRaw) - 1) & 1, A.status, &S.abort_flag)) break;
         tg::mbar_arrive_expect_tx(&S.raw_full[s], C::kRawBytes);
@@ -451,79 +357,75 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     __syncwarp();
   } else if (warp == 2) {
     // ---------------- queries, and what each key brings besides K and V ----------------
-    constexpr int kN = kQ ? 3 : 1;
-    constexpr int kAhead = 3;
-    Cursor la = c;   // loads run three tiles ahead
-    float x[kAhead + 1][kN][4];
+    // The keys' data by small asynchronous copies into their ring, kLag tiles before they are
+    // handed on. Keys behind the end read the last one's place: they are masked.
+    constexpr int kLag = kKeyStages - 1;
+    Cursor la = c;
     int n_q = 0;
+    auto queries = [&](const Cursor& t) {
+      if (lane == 0) {
+        tg::mbar_arrive_expect_tx(&S.q_full, C::kHalves * rows * 128);
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          tg::tma_load_3d(S.q[h], &tm_q, &S.q_full, 64 * h, t.kvh * A.group, t.b * A.n_draft + t.mt * A.tm);
+      }
+      ++n_q;
+      __syncwarp();
+    };
+    queries(c);
 #pragma unroll 1
-    for (int g = -kAhead; g < n; ++g) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a)
-#pragma unroll
-        for (int e = 0; e < kN; ++e)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[a][e][i] = x[a + 1][e][i];
-      if (g + kAhead < n) {
-        const bool draft = la.draft();
-        const int nv = la.keys();
-        const int64_t row0 = draft ? static_cast<int64_t>(la.b) * A.n_draft
-                                   : static_cast<int64_t>(la.b) * A.cap + la.j * kBN;
-        const int64_t n_rows = static_cast<int64_t>(A.batch) * (draft ? A.n_draft : A.cap);
-        const float* sc = (draft ? A.sd : A.sc) + row0;
+    for (int g = 0; g < n + kLag; ++g) {
+      if (g < n) {
+        const int s = g % kKeyStages;
+        if (g >= kKeyStages &&
+            !all_alive(wait(&S.b_empty[s], ((g / kKeyStages) - 1) & 1, A.status, &S.abort_flag)))
+          break;
+        const int64_t row0 = static_cast<int64_t>(la.b) * A.cap + la.j * kBN;
+        const int last = la.keys() - 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int j = lane + 32 * i;
-          const bool there = j < nv && tg::in_bounds(row0 + j, n_rows, A.status);
-          x[kAhead][0][i] = there ? sc[j] : 0.f;
+          const int64_t row = row0 + min(j, last);
+          if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
+          cp4(&S.key[s][0][j], A.sc + row);
           if constexpr (kQ) {
-            const int64_t hr = (row0 + j) * A.n_hkv + la.kvh;
-            x[kAhead][1][i] = there && !draft ? A.ks[hr] : 1.f;
-            x[kAhead][2][i] = there && !draft ? A.vs[hr] : 1.f;
+            cp4(&S.key[s][1][j], A.ks + row * A.n_hkv + la.kvh);
+            cp4(&S.key[s][2][j], A.vs + row * A.n_hkv + la.kvh);
           }
         }
         la.advance(A, Q);
       }
-      if (g < 0) continue;
-      if (g == 0 || c.j == 0) {   // a new item: its queries, once the last one's S are done
-        if (n_q > 0 && !all_alive(wait(&S.q_empty, (n_q - 1) & 1, A.status, &S.abort_flag))) break;
-        if (lane == 0) {
-          tg::mbar_arrive_expect_tx(&S.q_full, C::kHalves * rows * 128);
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            tg::tma_load_3d(S.q[h], &tm_q, &S.q_full, 64 * h, c.kvh * A.group,
-                            c.b * A.n_draft + c.mt * A.tm);
-        }
-        ++n_q;
-        __syncwarp();
+      cp_commit();
+      if (g < kLag) continue;
+      if (g > kLag && c.j == 0) {   // a new item: its queries, once the last one's S are done
+        if (!all_alive(wait(&S.q_empty, (n_q - 1) & 1, A.status, &S.abort_flag))) break;
+        queries(c);
       }
-      const int s = g % kKeyStages;
-      if (g >= kKeyStages &&
-          !all_alive(wait(&S.b_empty[s], ((g / kKeyStages) - 1) & 1, A.status, &S.abort_flag)))
-        break;
+      cp_wait_group<kLag>();
+      const int s = (g - kLag) % kKeyStages;
+      if constexpr (kQ) {
+        // The value scale v joins the logit as log2 v (see the softmax); where it is 0 all codes
+        // are, and any v small enough not to lead will do.
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = lane + 32 * i;
-        S.key[s][0][j] = x[0][0][i];
-        if constexpr (kQ) {
-          // a value scale of 0 has codes 0: any weight will do, and 1 keeps the row sum
-          const float vs = x[0][2][i] == 0.f ? 1.f : x[0][2][i];
-          S.key[s][1][j] = x[0][1][i];
-          S.key[s][2][j] = vs;
-          S.key[s][3][j] = 1.f / vs;
+        for (int i = 0; i < 4; ++i) {
+          const int j = lane + 32 * i;
+          const float v = S.key[s][2][j], vs = v == 0.f ? 0x1p-40f : v;
+          S.key[s][2][j] = __log2f(vs);
+          S.key[s][3][j] = __frcp_rn(vs);
         }
       }
       tg::mbar_arrive(&S.b_full[s]);
       c.advance(A, Q);
     }
+    cp_wait_all();
     if (S.abort_flag && n_q > 0 && lane == 0)
       wait(&S.q_full, (n_q - 1) & 1, A.status, nullptr);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
-      constexpr uint32_t idesc_s = tg::idesc_bf16_f32(kBM, kBN, false, false);
-      constexpr uint32_t idesc_o = tg::idesc_bf16_f32(kBM, DH, false, true);
+      constexpr uint32_t idesc_s = idesc<kQ>(kBM, kBN, false);
+      constexpr uint32_t idesc_o = idesc<kQ>(kBM, DH, true);
       const uint32_t q0 = tg::smem_u32(S.q[0]);
       auto issue_s = [&](int g) -> bool {
         const int s = g % C::kK;
@@ -545,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       int g0 = 0;
       for (int seg = 0; g0 < n && alive; ++seg) {
         const int nt = c.run();
-        alive = wait(&S.q_full, seg & 1, A.status, &S.abort_flag);
+        alive = wait(kQ ? &S.q_ready : &S.q_full, seg & 1, A.status, &S.abort_flag);
         for (int j = 0; j < C::kS && j < nt && alive; ++j) alive = issue_s(g0 + j);
         if (alive && nt <= C::kS) tg::mma_commit(&S.q_empty);   // every S of the item issued
         for (int j = 0; j < nt && alive; ++j) {
@@ -558,6 +460,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           tg::tc_fence_after();
           const uint32_t v0 = tg::smem_u32(S.v[s][0]);
           const int steps = (c.keys() + 15) / 16;   // rows of V behind these are not set
+#pragma unroll 1
           for (int kk = 0; kk < steps; ++kk) {
             const uint64_t bdesc = tg::smem_desc_sw128(v0 + kk * 16 * 128, kHalfBytes, 1024);
             tg::mma_bf16_ts(tmem + kColO, tmem + 128u * (g % C::kS) + kk * 8, bdesc, idesc_o, (j | kk) != 0);
@@ -583,25 +486,55 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       const int r2[2] = {row0 + (lane >> 2), row0 + (lane >> 2) + 8};
       const int cq = 2 * (lane & 3);
       const uint32_t lane_base = static_cast<uint32_t>(row0) << 16;
-      float ch[2], gh[2], m[2], l[2];
-      uint64_t see[2];
-      int seg = 0, n_draft = 0;
-      bool first = true, whole = false, alive = true;
+      float ch[2], gh[2], m[2], l[2], nm[2], most[2];
+      int seg = 0;
+      bool first = true, alive = true;
+#pragma unroll 1
       for (int g = 0; g < n; ++g) {
-        if (first) {
+        if (first) {   // a new item
+          float up[2] = {1.f, 1.f};
+          if constexpr (kQ) {
+            // The queries to fp16, two lanes a row: the row is multiplied by the power of two that
+            // brings its largest value (exponent field x) to [2^8, 2^9), so that values down to
+            // 2^-22 of it stay exact; the inverse joins the row's factor.
+            alive = wait(&S.q_full, seg & 1, A.status, &S.abort_flag);
+            if (!all_alive(alive)) break;
+            constexpr int kPer = DH / 16;   // 16-byte columns a lane
+            const int row = row0 + (lane >> 1);
+            uint8_t* q = S.q[0] + row * 128 + (DH == 128 ? (lane & 1) * kHalfBytes : 0);
+            const int c0 = DH == 128 ? 0 : 4 * (lane & 1);
+            uint4 x[kPer];
+            uint32_t mx = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              x[k] = *reinterpret_cast<const uint4*>(q + (((c0 + k) ^ (row & 7)) << 4));
+              mx = tg::max_u16x2(mx, tg::max_u16x2(tg::max_u16x2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu),
+                                                   tg::max_u16x2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu)));
+            }
+            mx = tg::max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+            const int xp = max(static_cast<int>(max(mx >> 16, mx & 0xFFFFu) >> 7), 9);
+            const float down = __int_as_float((262 - xp) << 23), inv = __int_as_float((xp - 8) << 23);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+              *reinterpret_cast<uint4*>(q + (((c0 + k) ^ (row & 7)) << 4)) =
+                  make_uint4(tg::bf16x2_to_f16x2(x[k].x, down), tg::bf16x2_to_f16x2(x[k].y, down),
+                             tg::bf16x2_to_f16x2(x[k].z, down), tg::bf16x2_to_f16x2(x[k].w, down));
+            up[0] = __shfl_sync(0xFFFFFFFFu, inv, 2 * (lane >> 2));
+            up[1] = __shfl_sync(0xFFFFFFFFu, inv, 2 * (lane >> 2) + 16);
+            tg::fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) tg::mbar_arrive(&S.q_ready);
+          }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int tok = tg::token_of(A, r2[e]), hq = c.kvh * A.group + r2[e] - tok * A.group;
-            ch[e] = kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]);
+            ch[e] = kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]) * up[e];
             gh[e] = A.gain[hq] * kLog2e;
-            const int t = c.mt * A.tm + tok;   // tokens behind the last see nothing
-            see[e] = t < c.dl
-                         ? static_cast<uint64_t>(A.mask[static_cast<int64_t>(c.b) * A.n_draft + t]) : 0;
-            if (c.dl < 64) see[e] &= (1ull << c.dl) - 1;
-            m[e] = -INFINITY;
+            m[e] = -INFINITY;      // nothing seen: logits as they are, and any of them moves m
+            nm[e] = 0.f;
+            most[e] = -INFINITY;
             l[e] = 0.f;
           }
-          whole = c.j == 0;
         }
         const int s = g % kKeyStages;
         const uint32_t sbuf = tmem + lane_base + 128u * (g % C::kS);
@@ -611,73 +544,85 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         tg::tc_fence_after();
         // 64 keys at a time: half the registers and half the code
         const int nv = c.keys();
-        const bool draft = c.draft();
-        bool fresh = first;   // nothing of this item in O or P yet
 #pragma unroll 1
         for (int hf = 0; 64 * hf < nv; ++hf) {
           const float* key = S.key[s][0] + 64 * hf + cq;
           float z[32];
-          {
-            uint32_t u[32];
-            tg::tmem_ld_16x256b_x8(sbuf + 64u * hf, u);
-            tg::tmem_ld_wait();
+#pragma unroll 1
+          for (int pass = 0;; ++pass) {   // twice where the reference moves, never more
+            {
+              uint32_t u[32];
+              tg::tmem_ld_16x256b_x8(sbuf + 64u * hf, u);
+              tg::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 sk = *reinterpret_cast<const float2*>(key + 8 * i);
-              float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
-                            __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
-              if constexpr (kQ) {
-                const float2 ks = *reinterpret_cast<const float2*>(key + kBN + 8 * i);
-                fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
-                fmul2(x[2], x[3], x[2], x[3], ks.x, ks.y);
+              for (int i = 0; i < 8; ++i) {
+                const float2 sk = *reinterpret_cast<const float2*>(key + 8 * i);
+                float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                              __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
+                float lx = 0.f, ly = 0.f;
+                if constexpr (kQ) {
+                  const float2 ks = *reinterpret_cast<const float2*>(key + kBN + 8 * i);
+                  const float2 lv = *reinterpret_cast<const float2*>(key + 2 * kBN + 8 * i);
+                  fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
+                  fmul2(x[2], x[3], x[2], x[3], ks.x, ks.y);
+                  lx = lv.x, ly = lv.y;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float b0 = nm[e], b1 = nm[e];
+                  if constexpr (kQ) fadd2(b0, b1, lx, ly, nm[e], nm[e]);
+                  ffma2(b0, b1, gh[e], gh[e], sk.x, sk.y, b0, b1);
+                  ffma2(z[4 * i + 2 * e], z[4 * i + 2 * e + 1], x[2 * e], x[2 * e + 1], ch[e], ch[e], b0, b1);
+                }
               }
-              float b0, b1;
-              fmul2(b0, b1, gh[0], gh[0], sk.x, sk.y);
-              ffma2(z[4 * i], z[4 * i + 1], x[0], x[1], ch[0], ch[0], b0, b1);
-              fmul2(b0, b1, gh[1], gh[1], sk.x, sk.y);
-              ffma2(z[4 * i + 2], z[4 * i + 3], x[2], x[3], ch[1], ch[1], b0, b1);
             }
-          }
-          if (draft || nv - 64 * hf < 64) {   // what is not there, or not seen
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint64_t there = draft ? see[e] : (1ull << (nv - 64 * hf)) - 1;
-              const uint32_t w[2] = {static_cast<uint32_t>(there) >> cq,
-                                     static_cast<uint32_t>(there >> 32) >> cq};
+            if (nv - 64 * hf < 64) {   // keys that are not there
 #pragma unroll
               for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
-                  if (!((w[i >> 2] >> (8 * (i & 3) + f)) & 1)) z[4 * i + 2 * e + f] = -INFINITY;
+                  if (64 * hf + 8 * i + cq + f >= nv) z[4 * i + f] = z[4 * i + 2 + f] = -INFINITY;
             }
-          }
-          // The reference of the weights is a whole number at or above the largest logit
-          // when it is set, so that moving it scales by an exact power of two; it moves
-          // only when a logit exceeds it by more than 2^8.
-          float alpha[2] = {1.f, 1.f}, nm[2];
-          bool rescale = false;
+            // A row's reference is a whole number at or above its largest logit (fp16 weights: 6
+            // below that, to keep small ones exact) when it is set, so that moving it scales by an
+            // exact power of two; it moves when a logit exceeds it by 2^8 more, so that bf16 weights
+            // stay below 2^8 and fp16 ones below 2^14.
+            constexpr float kLift = kQ ? 6.f : 0.f;
+            float mx[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float t0 = fmaxf(z[2 * e], z[2 * e + 1]), t1 = fmaxf(z[4 + 2 * e], z[5 + 2 * e]);
+            for (int e = 0; e < 2; ++e) {
+              float t0 = fmaxf(z[2 * e], z[2 * e + 1]), t1 = fmaxf(z[4 + 2 * e], z[5 + 2 * e]);
 #pragma unroll
-            for (int i = 2; i < 8; i += 2) {
-              t0 = fmax3(t0, z[4 * i + 2 * e], z[4 * i + 2 * e + 1]);
-              t1 = fmax3(t1, z[4 * i + 4 + 2 * e], z[4 * i + 5 + 2 * e]);
+              for (int i = 2; i < 8; i += 2) {
+                t0 = fmax3(t0, z[4 * i + 2 * e], z[4 * i + 2 * e + 1]);
+                t1 = fmax3(t1, z[4 * i + 4 + 2 * e], z[4 * i + 5 + 2 * e]);
+              }
+              mx[e] = fmaxf(t0, t1);
             }
-            float mt = fmaxf(t0, t1);
-            mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 1));
-            mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2));
-            if (fresh) {
-              m[e] = ceilf(mt);
-            } else if (mt > m[e] + tg::kRescaleThreshold) {
-              mt = ceilf(mt);
-              alpha[e] = tg::exp2_approx(m[e] - mt);
-              m[e] = mt;
-              rescale = true;
+            if (pass) {
+              // No logit exceeds its row's reference by more than it may now, but by rounding one
+              // may that is so large that its last place does (rows behind the last hold
+              // anything): it is brought down.
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (z[i] > kLift + tg::kRescaleThreshold) z[i] = kLift + tg::kRescaleThreshold;
+              break;
             }
-            nm[e] = m[e] == -INFINITY ? 0.f : -m[e];   // a row that has seen nothing: weights 0
-          }
-          if (__any_sync(0xFFFFFFFFu, rescale)) {
+            if (!__any_sync(0xFFFFFFFFu, mx[0] > most[0] || mx[1] > most[1])) break;
+            float alpha[2] = {1.f, 1.f};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
+              if (mx[e] > most[e]) {
+                const float t = ceilf(mx[e] - nm[e]) - kLift;
+                alpha[e] = tg::exp2_approx(m[e] - t);   // 0 where nothing was seen
+                m[e] = t;
+                nm[e] = -t;
+                most[e] = kLift + tg::kRescaleThreshold;
+                l[e] *= alpha[e];
+              }
+            }
             if (!first) {   // O must hold PV_{g-1} before it is scaled
               alive = wait(&S.o_done[(g - 1) % C::kS], ((g - 1) / C::kS) & 1, A.status, &S.abort_flag);
               if (!all_alive(alive)) { alive = false; break; }
@@ -693,6 +638,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
                   o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
                 tg::tmem_st_16x256b_x8(at, o);
               }
+              tg::tmem_st_wait();
             }
             if (hf > 0) {   // and the unit's first weights
               uint32_t w[16];
@@ -700,45 +646,44 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
               tmem_ld_16x128b_x8(sbuf, w);
               tg::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                w[i] = tg::pack_bf16x2(bf16_lo(w[i]) * alpha[i & 1], bf16_hi(w[i]) * alpha[i & 1]);
+              for (int i = 0; i < 16; ++i) {
+                if constexpr (kQ) {
+                  const float2 v = tg::f16x2_to_float2(w[i]);
+                  w[i] = tg::pack_f16x2(v.x * alpha[i & 1], v.y * alpha[i & 1]);
+                } else {
+                  w[i] = tg::pack_bf16x2(bf16_lo(w[i]) * alpha[i & 1], bf16_hi(w[i]) * alpha[i & 1]);
+                }
+              }
               tmem_st_16x128b_x8(sbuf, w);
             }
           }
+          if (!alive) break;
+          // Weights 2^z. Codes: log2 v is part of z, so these are what the codes are multiplied by
+          // and the reference follows their largest; the row sum takes them in fp32, divided by v.
+          // bf16: the row sum adds the rounded weights, so that a key which dominates its row gives
+          // its value exactly.
           uint32_t pk[16];
           float sum[2][2] = {};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float p[4];
+            float2 iv = {};
+            if constexpr (kQ) iv = *reinterpret_cast<const float2*>(key + 3 * kBN + 8 * i);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              fadd2(p[2 * e], p[2 * e + 1], z[4 * i + 2 * e], z[4 * i + 2 * e + 1], nm[e], nm[e]);
-              p[2 * e] = tg::exp2_approx(p[2 * e]);
-              p[2 * e + 1] = tg::exp2_approx(p[2 * e + 1]);
-            }
-            if constexpr (kQ) {
-              const float2 vs = *reinterpret_cast<const float2*>(key + 2 * kBN + 8 * i);
-              const float2 iv = *reinterpret_cast<const float2*>(key + 3 * kBN + 8 * i);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                fmul2(p[2 * e], p[2 * e + 1], p[2 * e], p[2 * e + 1], vs.x, vs.y);
-                pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
-                ffma2(sum[e][0], sum[e][1], bf16_lo(pk[2 * i + e]), bf16_hi(pk[2 * i + e]), iv.x, iv.y,
-                      sum[e][0], sum[e][1]);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
-                fadd2(sum[e][0], sum[e][1], bf16_lo(pk[2 * i + e]), bf16_hi(pk[2 * i + e]), sum[e][0],
-                      sum[e][1]);
+              const float p0 = tg::exp2_approx(z[4 * i + 2 * e]), p1 = tg::exp2_approx(z[4 * i + 2 * e + 1]);
+              if constexpr (kQ) {
+                pk[2 * i + e] = tg::pack_f16x2(p0, p1);
+                ffma2(sum[e][0], sum[e][1], p0, p1, iv.x, iv.y, sum[e][0], sum[e][1]);
+              } else {
+                pk[2 * i + e] = tg::pack_bf16x2(p0, p1);
+                add_bf16_lo(sum[e][0], pk[2 * i + e]);
+                add_bf16_hi(sum[e][1], pk[2 * i + e]);
               }
             }
           }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], alpha[e], sum[e][0] + sum[e][1]);
+          for (int e = 0; e < 2; ++e) l[e] += sum[e][0] + sum[e][1];
           tmem_st_16x128b_x8(sbuf + 32u * hf, pk);   // P over S columns that are read
-          fresh = false;
         }
         if (!alive) break;
         __syncwarp();
@@ -749,8 +694,9 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         if (lane == 0) tg::mbar_arrive(&S.p_full[g % C::kS]);
         first = c.run() == 1;   // the last unit of its item here: O is complete after PV_g
         if (first) {
-          const bool with_draft = draft;
-          whole = whole && with_draft;
+          // CTA c and item i (numbered over all sequences): slot c + i grows along the units
+          const int item = (c.b * A.n_hkv + c.kvh) * tg::row_tiles(A, A.n_draft) + c.mt;
+          const int64_t slot = static_cast<int64_t>(blockIdx.x + item) * rows;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
@@ -759,59 +705,27 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           alive = wait(&S.o_done[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag);
           if (!all_alive(alive)) { alive = false; break; }
           tg::tc_fence_after();
-          uint64_t bad = 0;
-          if (with_draft) bad = *reinterpret_cast<const uint64_t*>(S.bad[n_draft % kBadRing]);
-          const int slot = 2 * blockIdx.x + (seg > 0);
-          // where this thread's elements go: row r2[e], columns cq and cq + 1 of each 8
-          int64_t at[2];
-          float inv[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tok = tg::token_of(A, r2[e]), t = c.mt * A.tm + tok;
-            at[e] = whole ? (static_cast<int64_t>(c.b) * A.n_draft + t) * A.n_hq + c.kvh * A.group + r2[e] - tok * A.group
-                          : static_cast<int64_t>(slot) * rows + r2[e];
-            if (r2[e] >= rows || t >= c.dl ||
-                (whole && !tg::in_bounds(at[e], static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)))
-              at[e] = -1;
-            inv[e] = l[e] == 0.f ? 0.f : 1.f / l[e];   // nothing seen: zeros
-          }
 #pragma unroll 1
-          for (int h = 0; h < C::kHalves; ++h) {
+          for (int h = 0; h < C::kHalves; ++h) {   // columns cq and cq + 1 of each 8
             uint32_t o[32];
             tg::tmem_ld_16x256b_x8(tmem + lane_base + kColO + 64u * h, o);
             tg::tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (at[e] < 0) continue;
-              if (whole) {
-                __nv_bfloat16* p = A.out + at[e] * DH + 64 * h + cq;
+              if (r2[e] >= rows) continue;
+              float* p = A.part + (slot + r2[e]) * DH + 64 * h + cq;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint32_t*>(p + 8 * i) =
-                      tg::pack_bf16x2(__uint_as_float(o[4 * i + 2 * e]) * inv[e],
-                                      __uint_as_float(o[4 * i + 2 * e + 1]) * inv[e]);
-              } else {
-                float* p = A.part + at[e] * DH + 64 * h + cq;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint2*>(p + 8 * i) = make_uint2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
-              }
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint2*>(p + 8 * i) = make_uint2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
             }
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (at[e] < 0) continue;
-            if (!whole && (lane & 3) == 0)
-              *reinterpret_cast<float2*>(tg::part_ml(A, rows, DH) + at[e] * 2) =
-                  make_float2(m[e], l[e]);
-            if (bad & see[e])
-              add_infinite<DH>(A, c.b, c.kvh, bad & see[e], whole ? A.out + at[e] * DH + cq : nullptr,
-                               whole ? nullptr : A.part + at[e] * DH + cq, cq);
           }
           tg::tc_fence_before();
           __syncwarp();
           if (lane == 0) tg::mbar_arrive(&S.o_free);   // O may be overwritten
-          if (with_draft) ++n_draft;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if ((lane & 3) == 0 && r2[e] < rows)
+              *reinterpret_cast<float2*>(tg::part_ml(A, rows, DH) + (slot + r2[e]) * 2) = make_float2(m[e], l[e]);
           ++seg;
         }
         c.advance(A, Q);
@@ -828,7 +742,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     constexpr int kPasses = kRows * kC16 / 32;
     const int rl = lane & 7, cl = lane >> 3;               // row of eight, column of four
     Tile cur = {}, prev = {};
-    int r = 0, gk = 0, gv = 0, n_draft = 0;
+    int r = 0, gk = 0, gv = 0;
 #pragma unroll 1
     for (int i = 0; i < 2 * n; ++i) {
       const bool val = value_turn(i, n);
@@ -845,13 +759,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       uint8_t* dst = val ? S.v[0][0] : S.k[0][0];
       dst += s * kTileBytes;
       if (g >= n_st && !all_alive(wait(empty, ((g / n_st) - 1) & 1, A.status, &S.abort_flag))) break;
-      if (t.draft) {
-        if (cw < kMaxDraft / 16) {   // 16 rows each
-          if (val) draft_values<DH>(A, t.b, t.kvh, t.nv, dst, S.bad[n_draft % kBadRing], 16 * cw, 16 * cw + 16, lane);
-          else draft_keys<DH>(A, t.b, t.kvh, t.nv, dst, 16 * cw, 16 * cw + 16, lane);
-        }
-        if (val) ++n_draft;
-      } else {
+      {
         const int rs = r % C::kRaw;
         if (!all_alive(wait(&S.raw_full[rs], (r / C::kRaw) & 1, A.status, &S.abort_flag))) break;
         const uint8_t* src = S.raw[0] + rs * C::kRawBytes;
@@ -868,10 +776,8 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
           uint32_t y[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[2 * e] = widen2<kE4m3>(w[e], w[e], kE4m3 ? 0x1000 : 0x0100);
-            y[2 * e + 1] = widen2<kE4m3>(w[e], w[e], kE4m3 ? 0x3020 : 0x0302);
-          }
+          for (int e = 0; e < 4; ++e)
+            tg::widen4<kE4m3>(w[e] ^ (kE4m3 ? 0u : 0x80808080u), y[2 * e], y[2 * e + 1]);
           *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc)) = make_uint4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
         }
@@ -892,71 +798,82 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
   }
 }
 
-// Adds up what the CTAs left of every output row, one block a row: the partials of the
-// CTAs c0 .. c1 that share the row's item, kw each, in order, a quarter of them a warp.
-// tree_attn_kernel (kFew false): only items that were cut have partials; CTA c's are in
-// slot 2c (its first segment) or, where the item starts inside its share, 2c + 1.
-// tree_rows_kernel: every item has, CTA c's of item i (numbered over all sequences) in
-// slot c + i, which grows along the units, so no two share one; and the drafted rows that
-// the token sees come here, key by key, four warps in turn, so that what it does not see
-// is not even read.
-constexpr int kCombineWarps = 4;
-
-template <int DH, bool kFew>
-__global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const __grid_constant__ TreeArgs A) {
-  constexpr int kE = DH / 32;
+// Adds up what the CTAs left of every output row and brings in the drafted rows that its
+// token sees, key by key, so that what it does not see is not even read. kW warps a row: the
+// row's partials (of the CTAs c0 .. c1 that share its item, kw each, in order) and drafted
+// rows in turn, joined at the end. CTA c's partial of item i (numbered over all sequences)
+// is in slot c + i.
+template <int DH, int kW>
+__global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant__ TreeArgs A) {
+  constexpr int kE = DH / 32;           // dims of a lane
+  constexpr int kRows = 4 / kW;         // rows of a block, neighbouring heads
   using Vec = typename std::conditional<DH == 128, float4, float2>::type;
-  __shared__ float red[kCombineWarps][DH + 2];
+  using Half = typename std::conditional<DH == 128, uint2, uint32_t>::type;
+  __shared__ float red[4][DH + 2];
   tg::pdl_launch_dependents();
   tg::pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hq = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-  const int kvh = hq / A.group;
-  // what does not wait for anything else is asked for at once, the warp's first drafted row
-  // among it
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp % kW;
+  const int hq = blockIdx.x * kRows + warp / kW, t = blockIdx.y, b = blockIdx.z;
+  const bool mine = hq < A.n_hq;        // the last block's last warps may have no row
+  const int hr = mine ? hq : 0, kvh = hr / A.group;
+  // what does not wait for anything else is asked for at once
   const int64_t bt = static_cast<int64_t>(b) * A.n_draft + t;
   const int W = A.base[A.batch], first0 = A.base[b];
   const int2 sl = tg::seq_lens(A, b, false);
-  uint32_t see = 0;
-  uint2 qw = {}, kw = {}, vw = {};
-  float tau = 1.f, gain = 0.f, sd = 0.f;
-  auto drafted = [&](int i) {
-    const int64_t at = static_cast<int64_t>(b) * A.n_draft + min(i, A.n_draft - 1);
-    kw = *reinterpret_cast<const uint2*>(A.kd + (at * A.n_hkv + kvh) * DH + 4 * lane);
-    vw = *reinterpret_cast<const uint2*>(A.vd + (at * A.n_hkv + kvh) * DH + 4 * lane);
-    sd = A.sd[at];
-  };
-  if constexpr (kFew) {
-    see = static_cast<uint32_t>(A.mask[bt]);
-    qw = *reinterpret_cast<const uint2*>(A.q + (bt * A.n_hq + hq) * DH + 4 * lane);
-    tau = A.tau[hq];
-    gain = A.gain[hq];
-    drafted(warp);
-  }
+  uint64_t see = static_cast<uint64_t>(A.mask[bt]);
+  const Half qw = *reinterpret_cast<const Half*>(A.q + (bt * A.n_hq + hr) * DH + kE * lane);
+  const float tau = A.tau[hr], gain = A.gain[hr];
   if (t >= sl.y) return;
+  auto widen = [](const Half& h, float* f) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&h);
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) {
+      f[e] = bf16_lo(u[e / 2]);
+      f[e + 1] = bf16_hi(u[e / 2]);
+    }
+  };
+  // the warp's drafted rows: visible ones w0, w0 + kW, .., kD in flight at a time
+  constexpr int kD = 4;
+  if (sl.y < 64) see &= (1ull << sl.y) - 1;
+  for (int i = 0; i < w0; ++i) see &= see - 1;
+  Half kh[kD], vh[kD];
+  float sd[kD];
+  auto drafted = [&]() {
+#pragma unroll
+    for (int d = 0; d < kD; ++d) {
+      kh[d] = vh[d] = Half{};
+      sd[d] = 0.f;
+      if (!see) continue;
+      const int64_t at = static_cast<int64_t>(b) * A.n_draft + __ffsll(static_cast<long long>(see)) - 1;
+      kh[d] = *reinterpret_cast<const Half*>(A.kd + (at * A.n_hkv + kvh) * DH + kE * lane);
+      vh[d] = *reinterpret_cast<const Half*>(A.vd + (at * A.n_hkv + kvh) * DH + kE * lane);
+      sd[d] = A.sd[at];
+#pragma unroll
+      for (int i = 0; i < kW; ++i) see &= see - 1;
+    }
+  };
+  int left = (__popcll(see) + kW - 1) / kW;   // rows of this warp
+  drafted();
   float M = -INFINITY, L = 0.f, acc[kE] = {};
-  const int nt = tg::item_units(A, sl.x, sl.y);
+  const int nt = tg::key_units(A, sl.x);
   if (nt > 0) {
     const tg::Shares share(A, W);
     const int group = kvh / A.hw, hd = kvh - group * A.hw, mt = t / A.tm;
-    const int row = (t - mt * A.tm) * A.group + hq - kvh * A.group, rows = A.group * A.tm;
+    const int row = (t - mt * A.tm) * A.group + hr - kvh * A.group, rows = A.group * A.tm;
     const int first = first0 + (group * tg::row_tiles(A, sl.y) + mt) * nt;
     const int c0 = share.cta_of(first), c1 = share.cta_of(first + nt - 1);
-    if (!kFew && c0 == c1) return;                        // finished by that CTA
-    // the first CTA's place, and the others'
-    const int slot0 = kFew ? c0 + b * tg::head_groups(A) + group : 2 * c0 + (share.first(c0) != first);
+    const int slot0 = c0 + (b * tg::head_groups(A) + group) * tg::row_tiles(A, A.n_draft) + mt;
     const int parts = A.hw * A.kw, n = (c1 - c0 + 1) * A.kw;
     const float* ml = tg::part_ml(A, rows, DH);
-    // each warp: partials warp, warp + 4, ..; eight of them at a time, sums and O together
+    // eight partials at a time, sums and O together
 #pragma unroll 1
-    for (int i0 = warp; i0 < n; i0 += 8 * kCombineWarps) {
+    for (int i0 = w0; i0 < n; i0 += 8 * kW) {
       float2 v[8];
       Vec x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i = i0 + kCombineWarps * k, ci = A.kw == 1 ? i : i / A.kw;
-        const int slot = ci == 0 ? slot0 : kFew ? slot0 + ci : 2 * (c0 + ci);
-        const int64_t at = (static_cast<int64_t>(slot) * parts + hd * A.kw + (i - ci * A.kw)) * rows + row;
+        const int i = i0 + kW * k, ci = A.kw == 1 ? i : i / A.kw;
+        const int64_t at = (static_cast<int64_t>(slot0 + ci) * parts + hd * A.kw + (i - ci * A.kw)) * rows + row;
         v[k] = make_float2(-INFINITY, 0.f);
         x[k] = Vec{};
         if (i < n) {
@@ -981,54 +898,75 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
       }
     }
   }
-  if constexpr (kFew) {
-    if (sl.y < 32) see &= (1u << sl.y) - 1;
-    const float qf[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
-    const float ch = kLog2e / (sqrtf(static_cast<float>(DH)) * tau), gh = gain * kLog2e;
+  float qf[kE];
+  widen(qw, qf);
+  const float ch = kLog2e / (sqrtf(static_cast<float>(DH)) * tau), gh = gain * kLog2e;
 #pragma unroll 1
-    for (int i = warp; i < sl.y; i += kCombineWarps) {
-      const uint2 k1 = kw, v1 = vw;
-      const float s1 = sd;
-      drafted(i + kCombineWarps);
-      if (!((see >> i) & 1)) continue;
-      float z = fmaf(qf[0], bf16_lo(k1.x), fmaf(qf[1], bf16_hi(k1.x), fmaf(qf[2], bf16_lo(k1.y), qf[3] * bf16_hi(k1.y))));
+  for (; left > 0; left -= kD) {
+    float z[kD], vf[kD][kE], mn = M;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-      z = fmaf(z, ch, gh * s1);
-      if (z == -INFINITY) continue;   // a weight of zero
-      const float mn = fmaxf(M, z), scale = tg::exp2_approx(M - mn), p = tg::exp2_approx(z - mn);
-      M = mn;
-      L = fmaf(L, scale, p);
-      const float vf[4] = {bf16_lo(v1.x), bf16_hi(v1.x), bf16_lo(v1.y), bf16_hi(v1.y)};
+    for (int d = 0; d < kD; ++d) {
+      float kf[kE];
+      widen(kh[d], kf);
+      widen(vh[d], vf[d]);
+      z[d] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = fmaf(acc[e], scale, p * vf[e]);
+      for (int e = 0; e < kE; ++e) z[d] = fmaf(qf[e], kf[e], z[d]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z[d] += __shfl_xor_sync(0xFFFFFFFFu, z[d], o);
+      z[d] = d < left ? fmaf(z[d], ch, gh * sd[d]) : -INFINITY;
+      mn = fmaxf(mn, z[d]);
+    }
+    if (left > kD) drafted();
+    const float base = mn == -INFINITY ? 0.f : mn, scale = tg::exp2_approx(M - base);
+    M = mn;
+    L *= scale;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] *= scale;
+#pragma unroll
+    for (int d = 0; d < kD; ++d) {
+      if (z[d] == -INFINITY) continue;   // a weight of zero: its values do not count, whatever they are
+      const float p = tg::exp2_approx(z[d] - base);
+      L += p;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] = fmaf(p, vf[d][e], acc[e]);
     }
   }
+  const int64_t at = bt * A.n_hq + hr;
+  if constexpr (kW == 1) {
+    const float inv = L == 0.f ? 0.f : 1.f / L;   // nothing seen: zeros
+    if (!mine || !tg::in_bounds(at, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)) return;
+    uint32_t y[kE / 2];
 #pragma unroll
-  for (int e = 0; e < kE; ++e) red[warp][lane * kE + e] = acc[e];
-  if (lane == 0) {
-    red[warp][DH] = M;
-    red[warp][DH + 1] = L;
+    for (int e = 0; e < kE; e += 2) y[e / 2] = tg::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    *reinterpret_cast<Half*>(A.out + at * DH + kE * lane) = *reinterpret_cast<const Half*>(y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) red[warp][lane * kE + e] = acc[e];
+    if (lane == 0) {
+      red[warp][DH] = M;
+      red[warp][DH + 1] = L;
+    }
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d >= DH) return;
+    float Mx = -INFINITY, Lx = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) Mx = fmaxf(Mx, red[w][DH]);
+    const float base = Mx == -INFINITY ? 0.f : Mx;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      const float f = tg::exp2_approx(red[w][DH] - base);
+      Lx = fmaf(f, red[w][DH + 1], Lx);
+      y = fmaf(f, red[w][d], y);
+    }
+    if (!tg::in_bounds(at, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)) return;
+    A.out[at * DH + d] = __float2bfloat16_rn(y * (Lx == 0.f ? 0.f : 1.f / Lx));   // nothing seen: zeros
   }
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= DH) return;
-  float Mx = -INFINITY, Lx = 0.f, y = 0.f;
-#pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) Mx = fmaxf(Mx, red[w][DH]);
-  const float base = Mx == -INFINITY ? 0.f : Mx;
-#pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) {
-    const float f = tg::exp2_approx(red[w][DH] - base);
-    Lx = fmaf(f, red[w][DH + 1], Lx);
-    y = fmaf(f, red[w][d], y);
-  }
-  const int64_t at = bt * A.n_hq + hq;
-  if (!tg::in_bounds(at, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)) return;
-  A.out[at * DH + d] = __float2bfloat16_rn(y * (Lx == 0.f ? 0.f : 1.f / Lx));   // nothing seen: zeros
 }
 
 constexpr int kMinUnits = 2;
+constexpr int64_t kFewRows = 2048;
 
 // How a call is laid out: which kernel, tokens per row tile, units, CTAs and the
 // workspace's two parts.
@@ -1050,12 +988,12 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
   p.unit = p.few ? 16 * p.kw : kBN;
   auto units_of = [&](int64_t keys) { return (keys + p.unit - 1) / p.unit; };
   const int64_t items = static_cast<int64_t>(batch) * ((n_hkv + p.hw - 1) / p.hw) * ((n_draft + p.tm - 1) / p.tm);
-  p.units = items * (units_of(max_len) + (p.few ? 0 : 1));
+  p.units = items * units_of(max_len);
   const int64_t most = p.few ? tg::tree_rows_ctas(codes, rows) : kMaxCtas;
   // few rows: no fewer than kMinUnits units a CTA, since every CTA leaves a partial
   const int64_t want = p.few ? (p.units + kMinUnits - 1) / kMinUnits : p.units;
   p.n_cta = static_cast<int>(want < 1 ? 1 : want < most ? want : most);
-  p.slots = p.few ? p.n_cta + items : 2 * p.n_cta;
+  p.slots = p.n_cta + items;
   p.base_bytes = (static_cast<size_t>(batch) + 1) * sizeof(int32_t);
   p.base_bytes = (p.base_bytes + 255) / 256 * 256;
   p.bytes = p.base_bytes +
@@ -1063,11 +1001,14 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
   return p;
 }
 
-template <int DH, bool kFew>
+// Four warps a row where there are few rows, one where they fill the machine anyhow.
+template <int DH>
 tg_status launch_combine(const TreeArgs& a, tg_status r, cudaStream_t st) {
-  if (r != TG_OK || (!kFew && a.max_len == 0)) return r;   // there every item is one unit
-  return tg::launch(tree_combine_kernel<DH, kFew>, dim3(a.n_hq, a.n_draft, a.batch), dim3(32 * kCombineWarps), 0, st,
-                    0, a);
+  if (r != TG_OK) return r;
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.n_draft * a.n_hq;
+  if (rows <= kFewRows)
+    return tg::launch(tree_combine_kernel<DH, 4>, dim3(a.n_hq, a.n_draft, a.batch), dim3(128), 0, st, 0, a);
+  return tg::launch(tree_combine_kernel<DH, 1>, dim3((a.n_hq + 3) / 4, a.n_draft, a.batch), dim3(128), 0, st, 0, a);
 }
 
 template <int DH, int kType>
@@ -1085,7 +1026,7 @@ tg_status launch_tree(const TreeArgs& a, cudaStream_t st) {
   constexpr int smem = sizeof(TreeSmem<DH, kQ>) + 1024;
   static_assert(smem <= 232448, "the shared memory of one SM");
   if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_attn_kernel<DH, kType>), smem)) return TG_ERR_CUDA;
-  return launch_combine<DH, false>(
+  return launch_combine<DH>(
       a, tg::launch(tree_attn_kernel<DH, kType>, dim3(a.n_cta), dim3(C::kThreads), smem, st, 0, tq, tk, tv, a), st);
 }
 
@@ -1143,10 +1084,10 @@ extern "C" tg_status tg_tree_attention(
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.base_bytes);
   a.batch = batch, a.n_draft = n_draft, a.cap = cap, a.max_len = max_len, a.n_hq = n_hq, a.n_hkv = n_hkv;
   a.group = n_hq / n_hkv, a.group_inv = (65536 + a.group - 1) / a.group, a.tm = p.tm, a.unit = p.unit, a.hw = p.hw, a.kw = p.kw, a.n_cta = p.n_cta;
-  a.few = p.few, a.slots = p.slots;
+  a.slots = p.slots;
   a.status = tg::status_word();
   if (!a.status) return TG_ERR_CUDA;
-  if (p.few) return launch_combine<128, true>(a, tg::launch_tree_rows(a, cache_dtype, stream), stream);
+  if (p.few) return launch_combine<128>(a, tg::launch_tree_rows(a, cache_dtype, stream), stream);
   if (head_dim == 128) {
     if (cache_dtype == TG_BF16) return launch_tree<128, TG_BF16>(a, stream);
     return cache_dtype == TG_I8 ? launch_tree<128, TG_I8>(a, stream) : launch_tree<128, TG_E4M3>(a, stream);

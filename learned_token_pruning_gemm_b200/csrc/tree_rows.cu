@@ -21,8 +21,6 @@
 //        2 i + 8 and 2 i + 9: product t holds the dims at places 2 t and 2 t + 1 of these.
 // Codes are widened to fp16, which holds them exactly at half the instructions that bf16
 // takes; the queries are then fp16 too, after their largest value is brought near 2^8.
-#include <cuda_fp16.h>
-
 #include "tree.cuh"
 
 namespace {
@@ -30,7 +28,11 @@ namespace {
 using tg::TreeArgs;
 using tg::bf16_hi;
 using tg::bf16_lo;
+using tg::bf16x2_to_f16x2;
+using tg::max_u16x2;
+using tg::pack_f16x2;
 using tg::wait;
+using tg::widen4;
 
 // NT: tiles of eight rows. Several CTAs share an SM, so that one's start and end of an item
 // pass under the others' work; how many goes by registers, then the ring takes the rest of
@@ -142,34 +144,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Four codes (bytes of w; int8 ones with the sign bit flipped) to four fp16 values, exactly.
-template <bool kE4m3>
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (kE4m3) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  } else {   // 1024 + (code + 128) has the code's bits as its last eight; then less 1152
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
-  }
-}
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float scale) {
-  return pack_f16x2(bf16_lo(w) * scale, bf16_hi(w) * scale);
 }
 // 8 bytes global -> shared, asynchronously
 __device__ __forceinline__ void cp8(void* dst, const void* src) {
