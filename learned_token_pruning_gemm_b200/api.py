@@ -6,7 +6,6 @@ status. All arithmetic happens in the CUDA kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional, Sequence
@@ -42,7 +41,7 @@ def _numel(t: torch.Tensor, n: int, name: str) -> None:
 
 
 def _shape(t: torch.Tensor, shape, name: str, dtype=None) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise TokenGateError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TokenGateError(f"{name} must be {dtype}, got {t.dtype}")
@@ -383,33 +382,41 @@ def gated_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     return out
 
 
-def _launch_on(stream, *tensors):
-    """(context, stream handle) for a call on these tensors (None entries are skipped):
-    they must share one CUDA device, which is made current for the call if it is not,
-    and the stream is that device's current one unless given."""
-    dev = None
+def _call(fn, what: str, stream, tensors, args) -> None:
+    """fn(*args, stream) on the tensors' device, which must be one CUDA device (None entries
+    are skipped) and is made current for the call if it is not; the stream is that device's
+    current one unless given. Raises on a status other than OK."""
+    dev = tensors[0].get_device()   # -1 for a CPU tensor
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise TokenGateError("every tensor must be a CUDA tensor")
-        d = t.get_device()
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise TokenGateError("every tensor must be on the same device")
-    if stream is not None and stream.device.index != dev:
-        raise TokenGateError("the stream must be on the tensors' device")
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    ctx = contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-    return ctx, s.cuda_stream
+        if t is not None and t.get_device() != dev:
+            raise TokenGateError(f"{what}: every tensor must be on the same CUDA device")
+    if dev < 0:
+        raise TokenGateError(f"{what}: every tensor must be a CUDA tensor")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise TokenGateError(f"{what}: the stream must be on the tensors' device")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != 0:
+        check(st, what)
+
+
+def _ptr(t: torch.Tensor, name: str) -> int:
+    if not t.is_contiguous():
+        raise TokenGateError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _keep_for(stream, *tensors) -> None:
-    """Tensors allocated here (on the current stream) but used on a given stream."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+    """Tensors allocated here, on the current stream, but used on a given one."""
+    for t in tensors:
+        t.record_stream(stream)
 
 
 def _heads(t: torch.Tensor, T: int, H: int, dh: int, name: str, dtype) -> int:
@@ -445,23 +452,22 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
     may be views with any token stride (of a packed projection output); returns (q_out,
     k_out), dense unless `out` is given. `out` may be (q, k) themselves."""
     T, hq, hkv, dh, rot = _norm_rope_args("qk_norm_rope", q, k, q_weight, k_weight, pos, rot_dim)
-    q_st = _heads(q, T, hq, dh, "q", q.dtype)
-    k_st = _heads(k, T, hkv, dh, "k", q.dtype)
-    new = out is None
-    if new:
-        out = (torch.empty((T, hq, dh), dtype=q.dtype, device=q.device),
-               torch.empty((T, hkv, dh), dtype=q.dtype, device=q.device))
-    qo, ko = out
-    qo_st = _heads(qo, T, hq, dh, "q_out", q.dtype)
-    ko_st = _heads(ko, T, hkv, dh, "k_out", q.dtype)
-    w_q, w_k, p = (_cuda(q_weight, "q_weight"), _cuda(k_weight, "k_weight"), _cuda(pos, "pos"))
-    ctx, s = _launch_on(stream, q, k, q_weight, k_weight, pos, qo, ko)
-    with ctx:
-        st = _lib.load().tg_qk_norm_rope(q.data_ptr(), q_st, k.data_ptr(), k_st, _DT[q.dtype], T, hq,
-                                         hkv, dh, rot, w_q, w_k, float(eps), float(rope_base), p,
-                                         qo.data_ptr(), qo_st, ko.data_ptr(), ko_st, s)
-    check(st, "tg_qk_norm_rope")
-    if new:
+    dt = q.dtype
+    q_st = _heads(q, T, hq, dh, "q", dt)
+    k_st = _heads(k, T, hkv, dh, "k", dt)
+    if out is None:
+        qo, ko = q.new_empty((T, hq, dh)), q.new_empty((T, hkv, dh))
+        qo_st, ko_st = hq * dh, hkv * dh
+    else:
+        qo, ko = out
+        qo_st = _heads(qo, T, hq, dh, "q_out", dt)
+        ko_st = _heads(ko, T, hkv, dh, "k_out", dt)
+    _call(_lib.load().tg_qk_norm_rope, "tg_qk_norm_rope", stream,
+          (q, k, q_weight, k_weight, pos, qo, ko),
+          (q.data_ptr(), q_st, k.data_ptr(), k_st, _DT[dt], T, hq, hkv, dh, rot,
+           _ptr(q_weight, "q_weight"), _ptr(k_weight, "k_weight"), float(eps), float(rope_base), _ptr(pos, "pos"),
+           qo.data_ptr(), qo_st, ko.data_ptr(), ko_st))
+    if out is None and stream is not None:
         _keep_for(stream, qo, ko)
     return qo, ko
 
@@ -486,10 +492,8 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
     gk_st = _heads(dk_out, T, hkv, dh, "dk_out", dt)
     new = []
     if grads is None:
-        grads = new = [torch.empty((T, hq, dh), dtype=dt, device=q.device),
-                       torch.empty((T, hkv, dh), dtype=dt, device=q.device),
-                       torch.empty(dh, dtype=torch.float32, device=q.device),
-                       torch.empty(dh, dtype=torch.float32, device=q.device)]
+        grads = new = [q.new_empty((T, hq, dh)), q.new_empty((T, hkv, dh)),
+                       torch.empty_like(q_weight), torch.empty_like(k_weight)]
     dq, dk, dwq, dwk = grads
     dq_st = _heads(dq, T, hq, dh, "dq", dt)
     dk_st = _heads(dk, T, hkv, dh, "dk", dt)
@@ -497,20 +501,18 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
     _shape(dwk, (dh,), "dk_weight", torch.float32)
     lib = _lib.load()
     if workspace is None:
-        need = int(lib.tg_qk_norm_rope_bwd_workspace_size(T, hq, hkv, dh))
+        need = lib.tg_qk_norm_rope_bwd_workspace_size(T, hq, hkv, dh)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
         new = [*new, workspace]
-    w_q, w_k, p = (_cuda(q_weight, "q_weight"), _cuda(k_weight, "k_weight"), _cuda(pos, "pos"))
-    ctx, s = _launch_on(stream, q, k, q_weight, k_weight, pos, dq_out, dk_out, dq, dk, dwq, dwk,
-                        workspace)
-    with ctx:
-        st = lib.tg_qk_norm_rope_bwd(
-            q.data_ptr(), q_st, k.data_ptr(), k_st, dq_out.data_ptr(), gq_st, dk_out.data_ptr(), gk_st,
-            _DT[dt], T, hq, hkv, dh, rot, w_q, w_k, float(eps), float(rope_base), p, dq.data_ptr(),
-            dq_st, dk.data_ptr(), dk_st, _cuda(dwq, "dq_weight"), _cuda(dwk, "dk_weight"),
-            _cuda(workspace, "workspace"), workspace.numel() * workspace.element_size(), s)
-    check(st, "tg_qk_norm_rope_bwd")
-    _keep_for(stream, *new)
+    _call(lib.tg_qk_norm_rope_bwd, "tg_qk_norm_rope_bwd", stream,
+          (q, k, q_weight, k_weight, pos, dq_out, dk_out, dq, dk, dwq, dwk, workspace),
+          (q.data_ptr(), q_st, k.data_ptr(), k_st, dq_out.data_ptr(), gq_st, dk_out.data_ptr(), gk_st,
+           _DT[dt], T, hq, hkv, dh, rot, _ptr(q_weight, "q_weight"), _ptr(k_weight, "k_weight"), float(eps),
+           float(rope_base), _ptr(pos, "pos"), dq.data_ptr(), dq_st, dk.data_ptr(), dk_st,
+           _ptr(dwq, "dq_weight"), _ptr(dwk, "dk_weight"), _ptr(workspace, "workspace"),
+           workspace.numel() * workspace.element_size()))
+    if stream is not None:
+        _keep_for(stream, *new)
     return dq, dk, dwq, dwk
 
 
@@ -551,17 +553,14 @@ def quant_cache_append(k_new: torch.Tensor, v_new: torch.Tensor, s_new: torch.Te
         _shape(src_idx, (n_new,), "src_idx", torch.int32)
     if start is not None:
         _shape(start, (B,), "start", torch.int32)
-    args = (_cuda(k_new, "k_new"), _cuda(v_new, "v_new"), _cuda(s_new, "s_new"), R,
-            None if src_idx is None else _cuda(src_idx, "src_idx"), n_new, _cuda(cu_new, "cu_new"),
-            None if start is None else _cuda(start, "start"), B, cap, hkv, dh,
-            _CODE_DT[k_cache.dtype], _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache"),
-            _cuda(k_scale, "k_scale"), _cuda(v_scale, "v_scale"), _cuda(s_cache, "s_cache"),
-            _cuda(cache_len, "cache_len"))
-    ctx, s = _launch_on(stream, k_new, v_new, s_new, src_idx, cu_new, start, k_cache, v_cache, k_scale,
-                        v_scale, s_cache, cache_len)
-    with ctx:
-        st = _lib.load().tg_quant_cache_append(*args, s)
-    check(st, "tg_quant_cache_append")
+    _call(_lib.load().tg_quant_cache_append, "tg_quant_cache_append", stream,
+          (k_cache, v_cache, k_scale, v_scale, s_cache, cache_len, k_new, v_new, s_new, src_idx, cu_new,
+           start),
+          (_ptr(k_new, "k_new"), _ptr(v_new, "v_new"), _ptr(s_new, "s_new"), R,
+           None if src_idx is None else _ptr(src_idx, "src_idx"), n_new, _ptr(cu_new, "cu_new"),
+           None if start is None else _ptr(start, "start"), B, cap, hkv, dh, _CODE_DT[k_cache.dtype],
+           _ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache"), _ptr(k_scale, "k_scale"),
+           _ptr(v_scale, "v_scale"), _ptr(s_cache, "s_cache"), _ptr(cache_len, "cache_len")))
 
 
 def quant_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -577,28 +576,25 @@ def quant_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torc
     _shape(cu_rows, (B + 1,), "cu_rows", torch.int32)
     if start is not None:
         _shape(start, (B,), "start", torch.int32)
-    new = out is None
-    if new:
-        out = (torch.empty((total, hkv, dh), dtype=dtype, device=k_cache.device),
-               torch.empty((total, hkv, dh), dtype=dtype, device=k_cache.device),
-               torch.empty(total, dtype=torch.float32, device=k_cache.device))
-    k, v, s_out = out
-    if k.dtype not in _DT:
-        raise TokenGateError(f"quant_cache_read: unsupported dtype {k.dtype}")
-    _shape(k, (total, hkv, dh), "k", k.dtype)
-    _shape(v, (total, hkv, dh), "v", k.dtype)
-    _shape(s_out, (total,), "s", torch.float32)
-    args = (_cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache"), _cuda(k_scale, "k_scale"),
-            _cuda(v_scale, "v_scale"), _cuda(s_cache, "s_cache"), _cuda(cache_len, "cache_len"),
-            None if start is None else _cuda(start, "start"), _cuda(cu_rows, "cu_rows"), total, B, cap,
-            hkv, dh, _CODE_DT[k_cache.dtype], _DT[k.dtype], _cuda(k, "k"), _cuda(v, "v"),
-            _cuda(s_out, "s"))
-    ctx, s = _launch_on(stream, k_cache, v_cache, k_scale, v_scale, s_cache, cache_len, start, cu_rows,
-                        k, v, s_out)
-    with ctx:
-        st = _lib.load().tg_quant_cache_read(*args, s)
-    check(st, "tg_quant_cache_read")
-    if new:
+    if dtype not in _DT:
+        raise TokenGateError(f"quant_cache_read: unsupported dtype {dtype}")
+    if out is None:
+        k = k_cache.new_empty((total, hkv, dh), dtype=dtype)
+        v, s_out = torch.empty_like(k), s_cache.new_empty(total)
+    else:
+        k, v, s_out = out
+        if k.dtype not in _DT:
+            raise TokenGateError(f"quant_cache_read: unsupported dtype {k.dtype}")
+        _shape(k, (total, hkv, dh), "k", k.dtype)
+        _shape(v, (total, hkv, dh), "v", k.dtype)
+        _shape(s_out, (total,), "s", torch.float32)
+    _call(_lib.load().tg_quant_cache_read, "tg_quant_cache_read", stream,
+          (k_cache, v_cache, k_scale, v_scale, s_cache, cache_len, start, cu_rows, k, v, s_out),
+          (_ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache"), _ptr(k_scale, "k_scale"),
+           _ptr(v_scale, "v_scale"), _ptr(s_cache, "s_cache"), _ptr(cache_len, "cache_len"),
+           None if start is None else _ptr(start, "start"), _ptr(cu_rows, "cu_rows"), total, B, cap, hkv,
+           dh, _CODE_DT[k_cache.dtype], _DT[k.dtype], _ptr(k, "k"), _ptr(v, "v"), _ptr(s_out, "s")))
+    if out is None and stream is not None:
         _keep_for(stream, k, v, s_out)
     return k, v, s_out
 
@@ -662,35 +658,36 @@ def tree_attention(q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor
         cdt = _CODE_DT[k_cache.dtype]
         _shape(k_scale, (B, cap, hkv), "k_scale", torch.float32)
         _shape(v_scale, (B, cap, hkv), "v_scale", torch.float32)
-        ks, vs = _cuda(k_scale, "k_scale"), _cuda(v_scale, "v_scale")
+        ks, vs = _ptr(k_scale, "k_scale"), _ptr(v_scale, "v_scale")
     else:
         if k_cache.dtype != torch.bfloat16 or k_scale is not None or v_scale is not None:
             raise TokenGateError("tree_attention: a cache is bf16 without scales, or int8 or "
                                  "float8_e4m3fn with them")
         cdt, ks, vs = TG_BF16, None, None
+    if q.dtype != torch.bfloat16:
+        raise TokenGateError(f"q must be {torch.bfloat16}, got {q.dtype}")
+    max_len = int(max_len)
     new = []
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         new.append(out)
-    _shape(out, q.shape, "out", torch.bfloat16)
+    else:
+        _shape(out, q.shape, "out", torch.bfloat16)
     lib = _lib.load()
     if workspace is None:
-        need = int(lib.tg_tree_attention_workspace_size(B, T, int(max_len), hq, hkv, dh))
+        need = lib.tg_tree_attention_workspace_size(B, T, max_len, hq, hkv, dh)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
         new.append(workspace)
-    args = (_cuda(q, "q", torch.bfloat16), _cuda(k_draft, "k_draft"), _cuda(v_draft, "v_draft"),
-            _cuda(s_draft, "s_draft"), _cuda(tree_mask, "tree_mask"),
-            None if draft_len is None else _cuda(draft_len, "draft_len"), B, T,
-            _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache"), cdt, ks, vs,
-            _cuda(s_cache, "s_cache"), _cuda(cache_len, "cache_len"), cap, int(max_len), hq, hkv, dh,
-            _cuda(gain, "gain"), _cuda(tau, "tau"), _cuda(out, "out"), _cuda(workspace, "workspace"),
-            workspace.numel() * workspace.element_size())
-    ctx, s = _launch_on(stream, q, k_draft, v_draft, s_draft, tree_mask, draft_len, k_cache, v_cache,
-                        k_scale, v_scale, s_cache, cache_len, gain, tau, out, workspace)
-    with ctx:
-        st = lib.tg_tree_attention(*args, s)
-    check(st, "tg_tree_attention")
-    _keep_for(stream, *new)
+    _call(lib.tg_tree_attention, "tg_tree_attention", stream,
+          (q, k_draft, v_draft, s_draft, tree_mask, draft_len, k_cache, v_cache, k_scale, v_scale, s_cache,
+           cache_len, gain, tau, out, workspace),
+          (_ptr(q, "q"), _ptr(k_draft, "k_draft"), _ptr(v_draft, "v_draft"), _ptr(s_draft, "s_draft"),
+           _ptr(tree_mask, "tree_mask"), None if draft_len is None else _ptr(draft_len, "draft_len"), B, T,
+           _ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache"), cdt, ks, vs, _ptr(s_cache, "s_cache"),
+           _ptr(cache_len, "cache_len"), cap, max_len, hq, hkv, dh, _ptr(gain, "gain"), _ptr(tau, "tau"),
+           _ptr(out, "out"), _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()))
+    if stream is not None:
+        _keep_for(stream, *new)
     return out
 
 
