@@ -21,7 +21,7 @@
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxDh = 256;
 
@@ -40,62 +40,90 @@ struct NormRopeArgs {
   float* partial;                 // backward: [gridDim.x][2][dh] sums of g x r
 };
 
-template <typename T>
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// N elements of type T as N / 2 pairs of floats.
+template <typename T, int N>
 struct Io;
 template <>
-struct Io<__nv_bfloat16> {
-  using Vec = uint2;   // four elements
-  static __device__ __forceinline__ void unpack(const Vec& v, float* f) {
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+struct Io<__nv_bfloat16, 8> {
+  using Vec = uint4;
+  static __device__ __forceinline__ void unpack(const Vec& v, float2* f) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ Vec pack(const float* f) {
-    return make_uint2(tg::pack_bf16x2(f[0], f[1]), tg::pack_bf16x2(f[2], f[3]));
-  }
-  // absolute error about 2^-21, far below half a bf16 step of the result
-  static __device__ __forceinline__ void sincos(float half_turns, float* s, float* c) {
-    __sincosf(half_turns * 3.14159265358979f, s, c);
+  static __device__ __forceinline__ Vec pack(const float2* f) {
+    return make_uint4(tg::pack_bf16x2(f[0].x, f[0].y), tg::pack_bf16x2(f[1].x, f[1].y),
+                      tg::pack_bf16x2(f[2].x, f[2].y), tg::pack_bf16x2(f[3].x, f[3].y));
   }
 };
 template <>
-struct Io<float> {
-  using Vec = float4;
-  static __device__ __forceinline__ void unpack(const Vec& v, float* f) {
-    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+struct Io<__nv_bfloat16, 4> {
+  using Vec = uint2;
+  static __device__ __forceinline__ void unpack(const Vec& v, float2* f) {
+    f[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+    f[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ Vec pack(const float* f) {
-    return make_float4(f[0], f[1], f[2], f[3]);
-  }
-  static __device__ __forceinline__ void sincos(float half_turns, float* s, float* c) {
-    sincospif(half_turns, s, c);
+  static __device__ __forceinline__ Vec pack(const float2* f) {
+    return make_uint2(tg::pack_bf16x2(f[0].x, f[0].y), tg::pack_bf16x2(f[1].x, f[1].y));
   }
 };
+template <>
+struct Io<float, 4> {
+  using Vec = float4;
+  static __device__ __forceinline__ void unpack(const Vec& v, float2* f) {
+    f[0] = make_float2(v.x, v.y);
+    f[1] = make_float2(v.z, v.w);
+  }
+  static __device__ __forceinline__ Vec pack(const float2* f) { return make_float4(f[0].x, f[0].y, f[1].x, f[1].y); }
+};
 
-// The lane's frequencies F_i = ratio^i / (2 pi) in turns, 0.64 fixed point, i = 4c + j.
+// The lane's frequencies F_i = ratio^i / (2 pi) in turns, 0.64 fixed point, i = E c + j.
+template <int E>
 __device__ __forceinline__ void lane_turns(double ratio, int c, uint64_t* f) {
-  double t = 0.15915494309189535, p = (ratio * ratio) * (ratio * ratio);
+  double t = 0.15915494309189535, p = ratio;
+#pragma unroll
+  for (int b = 1; b < E; b <<= 1) p *= p;   // ratio^E
 #pragma unroll
   for (int b = 0; b < 5; ++b) {
     if ((c >> b) & 1) t *= p;
     p *= p;
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < E; ++j) {
     f[j] = __double2ull_rn(t * 18446744073709551616.0);
     t *= ratio;
   }
 }
 
-template <typename T>
+// Sine and cosine of position pos times a turn fraction. kFull: to fp32; otherwise by MUFU,
+// off by about 2^-21, far below half a bf16 step of the result.
+template <bool kFull>
 __device__ __forceinline__ void angle(int64_t pos, uint64_t turn, float* sn, float* cs) {
   const uint64_t fx = static_cast<uint64_t>(pos) * turn;
   const uint32_t hi = static_cast<uint32_t>((fx + (1ull << 31)) >> 32);   // 2^-32 of a turn
   const uint32_t quarter = (hi + (1u << 29)) >> 30;
-  const float x = static_cast<float>(static_cast<int32_t>(hi - (quarter << 30))) * 0x1p-31f;
+  const float x = static_cast<float>(static_cast<int32_t>(hi - (quarter << 30))) * 0x1p-31f;   // half turns
   float s, c;
-  Io<T>::sincos(x, &s, &c);
+  if constexpr (kFull) sincospif(x, &s, &c);
+  else __sincosf(x * 3.14159265358979f, &s, &c);
   const bool odd = quarter & 1;
   const float a = odd ? c : s, b = odd ? s : c;
   *sn = (quarter & 2) ? -a : a;
@@ -109,125 +137,135 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// LPH lanes per head (8, 16 or 32: dh up to 64, 128 or 256); kU heads of each lane
-// group are in flight at once.
-template <typename T, int LPH, bool kBwd>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs A) {
-  using Vec = typename Io<T>::Vec;
+// E: elements of a lane in either half of its pairs, LPH lanes per head (at least dh / (2 E)).
+// kU heads of each lane group are in flight at once.
+template <typename T, int E, int LPH, bool kBwd>
+__global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) norm_rope_kernel(const NormRopeArgs A) {
+  using IO = Io<T, E>;
+  using Vec = typename IO::Vec;
+  constexpr int kP = E / 2;
   constexpr int kHpw = 32 / LPH;   // heads a warp handles side by side
-  constexpr int kU = kBwd ? 2 : 4;
+  constexpr int kU = kBwd || E == 4 ? 2 : 4;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = lane % LPH, sub = lane / LPH;
-  const int nc = A.dh / 8, nr = A.rot / 8;
+  const int nc = A.dh / (2 * E), nr = A.rot / (2 * E);
   const bool active = c < nc, turns = c < nr;
-  const int offa = turns ? 4 * c : A.rot + 8 * (c - nr);
-  const int offb = turns ? A.rot / 2 + 4 * c : offa + 4;
-  uint64_t freq[4];
-  lane_turns(A.ratio, turns ? c : 0, freq);
+  const int offa = !active ? 0 : turns ? E * c : A.rot + 2 * E * (c - nr);
+  const int offb = !active ? 0 : turns ? A.rot / 2 + E * c : offa + E;
+  uint64_t freq[E];
+  lane_turns<E>(A.ratio, turns ? c : 0, freq);
   tg::pdl_launch_dependents();
   tg::pdl_wait();   // global memory only from here on
 
-  float wa[2][4], wb[2][4];   // this lane's weights, [0] queries, [1] keys
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float* w = e ? A.wk : A.wq;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      wa[e][j] = active ? w[offa + j] : 0.f;
-      wb[e][j] = active ? w[offb + j] : 0.f;
-    }
+  // the weights, [0] queries, [1] keys; zeros for lanes without elements
+  __shared__ __align__(16) float sw[2][kMaxDh];
+  for (int i = tid; i < 2 * kMaxDh; i += kThreads) {
+    const int d = i & (kMaxDh - 1);
+    sw[i / kMaxDh][d] = d < A.dh ? (i < kMaxDh ? A.wq : A.wk)[d] : 0.f;
   }
-  float dwa[2][4] = {}, dwb[2][4] = {};
+  __syncthreads();
+  float2 dwa[2][kBwd ? kP : 1] = {}, dwb[2][kBwd ? kP : 1] = {};
   const float inv_dh = 1.f / static_cast<float>(A.dh);
-  const int heads = A.n_hq + A.n_hkv;
   const int64_t n_work = A.n_tokens * A.parts;
+#pragma unroll 1
   for (int64_t wk = static_cast<int64_t>(blockIdx.x) * kWarps + warp; wk < n_work;
        wk += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t t = wk / A.parts;
+    const int64_t t = A.parts == 1 ? wk : wk / A.parts;
     const int part = static_cast<int>(wk - t * A.parts);
     const int64_t p = A.pos[t];
-    float sn[4], cs[4];
+    float2 sn[kP], cs[kP];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (turns) angle<T>(p, freq[j], &sn[j], &cs[j]);
-      else sn[j] = 0.f, cs[j] = 1.f;
+    for (int j = 0; j < E; ++j) {
+      float s = 0.f, k = 1.f;
+      if (turns) angle<sizeof(T) == 4>(p, freq[j], &s, &k);
+      if (j & 1) sn[j / 2].y = s, cs[j / 2].y = k;
+      else sn[j / 2].x = s, cs[j / 2].x = k;
     }
-    // heads part*kHpw + sub, then every parts*kHpw-th
-    const int step = A.parts * kHpw;
-    for (int h0 = part * kHpw + sub; h0 - sub < heads; h0 += kU * step) {
-      Vec va[kU], vb[kU], ga[kBwd ? kU : 1], gb[kBwd ? kU : 1];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int h = h0 + u * step;
-        if (h < heads && active) {
-          const bool key = h >= A.n_hq;
-          const T* x = key ? static_cast<const T*>(A.k) + t * A.k_st + (h - A.n_hq) * A.dh
-                           : static_cast<const T*>(A.q) + t * A.q_st + h * A.dh;
-          va[u] = *reinterpret_cast<const Vec*>(x + offa);
-          vb[u] = *reinterpret_cast<const Vec*>(x + offb);
-          if constexpr (kBwd) {
-            const T* g = key ? static_cast<const T*>(A.gk) + t * A.gk_st + (h - A.n_hq) * A.dh
-                             : static_cast<const T*>(A.gq) + t * A.gq_st + h * A.dh;
-            ga[u] = *reinterpret_cast<const Vec*>(g + offa);
-            gb[u] = *reinterpret_cast<const Vec*>(g + offb);
-          }
-        } else {
-          va[u] = Vec{}, vb[u] = Vec{};
-          if constexpr (kBwd) ga[u] = Vec{}, gb[u] = Vec{};
+    for (int key = 0; key < 2; ++key) {   // queries, then keys
+      const int heads = key ? A.n_hkv : A.n_hq;
+      const T* x0 = static_cast<const T*>(key ? A.k : A.q) + t * (key ? A.k_st : A.q_st);
+      const T* g0 = static_cast<const T*>(key ? A.gk : A.gq) + t * (key ? A.gk_st : A.gq_st);
+      T* y0 = static_cast<T*>(key ? A.ok : A.oq) + t * (key ? A.ok_st : A.oq_st);
+      // forward: y_a = r (x_a w_a cos - x_b w_b sin), y_b = r (x_b w_b cos + x_a w_a sin), with
+      // the products of weight and angle formed once for all heads
+      float2 wa[kP], wb[kP];
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        wa[j] = *reinterpret_cast<const float2*>(&sw[key][offa + 2 * j]);
+        wb[j] = *reinterpret_cast<const float2*>(&sw[key][offb + 2 * j]);
+      }
+      float2 ca[kP], sb[kP], cb[kP], sa[kP];
+      if constexpr (!kBwd) {
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          ca[j] = mul2(wa[j], cs[j]);
+          sa[j] = mul2(wa[j], sn[j]);
+          cb[j] = mul2(wb[j], cs[j]);
+          sb[j] = mul2(wb[j], make_float2(-sn[j].x, -sn[j].y));
         }
       }
+      // heads part*kHpw + sub, then every parts*kHpw-th
+      const int step = A.parts * kHpw;
+#pragma unroll 1
+      for (int h0 = part * kHpw + sub; h0 - sub < heads; h0 += kU * step) {
+        Vec va[kU], vb[kU], ga[kBwd ? kU : 1], gb[kBwd ? kU : 1];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int h = h0 + u * step;
-        const bool key = h >= A.n_hq;
-        float xa[4], xb[4], ya[4], yb[4];
-        Io<T>::unpack(va[u], xa);
-        Io<T>::unpack(vb[u], xb);
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
-        const float r = __frsqrt_rn(fmaf(head_sum<LPH>(ss), inv_dh, A.eps));
-        if constexpr (!kBwd) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float na = xa[j] * r * (key ? wa[1][j] : wa[0][j]);
-            const float nb = xb[j] * r * (key ? wb[1][j] : wb[0][j]);
-            ya[j] = fmaf(na, cs[j], -nb * sn[j]);
-            yb[j] = fmaf(nb, cs[j], na * sn[j]);
-          }
-        } else {
-          float da[4], db[4], m = 0.f;
-          Io<T>::unpack(ga[u], da);
-          Io<T>::unpack(gb[u], db);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float ua = fmaf(da[j], cs[j], db[j] * sn[j]);
-            const float ub = fmaf(db[j], cs[j], -da[j] * sn[j]);
-            xa[j] *= r;
-            xb[j] *= r;
-            if (key) {
-              dwa[1][j] = fmaf(ua, xa[j], dwa[1][j]);
-              dwb[1][j] = fmaf(ub, xb[j], dwb[1][j]);
-            } else {
-              dwa[0][j] = fmaf(ua, xa[j], dwa[0][j]);
-              dwb[0][j] = fmaf(ub, xb[j], dwb[0][j]);
+        for (int u = 0; u < kU; ++u) {
+          const int h = h0 + u * step;
+          va[u] = vb[u] = Vec{};
+          if constexpr (kBwd) ga[u] = gb[u] = Vec{};
+          if (h < heads && active) {
+            va[u] = *reinterpret_cast<const Vec*>(x0 + h * A.dh + offa);
+            vb[u] = *reinterpret_cast<const Vec*>(x0 + h * A.dh + offb);
+            if constexpr (kBwd) {
+              ga[u] = *reinterpret_cast<const Vec*>(g0 + h * A.dh + offa);
+              gb[u] = *reinterpret_cast<const Vec*>(g0 + h * A.dh + offb);
             }
-            da[j] = ua * (key ? wa[1][j] : wa[0][j]);
-            db[j] = ub * (key ? wb[1][j] : wb[0][j]);
-            m = fmaf(da[j], xa[j], fmaf(db[j], xb[j], m));
-          }
-          m = head_sum<LPH>(m) * inv_dh;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ya[j] = r * fmaf(-xa[j], m, da[j]);
-            yb[j] = r * fmaf(-xb[j], m, db[j]);
           }
         }
-        if (h < heads && active) {
-          T* y = key ? static_cast<T*>(A.ok) + t * A.ok_st + (h - A.n_hq) * A.dh
-                     : static_cast<T*>(A.oq) + t * A.oq_st + h * A.dh;
-          *reinterpret_cast<Vec*>(y + offa) = Io<T>::pack(ya);
-          *reinterpret_cast<Vec*>(y + offb) = Io<T>::pack(yb);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int h = h0 + u * step;
+          float2 xa[kP], xb[kP], ya[kP], yb[kP], ss = {};
+          IO::unpack(va[u], xa);
+          IO::unpack(vb[u], xb);
+#pragma unroll
+          for (int j = 0; j < kP; ++j) ss = fma2(xa[j], xa[j], fma2(xb[j], xb[j], ss));
+          const float r = __frsqrt_rn(fmaf(head_sum<LPH>(ss.x + ss.y), inv_dh, A.eps));
+          if constexpr (!kBwd) {
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {
+              ya[j] = mul2(both(r), fma2(xb[j], sb[j], mul2(xa[j], ca[j])));
+              yb[j] = mul2(both(r), fma2(xa[j], sa[j], mul2(xb[j], cb[j])));
+            }
+          } else {
+            float2 da[kP], db[kP], m2 = {};
+            IO::unpack(ga[u], da);
+            IO::unpack(gb[u], db);
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {
+              const float2 ua = fma2(da[j], cs[j], mul2(db[j], sn[j]));
+              const float2 ub = fma2(db[j], cs[j], mul2(da[j], make_float2(-sn[j].x, -sn[j].y)));
+              xa[j] = mul2(xa[j], both(r));
+              xb[j] = mul2(xb[j], both(r));
+              dwa[key][j] = fma2(ua, xa[j], dwa[key][j]);
+              dwb[key][j] = fma2(ub, xb[j], dwb[key][j]);
+              da[j] = mul2(ua, wa[j]);
+              db[j] = mul2(ub, wb[j]);
+              m2 = fma2(da[j], xa[j], fma2(db[j], xb[j], m2));
+            }
+            const float m = head_sum<LPH>(m2.x + m2.y) * -inv_dh;
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {
+              ya[j] = mul2(both(r), fma2(xa[j], both(m), da[j]));
+              yb[j] = mul2(both(r), fma2(xb[j], both(m), db[j]));
+            }
+          }
+          if (h < heads && active) {
+            *reinterpret_cast<Vec*>(y0 + h * A.dh + offa) = IO::pack(ya);
+            *reinterpret_cast<Vec*>(y0 + h * A.dh + offb) = IO::pack(yb);
+          }
         }
       }
     }
@@ -238,15 +276,17 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kP; ++j) {
+        float v[4] = {dwa[e][j].x, dwa[e][j].y, dwb[e][j].x, dwb[e][j].y};
 #pragma unroll
-        for (int o = LPH; o < 32; o <<= 1) {
-          dwa[e][j] += __shfl_xor_sync(0xFFFFFFFFu, dwa[e][j], o);
-          dwb[e][j] += __shfl_xor_sync(0xFFFFFFFFu, dwb[e][j], o);
-        }
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int o = LPH; o < 32; o <<= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
         if (sub == 0 && active) {
-          sums[warp][e][offa + j] = dwa[e][j];
-          sums[warp][e][offb + j] = dwb[e][j];
+          sums[warp][e][offa + 2 * j] = v[0];
+          sums[warp][e][offa + 2 * j + 1] = v[1];
+          sums[warp][e][offb + 2 * j] = v[2];
+          sums[warp][e][offb + 2 * j + 1] = v[3];
         }
       }
     __syncthreads();
@@ -281,29 +321,52 @@ __global__ void __launch_bounds__(1024)
   if (threadIdx.x == 0 && out < n) (out < dh ? dwq[out] : dwk[out - dh]) = s;
 }
 
-constexpr int kMaxBlocks = 148 * 4;   // blocks of a launch: four per SM
+// Blocks of a launch: as many as the SMs hold (four forward, three backward, whose sums
+// then are few), walking the tokens.
+int most_blocks(bool bwd) { return 148 * (bwd ? 3 : 4); }
 
-int n_blocks(int64_t n_tokens, int parts) {
-  const int64_t b = (n_tokens * parts + kWarps - 1) / kWarps;
-  return static_cast<int>(b < kMaxBlocks ? b : kMaxBlocks);
-}
+// Whether lanes take eight elements of either half (16-byte loads of bf16): the halves of
+// the rotated part and the rest must be made of whole such pieces. 16384 tokens of 24 heads
+// of 128: 57 us with four, WIDE us with eight.
+bool wide_lanes(tg_dtype dtype, int dh, int rot) { return dtype == TG_BF16 && dh % 16 == 0 && rot % 16 == 0; }
 
 // Warps per token: one, unless there are too few tokens to fill the machine.
-int warps_per_token(int64_t n_tokens, int heads, int dh) {
-  const int hpw = dh <= 64 ? 4 : dh <= 128 ? 2 : 1;
-  const int most = (heads + hpw - 1) / hpw;
-  int64_t p = kMaxBlocks * static_cast<int64_t>(kWarps) / (n_tokens > 0 ? n_tokens : 1);
+int warps_per_token(int64_t n_tokens, int heads, int lanes, bool bwd) {
+  const int hpw = 32 / lanes, most = (heads + hpw - 1) / hpw;
+  int64_t p = most_blocks(bwd) * static_cast<int64_t>(kWarps) / (n_tokens > 0 ? n_tokens : 1);
   if (p < 1) p = 1;
   return static_cast<int>(p < most ? p : most);
 }
+int lanes_of(int dh, int e) {
+  int lanes = 8;
+  while (lanes * 2 * e < dh) lanes *= 2;
+  return lanes;
+}
+int n_blocks(int64_t n_tokens, int parts, bool bwd) {
+  const int64_t b = (n_tokens * parts + kWarps - 1) / kWarps, most = most_blocks(bwd);
+  return static_cast<int>(b < most ? b : most);
+}
 
-template <typename T, bool kBwd>
-tg_status launch_norm(const NormRopeArgs& a, int blocks, cudaStream_t st) {
-  if (a.dh <= 64)
-    return tg::launch(norm_rope_kernel<T, 8, kBwd>, dim3(blocks), dim3(kThreads), 0, st, 0, a);
-  if (a.dh <= 128)
-    return tg::launch(norm_rope_kernel<T, 16, kBwd>, dim3(blocks), dim3(kThreads), 0, st, 0, a);
-  return tg::launch(norm_rope_kernel<T, 32, kBwd>, dim3(blocks), dim3(kThreads), 0, st, 0, a);
+template <typename T, int E, bool kBwd>
+tg_status launch_lanes(const NormRopeArgs& a, int lanes, int blocks, cudaStream_t st) {
+  const dim3 g(blocks), b(kThreads);
+  if (lanes == 8) return tg::launch(norm_rope_kernel<T, E, 8, kBwd>, g, b, 0, st, 0, a);
+  if (lanes == 16) return tg::launch(norm_rope_kernel<T, E, 16, kBwd>, g, b, 0, st, 0, a);
+  if constexpr (E == 4) return tg::launch(norm_rope_kernel<T, E, 32, kBwd>, g, b, 0, st, 0, a);
+  return TG_ERR_UNSUPPORTED;   // not reached: 16 lanes of 16 elements hold the widest head
+}
+
+// Fills in what follows from the sizes and launches.
+template <bool kBwd>
+tg_status launch_norm(NormRopeArgs a, tg_dtype dtype, float rope_base, int* blocks, cudaStream_t st) {
+  const bool wide = wide_lanes(dtype, a.dh, a.rot);
+  const int lanes = lanes_of(a.dh, wide ? 8 : 4);
+  a.ratio = a.rot ? exp(-2.0 / a.rot * log(static_cast<double>(rope_base))) : 0.0;
+  a.parts = warps_per_token(a.n_tokens, a.n_hq, lanes, kBwd);
+  *blocks = n_blocks(a.n_tokens, a.parts, kBwd);
+  if (dtype == TG_F32) return launch_lanes<float, 4, kBwd>(a, lanes, *blocks, st);
+  return wide ? launch_lanes<__nv_bfloat16, 8, kBwd>(a, lanes, *blocks, st)
+              : launch_lanes<__nv_bfloat16, 4, kBwd>(a, lanes, *blocks, st);
 }
 
 // What both directions ask of their arguments; es is the element size.
@@ -347,18 +410,17 @@ extern "C" tg_status tg_qk_norm_rope(const void* q, int64_t q_stride, const void
   a.wq = q_weight, a.wk = k_weight, a.pos = pos;
   a.n_tokens = n_tokens, a.n_hq = n_hq, a.n_hkv = n_hkv, a.dh = head_dim, a.rot = rot_dim;
   a.eps = eps;
-  a.ratio = rot_dim ? exp(-2.0 / rot_dim * log(static_cast<double>(rope_base))) : 0.0;
-  a.parts = warps_per_token(n_tokens, n_hq + n_hkv, head_dim);
-  const int blocks = n_blocks(n_tokens, a.parts);
-  return dtype == TG_BF16 ? launch_norm<__nv_bfloat16, false>(a, blocks, stream)
-                          : launch_norm<float, false>(a, blocks, stream);
+  int blocks;
+  return launch_norm<false>(a, dtype, rope_base, &blocks, stream);
 }
 
 extern "C" size_t tg_qk_norm_rope_bwd_workspace_size(int64_t n_tokens, int n_hq, int n_hkv,
                                                      int head_dim) {
   if (n_tokens <= 0 || n_hq <= 0 || n_hkv <= 0 || head_dim <= 0 || head_dim > kMaxDh) return 0;
-  return static_cast<size_t>(n_blocks(n_tokens, warps_per_token(n_tokens, n_hq + n_hkv, head_dim))) *
-         2 * head_dim * sizeof(float);
+  // the most blocks that either type and any rotation takes
+  const int64_t warps = n_tokens * (static_cast<int64_t>(n_hq) + n_hkv);
+  const int64_t b = (warps + kWarps - 1) / kWarps, most = most_blocks(true);
+  return static_cast<size_t>(b < most ? b : most) * 2 * head_dim * sizeof(float);
 }
 
 extern "C" tg_status tg_qk_norm_rope_bwd(
@@ -395,14 +457,10 @@ extern "C" tg_status tg_qk_norm_rope_bwd(
   a.wq = q_weight, a.wk = k_weight, a.pos = pos;
   a.n_tokens = n_tokens, a.n_hq = n_hq, a.n_hkv = n_hkv, a.dh = head_dim, a.rot = rot_dim;
   a.eps = eps;
-  a.ratio = rot_dim ? exp(-2.0 / rot_dim * log(static_cast<double>(rope_base))) : 0.0;
-  a.parts = warps_per_token(n_tokens, n_hq + n_hkv, head_dim);
   a.partial = static_cast<float*>(workspace);
   int blocks = 0;
   if (n_tokens > 0) {
-    blocks = n_blocks(n_tokens, a.parts);
-    const tg_status r = dtype == TG_BF16 ? launch_norm<__nv_bfloat16, true>(a, blocks, stream)
-                                         : launch_norm<float, true>(a, blocks, stream);
+    const tg_status r = launch_norm<true>(a, dtype, rope_base, &blocks, stream);
     if (r != TG_OK) return r;
   }
   return tg::launch(norm_dw_kernel, dim3((2 * head_dim + 31) / 32), dim3(32, 32), 0, stream, 0,
