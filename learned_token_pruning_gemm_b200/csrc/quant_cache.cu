@@ -6,10 +6,10 @@
 //     scale = fl32(max|x| / qmax), qmax = 127 (int8) or 448 (e4m3),
 //     code  = x / scale rounded to the nearest code, ties to even.
 // The code is that of the exact quotient: x * (1/scale) is taken in fp32 and widened
-// by 2^-22 to both sides, which holds the quotient (two roundings of 2^-24 each); only
-// where the two ends round to different codes is the border between them compared
-// with x, and border * scale - x is one exact fused product (at most 5 or 8 bits times
-// 24). Rows of bf16 values meet such borders often, since their quotients are of few
+// by 2^-21 to both sides, which holds the quotient (a reciprocal to 2^-23 and roundings of
+// 2^-24); only where the two ends round to different codes is the border between them
+// compared with x, and border * scale - x is one exact fused product (at most 5 or 8 bits
+// times 24). Rows of bf16 values meet such borders often, since their quotients are of few
 // bits, so a quotient that was rounded first would store other codes.
 // A scale below 2^-60 is stored as 0 with codes 0; a row that holds an infinity or a
 // NaN gets a NaN scale and codes 0, so it reads back as NaN.
@@ -17,8 +17,8 @@
 // tg_quant_cache_read gives rows back: code * scale in fp32, rounded once.
 //
 // Both are bound by memory (append: 2 bytes in and 1 out per value; read: 1 in and 2
-// or 4 out). A warp takes one row (for few rows: part of its heads); dh/8 lanes hold
-// a head, eight values a lane, so the row maximum is a few shuffles.
+// or 4 out). A warp takes one row (for few rows: part of its heads); a head's lanes hold 16
+// values each to write (so that the scale is formed by few) and 8 to read.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxBlocks = 148 * 8;
+constexpr int kMaxBlocks = 148 * 16;
 constexpr float kMinScale = 0x1p-60f;
 constexpr int kMaxBatch = 65535;
 
@@ -62,6 +62,25 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int64_t r,
   return lo < batch ? lo : -1;
 }
 
+// The offsets of up to kSmemBatch sequences and the rows they start at are read once a
+// block: every row then finds its sequence without a load from global memory.
+constexpr int kSmemBatch = 1024;
+struct SeqSmem {
+  int32_t cu[kSmemBatch + 1], start[kSmemBatch];
+};
+struct SeqTable {
+  const int32_t *cu, *start;   // start: null for 0
+};
+__device__ __forceinline__ SeqTable seq_table(const QuantArgs& A, SeqSmem& S) {
+  if (A.batch > kSmemBatch) return SeqTable{A.cu, A.start};
+  for (int b = threadIdx.x; b <= A.batch; b += kThreads) {
+    S.cu[b] = A.cu[b];
+    if (b < A.batch) S.start[b] = A.start ? A.start[b] : 0;
+  }
+  __syncthreads();
+  return SeqTable{S.cu, S.start};
+}
+
 // A sequence's rows as the call describes them, and whether they fit.
 struct SeqRows {
   int64_t first;   // its first packed row
@@ -69,12 +88,12 @@ struct SeqRows {
   int64_t start;   // cache row of the first
   bool ok;
 };
-__device__ __forceinline__ SeqRows seq_rows(const QuantArgs& A, int b, bool reading) {
+__device__ __forceinline__ SeqRows seq_rows(const QuantArgs& A, const SeqTable& Q, int b, bool reading) {
   SeqRows s;
-  const int64_t c0 = A.cu[b], c1 = A.cu[b + 1];
+  const int64_t c0 = Q.cu[b], c1 = Q.cu[b + 1];
   s.first = c0;
   s.n = c1 - c0;
-  s.start = A.start ? A.start[b] : 0;
+  s.start = Q.start ? Q.start[b] : 0;
   int64_t top = A.cap;
   if (reading) {
     const int64_t len = A.cache_len[b];
@@ -86,41 +105,53 @@ __device__ __forceinline__ SeqRows seq_rows(const QuantArgs& A, int b, bool read
 
 // ---- codes ----
 
+// Two quotients to two codes, as the low and high byte of 16 bits.
 template <bool kE4m3>
-struct Code;
-template <>
-struct Code<false> {
-  static constexpr float kMax = 127.f;
-  static __device__ __forceinline__ int of(float y) { return __float2int_rn(y); }
-  static __device__ __forceinline__ float value(int c) { return static_cast<float>(c); }
-  static __device__ __forceinline__ uint32_t bits(int c) { return static_cast<uint32_t>(c) & 0xFFu; }
-};
-template <>
-struct Code<true> {
-  static constexpr float kMax = 448.f;
-  static __device__ __forceinline__ int of(float y) {
+__device__ __forceinline__ uint32_t codes_of(float y0, float y1) {
+  if constexpr (kE4m3) {
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(y));
-    return r & 0xFF;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y1), "f"(y0));
+    return r;
+  } else {   // 1.5 * 2^23 + y has round(y) in its last bits (|y| <= 127), ties to even
+    const uint32_t a = __float_as_uint(y0 + 12582912.f), b = __float_as_uint(y1 + 12582912.f);
+    return __byte_perm(a, b, 0x0040) & 0xFFFFu;
   }
-  static __device__ __forceinline__ float value(int c) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
-  }
-  static __device__ __forceinline__ uint32_t bits(int c) { return static_cast<uint32_t>(c); }
-};
-
+}
 template <bool kE4m3>
-__device__ __forceinline__ uint32_t encode(float x, float inv, float scale) {
-  const float y = x * inv;
-  const int lo = Code<kE4m3>::of(y * (1.f - 0x1p-22f)), hi = Code<kE4m3>::of(y * (1.f + 0x1p-22f));
-  if (lo == hi) return Code<kE4m3>::bits(lo);
-  // the quotient lies next to the border m between two codes: compare x with m * scale
-  const float m = 0.5f * (Code<kE4m3>::value(lo) + Code<kE4m3>::value(hi));
+__device__ __forceinline__ float value_of(uint32_t code) {
+  if constexpr (kE4m3) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code & 0xFFu)));
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
+  } else {
+    return static_cast<float>(static_cast<int8_t>(code));
+  }
+}
+
+// The code of x / scale where the rounded quotients to its two sides disagree: the border m
+// between the codes lies next to the quotient, so x is compared with m * scale.
+template <bool kE4m3>
+__device__ __noinline__ uint32_t border_code(float x, float scale, uint32_t lo, uint32_t hi) {
+  if (lo == hi) return lo;
+  const float m = 0.5f * (value_of<kE4m3>(lo) + value_of<kE4m3>(hi));
   const float d = fmaf(-m, scale, x) * (x < 0.f ? -1.f : 1.f);
-  const bool up = d > 0.f || (d == 0.f && (hi & 1) == 0);
-  return Code<kE4m3>::bits(up ? hi : lo);
+  return d > 0.f || (d == 0.f && (hi & 1) == 0) ? hi : lo;
+}
+
+// The codes of a bf16 pair; inv is 1 / scale to 2^-23.
+template <bool kE4m3>
+__device__ __forceinline__ uint32_t encode2(uint32_t u, float inv, float scale) {
+  const float x0 = __uint_as_float(u << 16), x1 = __uint_as_float(u & 0xFFFF0000u);
+  const float y0 = x0 * inv, y1 = x1 * inv;
+  const uint32_t lo = codes_of<kE4m3>(y0 * (1.f - 0x1p-21f), y1 * (1.f - 0x1p-21f));
+  const uint32_t hi = codes_of<kE4m3>(y0 * (1.f + 0x1p-21f), y1 * (1.f + 0x1p-21f));
+  if (lo == hi) return lo;
+  return border_code<kE4m3>(x0, scale, lo & 0xFFu, hi & 0xFFu) | border_code<kE4m3>(x1, scale, lo >> 8, hi >> 8) << 8;
+}
+template <bool kE4m3>
+__device__ __forceinline__ uint2 encode8(const uint4& x, float inv, float scale) {
+  return make_uint2(encode2<kE4m3>(x.x, inv, scale) | encode2<kE4m3>(x.y, inv, scale) << 16,
+                    encode2<kE4m3>(x.z, inv, scale) | encode2<kE4m3>(x.w, inv, scale) << 16);
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -131,71 +162,88 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 
 template <int DH, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs A) {
-  constexpr int kLph = DH / 8;          // lanes of a head
+  constexpr int kLph = DH / 16;         // lanes of a head
   constexpr int kHpw = 32 / kLph;       // heads side by side
+  constexpr int kU = 2;                 // of them in flight
+  __shared__ SeqSmem S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % kLph, sub = lane / kLph;
   tg::pdl_launch_dependents();
   tg::pdl_wait();
+  const SeqTable Q = seq_table(A, S);
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  // lengths: one warp per sequence, and the record of sequences that do not fit
+  // lengths, and the record of sequences that do not fit
   for (int64_t b = gw * 32 + lane; b < A.batch; b += n_warps * 32) {
-    const SeqRows s = seq_rows(A, static_cast<int>(b), false);
+    const SeqRows s = seq_rows(A, Q, static_cast<int>(b), false);
     if (!s.ok) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
     else if (A.new_len) A.new_len[b] = static_cast<int32_t>(s.start + s.n);
   }
+  const int heads = 2 * A.n_hkv;        // of K, then of V
   const int64_t n_work = A.n_rows * A.parts;
+#pragma unroll 1
   for (int64_t w = gw; w < n_work; w += n_warps) {
-    const int64_t r = w / A.parts;
+    const int64_t r = A.parts == 1 ? w : w / A.parts;
     const int part = static_cast<int>(w - r * A.parts);
-    const int b = find_seq(A.cu, A.batch, r, lane);
+    const int64_t src = A.src_idx ? A.src_idx[r] : r;
+    const bool have = src >= 0 && src < A.n_src;   // a row that is not there is stored as zeros
+    const int b = find_seq(Q.cu, A.batch, r, lane);
     if (b < 0) continue;
-    const SeqRows s = seq_rows(A, b, false);
+    const SeqRows s = seq_rows(A, Q, b, false);
     if (!s.ok || r - s.first >= s.n) continue;
     const int64_t row = static_cast<int64_t>(b) * A.cap + s.start + (r - s.first);
     if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
-    const int64_t src = A.src_idx ? A.src_idx[r] : r;
-    const bool have = src >= 0 && src < A.n_src;   // a row that is not there is stored as zeros
     if (part == 0 && lane == 0) {
       if (!have) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
       A.s_cache[row] = have ? A.s_new[src] : 0.f;
     }
-    // heads of K, then of V: part*kHpw + sub, then every parts*kHpw-th
-    for (int h0 = part * kHpw; h0 < 2 * A.n_hkv; h0 += A.parts * kHpw) {
-      const int h = h0 + sub;
-      const bool val = h >= A.n_hkv, in = h < 2 * A.n_hkv;
-      const int head = val ? h - A.n_hkv : h;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (in && have)
-        x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(val ? A.v : A.k) +
-                                            (src * A.n_hkv + head) * DH + 8 * c);
-      // bf16 magnitudes order as their bits do, infinities and NaN on top
-      uint32_t m = max_u16x2(max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                             max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    // heads part*kHpw + sub, then every parts*kHpw-th
+    const int step = A.parts * kHpw;
+#pragma unroll 1
+    for (int h0 = part * kHpw; h0 < heads; h0 += kU * step) {
+      uint4 x[kU][2];
 #pragma unroll
-      for (int o = kLph / 2; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      m = max(m >> 16, m & 0xFFFFu);
-      const bool finite = m < 0x7F80u;
-      float scale = __fdiv_rn(__uint_as_float(m << 16), Code<kE4m3>::kMax);
-      if (scale < kMinScale) scale = 0.f;
-      uint32_t w0 = 0, w1 = 0;
-      if (finite && scale > 0.f) {
-        const float inv = __frcp_rn(scale);
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t e0 = encode<kE4m3>(__uint_as_float(u[j] << 16), inv, scale);
-          const uint32_t e1 = encode<kE4m3>(__uint_as_float(u[j] & 0xFFFF0000u), inv, scale);
-          const uint32_t e = (e0 | e1 << 8) << (16 * (j & 1));
-          if (j < 2) w0 |= e;
-          else w1 |= e;
+      for (int u = 0; u < kU; ++u) {
+        const int h = h0 + u * step + sub;
+        const bool val = h >= A.n_hkv;
+        x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+        if (h < heads && have) {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(val ? A.v : A.k) +
+                                                          (src * A.n_hkv + (val ? h - A.n_hkv : h)) * DH + 16 * c);
+          x[u][0] = p[0];
+          x[u][1] = p[1];
         }
       }
-      if (in) {
-        const int64_t hr = row * A.n_hkv + head;
-        *reinterpret_cast<uint2*>((val ? A.vc : A.kc) + hr * DH + 8 * c) = make_uint2(w0, w1);
-        if (c == 0) (val ? A.vs : A.ks)[hr] = finite ? scale : __uint_as_float(0x7FC00000u);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int h = h0 + u * step + sub;
+        const bool val = h >= A.n_hkv;
+        // bf16 magnitudes order as their bits do, infinities and NaN on top
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          m = max_u16x2(m, max_u16x2(max_u16x2(x[u][i].x & 0x7FFF7FFFu, x[u][i].y & 0x7FFF7FFFu),
+                                     max_u16x2(x[u][i].z & 0x7FFF7FFFu, x[u][i].w & 0x7FFF7FFFu)));
+#pragma unroll
+        for (int o = kLph / 2; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        m = max(m >> 16, m & 0xFFFFu);
+        const bool finite = m < 0x7F80u;
+        // max / qmax rounded once to fp32: the quotient of eight bits by qmax lies far more than
+        // a 64-bit product's 2^-52 from any border between two fp32 values
+        float scale = static_cast<float>(static_cast<double>(__uint_as_float(m << 16)) * (1.0 / (kE4m3 ? 448.0 : 127.0)));
+        if (scale < kMinScale) scale = 0.f;
+        uint2 a = make_uint2(0, 0), b2 = a;
+        if (finite && scale > 0.f) {
+          float inv;
+          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+          a = encode8<kE4m3>(x[u][0], inv, scale);
+          b2 = encode8<kE4m3>(x[u][1], inv, scale);
+        }
+        if (h < heads) {
+          const int64_t hr = row * A.n_hkv + (val ? h - A.n_hkv : h);
+          *reinterpret_cast<uint4*>((val ? A.vc : A.kc) + hr * DH + 16 * c) = make_uint4(a.x, a.y, b2.x, b2.y);
+          if (c == 0) (val ? A.vs : A.ks)[hr] = finite ? scale : __uint_as_float(0x7FC00000u);
+        }
       }
     }
   }
@@ -208,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) quant_len_kernel(const QuantArgs A, 
   tg::pdl_wait();
   const int b = blockIdx.x * kThreads + threadIdx.x;
   if (b >= A.batch) return;
-  const SeqRows s = seq_rows(A, b, false);
+  const SeqRows s = seq_rows(A, SeqTable{A.cu, A.start}, b, false);
   if (s.ok) len[b] = static_cast<int32_t>(s.start + s.n);
 }
 
@@ -235,19 +283,21 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const QuantArgs A)
   constexpr int kHpw = 32 / kLph;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % kLph, sub = lane / kLph;
+  __shared__ SeqSmem S;
   tg::pdl_launch_dependents();
   tg::pdl_wait();
+  const SeqTable Q = seq_table(A, S);
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t b = gw * 32 + lane; b < A.batch; b += n_warps * 32)
-    if (!seq_rows(A, static_cast<int>(b), true).ok) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
+    if (!seq_rows(A, Q, static_cast<int>(b), true).ok) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
   const int64_t n_work = A.n_rows * A.parts;
   for (int64_t w = gw; w < n_work; w += n_warps) {
-    const int64_t r = w / A.parts;
+    const int64_t r = A.parts == 1 ? w : w / A.parts;
     const int part = static_cast<int>(w - r * A.parts);
-    const int b = find_seq(A.cu, A.batch, r, lane);
+    const int b = find_seq(Q.cu, A.batch, r, lane);
     if (b < 0) continue;
-    const SeqRows s = seq_rows(A, b, true);
+    const SeqRows s = seq_rows(A, Q, b, true);
     if (!s.ok || r - s.first >= s.n) continue;
     const int64_t row = static_cast<int64_t>(b) * A.cap + s.start + (r - s.first);
     if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
@@ -291,13 +341,14 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const QuantArgs A)
   }
 }
 
-// Warps per row: one, unless there are too few rows to fill the machine.
-int warps_per_row(int64_t n_rows, int n_hkv, int dh) {
-  const int hpw = 32 / (dh / 8);
+// Warps per row: one, unless there are too few rows to give every warp of the machine four
+// of them.
+int warps_per_row(int64_t n_rows, int n_hkv, int dh, int per_lane) {
+  const int hpw = 32 / (dh / per_lane);
   const int most = (2 * n_hkv + hpw - 1) / hpw;
-  int64_t p = 148 * 4 * static_cast<int64_t>(kWarps) / (n_rows > 0 ? n_rows : 1);
-  if (p < 1) p = 1;
-  return static_cast<int>(p < most ? p : most);
+  const int64_t want = 4 * 148 * 4 * static_cast<int64_t>(kWarps);
+  const int64_t p = n_rows > 0 ? (want + n_rows - 1) / n_rows : 1;
+  return static_cast<int>(p < 1 ? 1 : p < most ? p : most);
 }
 
 int n_blocks(int64_t n_rows, int parts, int batch) {
@@ -344,7 +395,7 @@ extern "C" tg_status tg_quant_cache_append(
   a.ks = k_scale, a.vs = v_scale, a.s_cache = s_cache;
   a.new_len = in_place ? nullptr : cache_len;
   a.n_rows = n_new, a.n_src = n_src, a.batch = batch, a.cap = cap, a.n_hkv = n_hkv;
-  a.parts = warps_per_row(n_new, n_hkv, head_dim);
+  a.parts = warps_per_row(n_new, n_hkv, head_dim, 16);
   a.status = tg::status_word();
   if (!a.status) return TG_ERR_CUDA;
   const dim3 grid(n_blocks(n_new, a.parts, batch)), block(kThreads);
@@ -385,7 +436,7 @@ extern "C" tg_status tg_quant_cache_read(const void* k_cache, const void* v_cach
   a.s_cache = const_cast<float*>(s_cache);
   a.ko = k, a.vo = v, a.so = s;
   a.n_rows = n_rows, a.batch = batch, a.cap = cap, a.n_hkv = n_hkv;
-  a.parts = warps_per_row(n_rows, n_hkv, head_dim);
+  a.parts = warps_per_row(n_rows, n_hkv, head_dim, 8);
   a.status = tg::status_word();
   if (!a.status) return TG_ERR_CUDA;
   const dim3 grid(n_blocks(n_rows, a.parts, batch)), block(kThreads);
