@@ -2,7 +2,7 @@
 // into equal shares.
 //
 // Work units are pieces of `unit` cache rows. An item is a sequence's KV heads, `hw` at a
-// time, and a tile of its query rows; it has the units of its cache. All units of all items
+// time, and a pair of tiles of its query rows (or one tile); it has the units of its cache. All units of all items
 // are numbered in a row, and every CTA takes an equal share of that row, so ragged lengths
 // and few heads fill the machine alike.
 #pragma once
@@ -34,7 +34,7 @@ struct TreeArgs {
   int group, group_inv;   // query heads per KV head; ceil(2^16 / group)
   int tm;             // tokens of a row tile
   int unit;           // keys of a unit
-  int hw, kw;         // KV heads of an item, and warps that share a head's keys of a unit
+  int hw, kw;         // KV heads of an item, and parts (warps, sides) that its keys or rows are split in
   int n_cta;
   int* status;
 };
@@ -53,6 +53,7 @@ __device__ __forceinline__ int2 seq_lens(const TreeArgs& A, int b, bool record) 
   return make_int2(len, dl);
 }
 __device__ __forceinline__ int row_tiles(const TreeArgs& A, int dl) { return (dl + A.tm - 1) / A.tm; }
+__device__ __forceinline__ int row_pairs(const TreeArgs& A, int dl) { return (row_tiles(A, dl) + 1) / 2; }
 __device__ __forceinline__ int key_units(const TreeArgs& A, int keys) { return (keys + A.unit - 1) / A.unit; }
 __device__ __forceinline__ int head_groups(const TreeArgs& A) { return (A.n_hkv + A.hw - 1) / A.hw; }
 // Where the maxima and sums of the partials begin.
@@ -94,7 +95,7 @@ __device__ __forceinline__ int count_units(const TreeArgs& A, const TreeSeqs& S)
     const int2 l = seq_lens(A, b, blockIdx.x == 0);
     S.len[b] = l.x;
     S.dl[b] = static_cast<uint8_t>(l.y);
-    S.base[b + 1] = l.y ? head_groups(A) * row_tiles(A, l.y) * key_units(A, l.x) : 0;
+    S.base[b + 1] = l.y ? head_groups(A) * row_pairs(A, l.y) * key_units(A, l.x) : 0;
   }
   __syncthreads();
   if (tid < 32) {

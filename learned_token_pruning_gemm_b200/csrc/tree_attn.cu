@@ -11,25 +11,31 @@
 // Here the rows are packed into M = 128 tiles (row r is token r / G, head r % G) and both
 // products run on the tensor cores with accumulators in TMEM; up to 32 rows of head dim 128
 // take the kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128
-// cache rows; what a CTA has of an item it leaves as a partial (max, sum, O), and the
+// cache rows; what a CTA has of an item it leaves as partials (max, sum, O), and the
 // kernel at the end adds the partials up in CTA order, so results do not depend on timing,
 // and brings in the drafted rows that each token sees.
+//
+// A CTA has two sides, each with its own softmax warps (a thread a row), S buffers and O in
+// TMEM. The sides take the two row tiles of an item, which then share every K and V tile
+// and its widening; of an item of one row tile they take half of every unit's keys each,
+// and each leaves a partial. A job is 64 keys of a side; it has two S buffers, so that its
+// products run while the softmax is at the job before.
 //
 // Per CTA, pipelines run over the units:
 //   warp 0       K tiles by TMA (bf16: into the operand ring; codes: K and V codes into a
 //                raw ring). A bf16 tile that ends inside is copied row by row.
 //   warp 3       V tiles likewise (bf16 cache)
 //   warp 2       the rows' queries, and per key: score, scales (a ring of four tiles)
-//   warps 12-19  codes only: widen the raw tiles into fp16 operand tiles. Codes are exact in
+//   warps 12-15  codes only: widen the raw tiles into fp16 operand tiles. Codes are exact in
 //                fp16, so scales are applied in fp32, to logits and weights.
-//   warp 1       MMA issuer (one thread): S_0, .., PV_0, S_n, PV_1, ...; S_j = Q K_j^T into one
-//                of kS 128-column TMEM buffers, O += P_j V_j with P_j read from TMEM (it
-//                overwrites S_j) and V_j as an MN-major shared-memory operand.
-//   warps 4-11   softmax, 16 rows each, those with rows only: logits in the log2 domain less
-//                the row's running reference, which moves only when one exceeds it by more
+//   warp 1       MMA issuer (one thread), the sides in turn: S_0, S_1, then PV_k, S_{k + 2}, ..;
+//                S = Q K^T into one of the side's TMEM buffers, O += P V with P read from TMEM
+//                (it overwrites S) and V as an MN-major shared-memory operand.
+//   warps 4-11   softmax, four warps a side, those with rows only: logits in the log2 domain
+//                less the row's running reference, which moves only when one exceeds it by more
 //                than it may (O is then rescaled in TMEM).
-// The parity waits are exact for the reasons given at the gated attention's kernel: S_g is
-// issued after PV_{g - kS}, and a softmax warp is never more than kS tiles ahead.
+// A side's S_k is issued after its PV_{k - 2}, and products end in the order they are issued:
+// when S_k is there, all but PV_{k - 1} are done, so no parity wait is passed by.
 #include <type_traits>
 
 #include "tree.cuh"
@@ -44,30 +50,30 @@ using tg::wait;
 
 constexpr int kBM = 128;           // rows of a row tile
 constexpr int kBN = 128;           // keys of a unit
+constexpr int kJob = 64;           // keys of a job
 constexpr int kMaxDraft = 64;
 constexpr int kKeyStages = 4;
-constexpr int kSoftmaxWarps = 8;
-constexpr int kConvWarps = 8;
+constexpr int kSideWarps = 4;      // softmax warps of a side
+constexpr int kConvWarps = 4;
 constexpr int kMaxCtas = 148;      // one per SM
 constexpr uint32_t kHalfBytes = kBN * 128;  // 64 columns of 128 rows, bf16, 128-byte swizzle
-constexpr uint32_t kTmemCols = 512, kColO = 384;
+constexpr uint32_t kTmemCols = 512, kColO = 256;   // S at 0 and 128, O at 256 and 384
 
 template <int DH, bool kQ>
 struct Cfg {
   static constexpr int kHalves = DH / 64;
-  static constexpr int kS = kQ ? 2 : 3;                                  // S/P buffers in TMEM
-  static constexpr int kK = kQ ? (DH == 128 ? 2 : 3) : (DH == 128 ? 3 : 5);   // K operand tiles
-  static constexpr int kV = kQ ? 2 : DH == 128 ? 2 : 4;                  // V operand tiles
-  static constexpr int kRaw = kQ ? (DH == 128 ? 3 : 8) : 1;              // raw tiles of codes
+  static constexpr int kK = DH == 128 ? 2 : 4;                           // K operand tiles
+  static constexpr int kV = DH == 128 ? (kQ ? 1 : 2) : 4;                // V operand tiles
+  static constexpr int kRaw = kQ ? (DH == 128 ? 3 : 4) : 1;              // raw tiles of codes
   static constexpr int kRawBytes = kQ ? kBN * DH : 16;
-  static constexpr int kThreads = 128 + kSoftmaxWarps * 32 + (kQ ? kConvWarps * 32 : 0);
+  static constexpr int kThreads = 128 + 2 * kSideWarps * 32 + (kQ ? kConvWarps * 32 : 0);
   static constexpr int kFullArrivals = kQ ? kConvWarps : 1;              // a K or V tile is ready
 };
 
 template <int DH, bool kQ>
 struct TreeSmem {
   using C = Cfg<DH, kQ>;
-  uint8_t q[C::kHalves][kHalfBytes];
+  uint8_t q[2][C::kHalves][kHalfBytes];   // by side
   uint8_t k[C::kK][C::kHalves][kHalfBytes];
   uint8_t v[C::kV][C::kHalves][kHalfBytes];
   uint8_t raw[C::kRaw][C::kRawBytes];
@@ -80,34 +86,33 @@ struct TreeSmem {
   uint64_t v_full[C::kV], v_empty[C::kV];
   uint64_t raw_full[C::kRaw], raw_empty[C::kRaw];
   uint64_t b_full[kKeyStages], b_empty[kKeyStages];
-  uint64_t s_full[C::kS], p_full[C::kS], o_done[C::kS];
-  uint64_t o_free;
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2], o_free[2];   // by side, and by buffer
   uint32_t tmem_base;
   int abort_flag;
 };
 
 __device__ __forceinline__ bool all_alive(bool a) { return __all_sync(0xFFFFFFFFu, a); }
 
-// The order in which the tiles of a quantised cache pass, K one unit ahead of V:
+// The order in which the tiles of a quantised cache pass, K two units ahead of V as S is of O:
 // K_0, K_1, V_0, K_2, V_1, .., K_{n-1}, V_{n-2}, V_{n-1}. Whether turn i is a V.
-__device__ __forceinline__ bool value_turn(int i, int n) {
-  return i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
-}
+__device__ __forceinline__ bool value_turn(int i, int n) { return i == 2 * n - 1 || (i > 0 && (i & 1) == 0); }
 
-// Walks a CTA's units in order: the unit's sequence, KV head, row tile and place among its
-// item's units.
+// Walks a CTA's units in order: the unit's sequence, KV head, pair of row tiles and place
+// among its item's units. two: the pair's second tile is there.
 struct Cursor {
-  int u, u1, b, item, n_items, kvh, mt, j, nt, len, dl;
+  int u, u1, b, item, n_items, kvh, pair, j, nt, len, tiles;
+  bool two;
   __device__ __forceinline__ void load_seq(const TreeArgs& A, const tg::TreeSeqs& s) {
     len = s.len[b];
-    dl = s.dl[b];
+    tiles = tg::row_tiles(A, s.dl[b]);
     nt = (len + kBN - 1) / kBN;
-    n_items = A.n_hkv * tg::row_tiles(A, dl);
+    n_items = A.n_hkv * ((tiles + 1) / 2);
   }
   __device__ __forceinline__ void split_item(const TreeArgs& A) {
-    const int amt = tg::row_tiles(A, dl);
-    kvh = item / amt;
-    mt = item - kvh * amt;
+    const int pairs = (tiles + 1) / 2;
+    kvh = item / pairs;
+    pair = item - kvh * pairs;
+    two = 2 * pair + 1 < tiles;
   }
   __device__ __forceinline__ void start(const TreeArgs& A, const tg::TreeSeqs& s, int first, int n) {
     u = first;
@@ -118,9 +123,9 @@ struct Cursor {
     j = u - s.base[b] - item * nt;
     split_item(A);
   }
-  __device__ __forceinline__ void advance(const TreeArgs& A, const tg::TreeSeqs& s) {
-    ++u;
-    if (++j < nt || u >= u1) return;
+  __device__ __forceinline__ void advance(const TreeArgs& A, const tg::TreeSeqs& s, int by = 1) {   // by: run() at most
+    u += by;
+    if ((j += by) < nt || u >= u1) return;
     j = 0;
     if (++item == n_items) {
       item = 0;
@@ -134,14 +139,6 @@ struct Cursor {
   // units of the current item from here on within the CTA's share
   __device__ __forceinline__ int run() const { return min(nt - j, u1 - u); }
 };
-
-// What the copy of one unit needs to know of it.
-struct Tile {
-  int b, kvh, j, nv;
-};
-__device__ __forceinline__ Tile tile_of(const Cursor& c) {
-  return Tile{c.b, c.kvh, c.j, c.keys()};
-}
 
 // 16 bytes global -> shared, or 16 zero bytes when !ok (src is not read then)
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
@@ -180,25 +177,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// 16 rows by 32 columns: thread l holds (row l/4, column 4i + l%4) in register 2i and
-// the same column of row l/4 + 8 in register 2i + 1.
-__device__ __forceinline__ void tmem_ld_16x128b_x8(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x128b.x8.b32"
-      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32"
-      " [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 // acc += the low (lo) or high (hi) bf16 half of a packed pair, widened exactly
 __device__ __forceinline__ void add_bf16_lo(float& acc, uint32_t u) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, l, %0;\n\t}" : "+f"(acc) : "r"(u));
@@ -213,6 +191,12 @@ template <int N>
 __device__ __forceinline__ void cp_wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// One lane of a converged warp; the compiler then knows that a single thread goes on.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes;
+}
 // Instruction descriptor of an fp16 (kF16) or bf16 product: the format fields are 0 for fp16.
 template <bool kF16>
 constexpr uint32_t idesc(int M, int N, bool b_mn) {
@@ -232,11 +216,11 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
   Smem& S = *reinterpret_cast<Smem*>(smem_raw + pad);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = A.group * A.tm;                    // rows in use of a row tile
-  const int n_act = (rows + 15) / 16;                 // softmax warps with rows
+  const int n_act = (rows + 31) / 32;                 // softmax warps of a side with rows
 
   if (tid == 0) {
     tg::mbar_init(&S.q_full, 1);
-    tg::mbar_init(&S.q_ready, n_act);
+    tg::mbar_init(&S.q_ready, 2 * n_act);
     tg::mbar_init(&S.q_empty, 1);
     for (int s = 0; s < C::kK; ++s) {
       tg::mbar_init(&S.k_full[s], C::kFullArrivals);
@@ -252,14 +236,16 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     }
     for (int s = 0; s < kKeyStages; ++s) {
       tg::mbar_init(&S.b_full[s], 32);
-      tg::mbar_init(&S.b_empty[s], n_act);
+      tg::mbar_init(&S.b_empty[s], 2 * n_act);
     }
-    for (int s = 0; s < C::kS; ++s) {
-      tg::mbar_init(&S.s_full[s], 1);
-      tg::mbar_init(&S.p_full[s], n_act);
-      tg::mbar_init(&S.o_done[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      for (int i = 0; i < 2; ++i) {
+        tg::mbar_init(&S.s_full[s][i], 1);
+        tg::mbar_init(&S.p_full[s][i], n_act);
+        tg::mbar_init(&S.o_done[s][i], 1);
+      }
+      tg::mbar_init(&S.o_free[s], n_act);
     }
-    tg::mbar_init(&S.o_free, n_act);
     S.abort_flag = 0;
     tg::fence_barrier_init();
     tg::tma_prefetch_desc(&tm_q);
@@ -330,25 +316,23 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         wait(&full[i % n_st], (i / n_st) & 1, A.status, nullptr);
     __syncwarp();
   } else if (kQ && warp == 0) {
-    // ---------------- codes by TMA: K_0, K_1, V_0, K_2, V_1, ... ----------------
+    // ---------------- codes by TMA ----------------
     if (lane == 0) {
-      Tile cur = {}, prev = {};
-      int r = 0;
+      int r = 0, row = 0, kvh = 0, last_row = 0, last_kvh = 0;   // of the K tile and the one before
 #pragma unroll 1
-      for (int i = 0; i < 2 * n; ++i) {
-        const bool val = value_turn(i, n);
+      for (; r < 2 * n; ++r) {
+        const bool val = value_turn(r, n);
         if (!val) {
-          prev = cur;
-          cur = tile_of(c);
+          last_row = row, last_kvh = kvh;
+          row = static_cast<int>(static_cast<int64_t>(c.b) * A.cap + c.j * kBN), kvh = c.kvh;
           c.advance(A, Q);
         }
-        const Tile t = val && i < 2 * n - 1 ? prev : cur;
+        const bool before = val && r < 2 * n - 1;
         const int s = r % C::kRaw;
         if (r >= C::kRaw && !wait(&S.raw_empty[s], ((r / C::kRaw) - 1) & 1, A.status, &S.abort_flag)) break;
         tg::mbar_arrive_expect_tx(&S.raw_full[s], C::kRawBytes);
-        tg::tma_load_3d(S.raw[s], val ? &tm_v : &tm_k, &S.raw_full[s], 0,
-                        static_cast<int>(static_cast<int64_t>(t.b) * A.cap + t.j * kBN), t.kvh);
-        ++r;
+        tg::tma_load_3d(S.raw[s], val ? &tm_v : &tm_k, &S.raw_full[s], 0, before ? last_row : row,
+                        before ? last_kvh : kvh);
       }
       if (S.abort_flag)
         for (int i = r > C::kRaw ? r - C::kRaw : 0; i < r; ++i)
@@ -358,16 +342,19 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
   } else if (warp == 2) {
     // ---------------- queries, and what each key brings besides K and V ----------------
     // The keys' data by small asynchronous copies into their ring, kLag tiles before they are
-    // handed on. Keys behind the end read the last one's place: they are masked.
-    constexpr int kLag = kKeyStages - 1;
+    // handed on: with two, the copies that go ahead wait for the tile before the last, not for
+    // the one at work. Keys behind the end read the last one's place: they are masked.
+    constexpr int kLag = kKeyStages - 2;
     Cursor la = c;
     int n_q = 0;
     auto queries = [&](const Cursor& t) {
       if (lane == 0) {
-        tg::mbar_arrive_expect_tx(&S.q_full, C::kHalves * rows * 128);
+        tg::mbar_arrive_expect_tx(&S.q_full, 2 * C::kHalves * rows * 128);
 #pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-          tg::tma_load_3d(S.q[h], &tm_q, &S.q_full, 64 * h, t.kvh * A.group, t.b * A.n_draft + t.mt * A.tm);
+        for (int i = 0; i < 2 * C::kHalves; ++i) {   // one row tile: for either side
+          const int side = i / C::kHalves, h = i % C::kHalves, mt = 2 * t.pair + (t.two ? side : 0);
+          tg::tma_load_3d(S.q[side][h], &tm_q, &S.q_full, 64 * h, t.kvh * A.group, t.b * A.n_draft + mt * A.tm);
+        }
       }
       ++n_q;
       __syncwarp();
@@ -423,367 +410,343 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc<kQ>(kBM, kBN, false);
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = idesc<kQ>(kBM, kJob, false);
       constexpr uint32_t idesc_o = idesc<kQ>(kBM, DH, true);
-      const uint32_t q0 = tg::smem_u32(S.q[0]);
-      auto issue_s = [&](int g) -> bool {
-        const int s = g % C::kK;
-        if (!wait(&S.k_full[s], (g / C::kK) & 1, A.status, &S.abort_flag)) return false;
-        tg::tc_fence_after();
-        const uint32_t k0 = tg::smem_u32(S.k[s][0]);
-        const uint32_t d = tmem + 128u * (g % C::kS);
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-          tg::mma_bf16_ss(d, tg::smem_desc_sw128(q0 + off, 16, 1024),
-                          tg::smem_desc_sw128(k0 + off, 16, 1024), idesc_s, kk != 0);
-        }
-        tg::mma_commit(&S.s_full[g % C::kS]);
-        tg::mma_commit(&S.k_empty[s]);
-        return true;
-      };
+      // descriptors of the first tiles; others by their distance in 16 bytes (14 bits hold them all)
+      const uint64_t desc_q = tg::smem_desc_sw128(tg::smem_u32(S.q[0][0]), 16, 1024);
+      const uint64_t desc_k = tg::smem_desc_sw128(tg::smem_u32(S.k[0][0]), 16, 1024);
+      const uint64_t desc_v = tg::smem_desc_sw128(tg::smem_u32(S.v[0][0]), kHalfBytes, 1024);
       bool alive = true;
-      int g0 = 0;
-      for (int seg = 0; g0 < n && alive; ++seg) {
-        const int nt = c.run();
-        alive = wait(kQ ? &S.q_ready : &S.q_full, seg & 1, A.status, &S.abort_flag);
-        for (int j = 0; j < C::kS && j < nt && alive; ++j) alive = issue_s(g0 + j);
-        if (alive && nt <= C::kS) tg::mma_commit(&S.q_empty);   // every S of the item issued
-        for (int j = 0; j < nt && alive; ++j) {
-          const int g = g0 + j, s = g % C::kV;
-          alive = wait(&S.p_full[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag) &&
-                  wait(&S.v_full[s], (g / C::kV) & 1, A.status, &S.abort_flag);
-          if (alive && j == 0 && seg > 0)
-            alive = wait(&S.o_free, (seg - 1) & 1, A.status, &S.abort_flag);
-          if (!alive) break;
-          tg::tc_fence_after();
-          const uint32_t v0 = tg::smem_u32(S.v[s][0]);
-          const int steps = (c.keys() + 15) / 16;   // rows of V behind these are not set
+      int g0 = 0, jobs[2] = {}, items[2] = {};   // of either side, before this item
 #pragma unroll 1
-          for (int kk = 0; kk < steps; ++kk) {
-            const uint64_t bdesc = tg::smem_desc_sw128(v0 + kk * 16 * 128, kHalfBytes, 1024);
-            tg::mma_bf16_ts(tmem + kColO, tmem + 128u * (g % C::kS) + kk * 8, bdesc, idesc_o, (j | kk) != 0);
+      for (int seg = 0; g0 < n && alive; ++seg) {
+        // Job k of a side is half k & 1 of unit k / 2, of one row tile: half `side` of unit k. The
+        // last unit may have no second half.
+        const int nt = c.run(), sh = c.two ? 1 : 0;
+        const int last_keys = min(kBN, c.len - (c.j + nt - 1) * kBN), no_half = last_keys <= kJob ? 1 : 0;
+        const int n0 = c.two ? 2 * nt - no_half : nt, n1 = c.two ? n0 : nt - no_half;
+        alive = wait(kQ ? &S.q_ready : &S.q_full, seg & 1, A.status, &S.abort_flag);
+#pragma unroll 1
+        for (int k = -2; k < n0 && alive; ++k) {
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const int nj = side ? n1 : n0;
+            if (k >= 0 && k < nj && alive) {
+              const int u = k >> sh, half = sh ? k & 1 : side, g = g0 + u, s = g % C::kV, job = jobs[side] + k;
+              alive = wait(&S.p_full[side][job & 1], (job >> 1) & 1, A.status, &S.abort_flag) &&
+                      wait(&S.v_full[s], (g / C::kV) & 1, A.status, &S.abort_flag);
+              if (alive && k == 0 && items[side] > 0)   // the side's O of the item before has been read
+                alive = wait(&S.o_free[side], (items[side] - 1) & 1, A.status, &S.abort_flag);
+              if (!alive) break;
+              tg::tc_fence_after();
+              const uint64_t v0 = desc_v + ((s * kTileBytes + half * kJob * 128) >> 4);
+              const uint32_t p0 = tmem + 128u * side + 64u * (job & 1), o = tmem + kColO + 128u * side;
+              // rows of V behind the last are not set, but for those up to a multiple of 16
+              const int steps = u == nt - 1 ? (min(kJob, last_keys - half * kJob) + 15) / 16 : kJob / 16;
+#pragma unroll
+              for (int kk = 0; kk < kJob / 16; ++kk)
+                if (kk < steps)
+                  tg::mma_bf16_ts(o, p0 + kk * 8, v0 + (kk * 16 * 128 >> 4), idesc_o, kk > 0 ? 1 : k > 0);
+              tg::mma_commit(&S.o_done[side][job & 1]);
+              // no other job reads this V
+              if (sh ? side == 1 && (half == 1 || k == nj - 1) : side == 1 || k >= n1) tg::mma_commit(&S.v_empty[s]);
+            }
+            const int q = k + 2;
+            if (q < nj && alive) {
+              const int u = q >> sh, half = sh ? q & 1 : side, g = g0 + u, s = g % C::kK, job = jobs[side] + q;
+              alive = wait(&S.k_full[s], (g / C::kK) & 1, A.status, &S.abort_flag);
+              if (!alive) break;
+              tg::tc_fence_after();
+              const uint64_t k0 = desc_k + ((s * kTileBytes + half * kJob * 128) >> 4);
+              const uint32_t d = tmem + 128u * side + 64u * (job & 1);
+#pragma unroll
+              for (int kk = 0; kk < DH / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+                tg::mma_bf16_ss(d, desc_q + ((side * kTileBytes) >> 4) + off, k0 + off, idesc_s, kk != 0);
+              }
+              tg::mma_commit(&S.s_full[side][job & 1]);
+              if (sh ? side == 1 && (half == 1 || q == nj - 1) : side == 1 || q >= n1) tg::mma_commit(&S.k_empty[s]);
+            }
           }
-          tg::mma_commit(&S.o_done[g % C::kS]);
-          tg::mma_commit(&S.v_empty[s]);
-          if (j + C::kS < nt) {
-            alive = issue_s(g + C::kS);
-            if (alive && j + C::kS + 1 == nt) tg::mma_commit(&S.q_empty);
-          }
-          c.advance(A, Q);
+          if (alive && k + 3 == n0) tg::mma_commit(&S.q_empty);   // every S of the item issued
         }
+        jobs[0] += n0;
+        jobs[1] += n1;
+        items[0] += 1;
+        items[1] += n1 > 0;
         g0 += nt;
+        c.advance(A, Q, nt);
       }
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 4 + kSoftmaxWarps) {
-    // ---------------- softmax: one warp per 16 rows ----------------
-    // 16x256b TMEM loads: thread l holds rows ra = l/4 and rb = ra + 8 of the warp's 16
-    // at columns 8i + 2(l%4) + {0, 1}, so a row's keys sit in one quad of threads.
-    const int row0 = (warp & 3) * 32 + ((warp - 4) >> 2) * 16;
-    if (row0 < rows) {
-      const int r2[2] = {row0 + (lane >> 2), row0 + (lane >> 2) + 8};
-      const int cq = 2 * (lane & 3);
-      const uint32_t lane_base = static_cast<uint32_t>(row0) << 16;
-      float ch[2], gh[2], m[2], l[2], nm[2], most[2];
-      int seg = 0;
+  } else if (warp >= 4 && warp < 4 + 2 * kSideWarps) {
+    // ---------------- softmax: one thread per row ----------------
+    const int side = (warp - 4) / kSideWarps, row = (warp & 3) * 32 + lane;
+    if ((warp & 3) < n_act) {
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t s0 = tmem + lane_base + 128u * side, obuf = s0 + kColO;
+      float ch = 0.f, gh = 0.f, l = 0.f, nm = 0.f, most = 0.f;
+      int seg = 0, jobs = 0, item_jobs = 0;   // jobs of this side
       bool first = true, alive = true;
 #pragma unroll 1
       for (int g = 0; g < n; ++g) {
         if (first) {   // a new item
-          float up[2] = {1.f, 1.f};
+          float up = 1.f;
           if constexpr (kQ) {
-            // The queries to fp16, two lanes a row: the row is multiplied by the power of two that
-            // brings its largest value (exponent field x) to [2^8, 2^9), so that values down to
-            // 2^-22 of it stay exact; the inverse joins the row's factor.
+            // The queries to fp16: the row is multiplied by the power of two that brings its
+            // largest value (exponent field x) to [2^8, 2^9), so that values down to 2^-22 of it
+            // stay exact; the inverse joins the row's factor.
             alive = wait(&S.q_full, seg & 1, A.status, &S.abort_flag);
             if (!all_alive(alive)) break;
-            constexpr int kPer = DH / 16;   // 16-byte columns a lane
-            const int row = row0 + (lane >> 1);
-            uint8_t* q = S.q[0] + row * 128 + (DH == 128 ? (lane & 1) * kHalfBytes : 0);
-            const int c0 = DH == 128 ? 0 : 4 * (lane & 1);
-            uint4 x[kPer];
+            uint8_t* q = S.q[side][0] + row * 128;
             uint32_t mx = 0;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              x[k] = *reinterpret_cast<const uint4*>(q + (((c0 + k) ^ (row & 7)) << 4));
-              mx = tg::max_u16x2(mx, tg::max_u16x2(tg::max_u16x2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu),
-                                                   tg::max_u16x2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu)));
+#pragma unroll 4
+            for (int k = 0; k < DH / 8; ++k) {
+              const uint4 x = *reinterpret_cast<const uint4*>(q + (k >> 3) * kHalfBytes + (((k ^ row) & 7) << 4));
+              mx = tg::max_u16x2(mx, tg::max_u16x2(tg::max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                                   tg::max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
             }
-            mx = tg::max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
             const int xp = max(static_cast<int>(max(mx >> 16, mx & 0xFFFFu) >> 7), 9);
-            const float down = __int_as_float((262 - xp) << 23), inv = __int_as_float((xp - 8) << 23);
-#pragma unroll
-            for (int k = 0; k < kPer; ++k)
-              *reinterpret_cast<uint4*>(q + (((c0 + k) ^ (row & 7)) << 4)) =
-                  make_uint4(tg::bf16x2_to_f16x2(x[k].x, down), tg::bf16x2_to_f16x2(x[k].y, down),
-                             tg::bf16x2_to_f16x2(x[k].z, down), tg::bf16x2_to_f16x2(x[k].w, down));
-            up[0] = __shfl_sync(0xFFFFFFFFu, inv, 2 * (lane >> 2));
-            up[1] = __shfl_sync(0xFFFFFFFFu, inv, 2 * (lane >> 2) + 16);
+            const float down = __int_as_float((262 - xp) << 23);
+            up = __int_as_float((xp - 8) << 23);
+#pragma unroll 4
+            for (int k = 0; k < DH / 8; ++k) {
+              uint4* at = reinterpret_cast<uint4*>(q + (k >> 3) * kHalfBytes + (((k ^ row) & 7) << 4));
+              const uint4 x = *at;
+              *at = make_uint4(tg::bf16x2_to_f16x2(x.x, down), tg::bf16x2_to_f16x2(x.y, down),
+                               tg::bf16x2_to_f16x2(x.z, down), tg::bf16x2_to_f16x2(x.w, down));
+            }
             tg::fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) tg::mbar_arrive(&S.q_ready);
           }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tok = tg::token_of(A, r2[e]), hq = c.kvh * A.group + r2[e] - tok * A.group;
-            ch[e] = kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]) * up[e];
-            gh[e] = A.gain[hq] * kLog2e;
-            m[e] = -INFINITY;      // nothing seen: logits as they are, and any of them moves m
-            nm[e] = 0.f;
-            most[e] = -INFINITY;
-            l[e] = 0.f;
-          }
+          // rows behind the last hold anything: with factors of zero they leave the reference alone
+          const int hq = c.kvh * A.group + row - tg::token_of(A, row) * A.group;
+          ch = row < rows ? kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]) * up : 0.f;
+          gh = row < rows ? A.gain[hq] * kLog2e : 0.f;
+          most = -INFINITY;   // nothing seen: logits as they are, and any of them moves the reference
+          nm = l = 0.f;
+          item_jobs = 0;
         }
         const int s = g % kKeyStages;
-        const uint32_t sbuf = tmem + lane_base + 128u * (g % C::kS);
-        alive = wait(&S.s_full[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag) &&
-                wait(&S.b_full[s], (g / kKeyStages) & 1, A.status, &S.abort_flag);
-        if (!all_alive(alive)) { alive = false; break; }
-        tg::tc_fence_after();
-        // 64 keys at a time: half the registers and half the code
+        alive = wait(&S.b_full[s], (g / kKeyStages) & 1, A.status, &S.abort_flag);
         const int nv = c.keys();
 #pragma unroll 1
-        for (int hf = 0; 64 * hf < nv; ++hf) {
-          const float* key = S.key[s][0] + 64 * hf + cq;
-          float z[32];
+        for (int half = c.two ? 0 : side; alive && kJob * half < nv; ++half) {
+          const uint32_t sbuf = s0 + 64u * (jobs & 1);
+          alive = wait(&S.s_full[side][jobs & 1], (jobs >> 1) & 1, A.status, &S.abort_flag);
+          if (!all_alive(alive)) { alive = false; break; }
+          tg::tc_fence_after();
+          // 32 keys at a time: registers and code stay few
+          const int nh = nv - kJob * half;
 #pragma unroll 1
-          for (int pass = 0;; ++pass) {   // twice where the reference moves, never more
+          for (int part = 0; part < kJob / 32 && 32 * part < nh; ++part) {
+            const float4* key = reinterpret_cast<const float4*>(S.key[s][0] + kJob * half + 32 * part);
+            float z[32];
             {
               uint32_t u[32];
-              tg::tmem_ld_16x256b_x8(sbuf + 64u * hf, u);
+              tg::tmem_ld32(sbuf + 32u * part, u);
               tg::tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float2 sk = *reinterpret_cast<const float2*>(key + 8 * i);
+                const float4 sk = key[i];
                 float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
                               __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
-                float lx = 0.f, ly = 0.f;
+                float b[4] = {nm, nm, nm, nm};
                 if constexpr (kQ) {
-                  const float2 ks = *reinterpret_cast<const float2*>(key + kBN + 8 * i);
-                  const float2 lv = *reinterpret_cast<const float2*>(key + 2 * kBN + 8 * i);
+                  const float4 ks = key[kBN / 4 + i], lv = key[2 * (kBN / 4) + i];
                   fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
-                  fmul2(x[2], x[3], x[2], x[3], ks.x, ks.y);
-                  lx = lv.x, ly = lv.y;
+                  fmul2(x[2], x[3], x[2], x[3], ks.z, ks.w);
+                  fadd2(b[0], b[1], lv.x, lv.y, nm, nm);
+                  fadd2(b[2], b[3], lv.z, lv.w, nm, nm);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float b0 = nm[e], b1 = nm[e];
-                  if constexpr (kQ) fadd2(b0, b1, lx, ly, nm[e], nm[e]);
-                  ffma2(b0, b1, gh[e], gh[e], sk.x, sk.y, b0, b1);
-                  ffma2(z[4 * i + 2 * e], z[4 * i + 2 * e + 1], x[2 * e], x[2 * e + 1], ch[e], ch[e], b0, b1);
-                }
+                ffma2(b[0], b[1], gh, gh, sk.x, sk.y, b[0], b[1]);
+                ffma2(b[2], b[3], gh, gh, sk.z, sk.w, b[2], b[3]);
+                ffma2(z[4 * i], z[4 * i + 1], x[0], x[1], ch, ch, b[0], b[1]);
+                ffma2(z[4 * i + 2], z[4 * i + 3], x[2], x[3], ch, ch, b[2], b[3]);
               }
             }
-            if (nv - 64 * hf < 64) {   // keys that are not there
+            if (nh - 32 * part < 32) {   // keys that are not there
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-                  if (64 * hf + 8 * i + cq + f >= nv) z[4 * i + f] = z[4 * i + 2 + f] = -INFINITY;
+              for (int i = 0; i < 32; ++i)
+                if (32 * part + i >= nh) z[i] = -INFINITY;
             }
+            float t0 = fmaxf(z[0], z[1]), t1 = fmaxf(z[2], z[3]);
+#pragma unroll
+            for (int i = 4; i < 32; i += 4) {
+              t0 = fmax3(t0, z[i], z[i + 1]);
+              t1 = fmax3(t1, z[i + 2], z[i + 3]);
+            }
+            const float mx = fmaxf(t0, t1);
             // A row's reference is a whole number at or above its largest logit (fp16 weights: 6
             // below that, to keep small ones exact) when it is set, so that moving it scales by an
             // exact power of two; it moves when a logit exceeds it by 2^8 more, so that bf16 weights
             // stay below 2^8 and fp16 ones below 2^14.
-            constexpr float kLift = kQ ? 6.f : 0.f;
-            float mx[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float t0 = fmaxf(z[2 * e], z[2 * e + 1]), t1 = fmaxf(z[4 + 2 * e], z[5 + 2 * e]);
-#pragma unroll
-              for (int i = 2; i < 8; i += 2) {
-                t0 = fmax3(t0, z[4 * i + 2 * e], z[4 * i + 2 * e + 1]);
-                t1 = fmax3(t1, z[4 * i + 4 + 2 * e], z[4 * i + 5 + 2 * e]);
+            if (__any_sync(0xFFFFFFFFu, mx > most)) {
+              constexpr float kLift = kQ ? 6.f : 0.f;
+              float alpha = 1.f, up = 0.f;   // up: by how much the reference moves
+              if (mx > most) {
+                const float to = nm - (ceilf(mx) - kLift);
+                up = nm - to;
+                nm = to;
+                alpha = most == -INFINITY ? 0.f : tg::exp2_approx(-up);   // 0 where nothing was seen
+                most = kLift + tg::kRescaleThreshold;
+                l *= alpha;
               }
-              mx[e] = fmaxf(t0, t1);
-            }
-            if (pass) {
-              // No logit exceeds its row's reference by more than it may now, but by rounding one
-              // may that is so large that its last place does (rows behind the last hold
-              // anything): it is brought down.
+              __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (z[i] > kLift + tg::kRescaleThreshold) z[i] = kLift + tg::kRescaleThreshold;
-              break;
-            }
-            if (!__any_sync(0xFFFFFFFFu, mx[0] > most[0] || mx[1] > most[1])) break;
-            float alpha[2] = {1.f, 1.f};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
-              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
-              if (mx[e] > most[e]) {
-                const float t = ceilf(mx[e] - nm[e]) - kLift;
-                alpha[e] = tg::exp2_approx(m[e] - t);   // 0 where nothing was seen
-                m[e] = t;
-                nm[e] = -t;
-                most[e] = kLift + tg::kRescaleThreshold;
-                l[e] *= alpha[e];
-              }
-            }
-            if (!first) {   // O must hold PV_{g-1} before it is scaled
-              alive = wait(&S.o_done[(g - 1) % C::kS], ((g - 1) / C::kS) & 1, A.status, &S.abort_flag);
-              if (!all_alive(alive)) { alive = false; break; }
-              tg::tc_fence_after();
+              for (int i = 0; i < 32; ++i) z[i] -= up;
+              if (item_jobs > 0) {   // once O holds the jobs before
+                alive = wait(&S.o_done[side][(jobs - 1) & 1], ((jobs - 1) >> 1) & 1, A.status, &S.abort_flag);
+                __syncwarp();
+                tg::tc_fence_after();
 #pragma unroll 1
-              for (int h = 0; h < C::kHalves; ++h) {
-                uint32_t o[32];
-                const uint32_t at = tmem + lane_base + kColO + 64u * h;
-                tg::tmem_ld_16x256b_x8(at, o);
-                tg::tmem_ld_wait();
+                for (int h = 0; h < DH / 16; ++h) {
+                  uint32_t o[16];
+                  tg::tmem_ld16(obuf + 16u * h, o);
+                  tg::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
-                tg::tmem_st_16x256b_x8(at, o);
-              }
-              tg::tmem_st_wait();
-            }
-            if (hf > 0) {   // and the unit's first weights
-              uint32_t w[16];
-              tg::tmem_st_wait();
-              tmem_ld_16x128b_x8(sbuf, w);
-              tg::tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                if constexpr (kQ) {
-                  const float2 v = tg::f16x2_to_float2(w[i]);
-                  w[i] = tg::pack_f16x2(v.x * alpha[i & 1], v.y * alpha[i & 1]);
-                } else {
-                  w[i] = tg::pack_bf16x2(bf16_lo(w[i]) * alpha[i & 1], bf16_hi(w[i]) * alpha[i & 1]);
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                  tg::tmem_st16(obuf + 16u * h, o);
                 }
               }
-              tmem_st_16x128b_x8(sbuf, w);
-            }
-          }
-          if (!alive) break;
-          // Weights 2^z. Codes: log2 v is part of z, so these are what the codes are multiplied by
-          // and the reference follows their largest; the row sum takes them in fp32, divided by v.
-          // bf16: the row sum adds the rounded weights, so that a key which dominates its row gives
-          // its value exactly.
-          uint32_t pk[16];
-          float sum[2][2] = {};
+              tg::tmem_st_wait();
+#pragma unroll 1
+              for (int h = 0; h < part; ++h) {   // and the job's first weights
+                uint32_t w[16];
+                tg::tmem_ld16(sbuf + 16u * h, w);
+                tg::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float2 iv = {};
-            if constexpr (kQ) iv = *reinterpret_cast<const float2*>(key + 3 * kBN + 8 * i);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p0 = tg::exp2_approx(z[4 * i + 2 * e]), p1 = tg::exp2_approx(z[4 * i + 2 * e + 1]);
-              if constexpr (kQ) {
-                pk[2 * i + e] = tg::pack_f16x2(p0, p1);
-                ffma2(sum[e][0], sum[e][1], p0, p1, iv.x, iv.y, sum[e][0], sum[e][1]);
-              } else {
-                pk[2 * i + e] = tg::pack_bf16x2(p0, p1);
-                add_bf16_lo(sum[e][0], pk[2 * i + e]);
-                add_bf16_hi(sum[e][1], pk[2 * i + e]);
+                for (int i = 0; i < 16; ++i) {
+                  if constexpr (kQ) {
+                    const float2 v = tg::f16x2_to_float2(w[i]);
+                    w[i] = tg::pack_f16x2(v.x * alpha, v.y * alpha);
+                  } else {
+                    w[i] = tg::pack_bf16x2(bf16_lo(w[i]) * alpha, bf16_hi(w[i]) * alpha);
+                  }
+                }
+                tg::tmem_st16(sbuf + 16u * h, w);
               }
             }
-          }
+            // Weights 2^z. Codes: log2 v is part of z, so these are what the codes are multiplied
+            // by and the reference follows their largest; the row sum takes them in fp32, divided by
+            // v. bf16: the row sum adds the rounded weights, so that a key which dominates its row
+            // gives its value exactly.
+            uint32_t pk[16];
+            float sum[4] = {};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) l[e] += sum[e][0] + sum[e][1];
-          tmem_st_16x128b_x8(sbuf + 32u * hf, pk);   // P over S columns that are read
-        }
-        if (!alive) break;
-        __syncwarp();
-        if (lane == 0) tg::mbar_arrive(&S.b_empty[s]);   // this warp is done with the keys' data
-        tg::tmem_st_wait();
-        tg::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tg::mbar_arrive(&S.p_full[g % C::kS]);
-        first = c.run() == 1;   // the last unit of its item here: O is complete after PV_g
-        if (first) {
-          // CTA c and item i (numbered over all sequences): slot c + i grows along the units
-          const int item = (c.b * A.n_hkv + c.kvh) * tg::row_tiles(A, A.n_draft) + c.mt;
-          const int64_t slot = static_cast<int64_t>(blockIdx.x + item) * rows;
+            for (int i = 0; i < 8; ++i) {
+              float p[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
-          }
-          alive = wait(&S.o_done[g % C::kS], (g / C::kS) & 1, A.status, &S.abort_flag);
-          if (!all_alive(alive)) { alive = false; break; }
-          tg::tc_fence_after();
-#pragma unroll 1
-          for (int h = 0; h < C::kHalves; ++h) {   // columns cq and cq + 1 of each 8
-            uint32_t o[32];
-            tg::tmem_ld_16x256b_x8(tmem + lane_base + kColO + 64u * h, o);
-            tg::tmem_ld_wait();
+              for (int e = 0; e < 4; ++e) p[e] = tg::exp2_approx(z[4 * i + e]);
+              if constexpr (kQ) {
+                const float4 iv = key[3 * (kBN / 4) + i];
+                pk[2 * i] = tg::pack_f16x2(p[0], p[1]);
+                pk[2 * i + 1] = tg::pack_f16x2(p[2], p[3]);
+                ffma2(sum[0], sum[1], p[0], p[1], iv.x, iv.y, sum[0], sum[1]);
+                ffma2(sum[2], sum[3], p[2], p[3], iv.z, iv.w, sum[2], sum[3]);
+              } else {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (r2[e] >= rows) continue;
-              float* p = A.part + (slot + r2[e]) * DH + 64 * h + cq;
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint2*>(p + 8 * i) = make_uint2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
+                for (int e = 0; e < 2; ++e) {
+                  pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
+                  add_bf16_lo(sum[2 * e], pk[2 * i + e]);
+                  add_bf16_hi(sum[2 * e + 1], pk[2 * i + e]);
+                }
+              }
             }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tg::tmem_st16(sbuf + 16u * part, pk);   // P over S columns that are read
           }
+          tg::tmem_st_wait();
           tg::tc_fence_before();
           __syncwarp();
-          if (lane == 0) tg::mbar_arrive(&S.o_free);   // O may be overwritten
+          if (lane == 0) tg::mbar_arrive(&S.p_full[side][jobs & 1]);
+          ++jobs;
+          ++item_jobs;
+          if (!c.two) break;
+        }
+        if (!all_alive(alive)) { alive = false; break; }
+        if (lane == 0) tg::mbar_arrive(&S.b_empty[s]);   // this warp is done with the keys' data
+        first = c.run() == 1;   // the last unit of its item here: O is complete after the last PV
+        if (first) {
+          // CTA c and item i (numbered over all sequences): slot c + i grows along the units
+          const int item = (c.b * A.n_hkv + c.kvh) * tg::row_pairs(A, A.n_draft) + c.pair;
+          const int64_t at = (static_cast<int64_t>(blockIdx.x + item) * 2 + side) * rows + row;
+          if (item_jobs > 0) {
+            alive = wait(&S.o_done[side][(jobs - 1) & 1], ((jobs - 1) >> 1) & 1, A.status, &S.abort_flag);
+            if (!all_alive(alive)) { alive = false; break; }
+            tg::tc_fence_after();
+#pragma unroll 1
+            for (int h = 0; h < DH / 32; ++h) {
+              uint32_t o[32];
+              tg::tmem_ld32(obuf + 32u * h, o);
+              tg::tmem_ld_wait();
+              if (row < rows) {
+                uint4* p = reinterpret_cast<uint4*>(A.part + at * DH + 32 * h);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if ((lane & 3) == 0 && r2[e] < rows)
-              *reinterpret_cast<float2*>(tg::part_ml(A, rows, DH) + (slot + r2[e]) * 2) = make_float2(m[e], l[e]);
+                for (int i = 0; i < 8; ++i) p[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
+              __syncwarp();
+            }
+            tg::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tg::mbar_arrive(&S.o_free[side]);   // O may be overwritten
+          }
+          if (row < rows)   // without a job: a sum of nothing, whose O is not read
+            *reinterpret_cast<float2*>(tg::part_ml(A, rows, DH) + at * 2) = make_float2(most == -INFINITY ? most : -nm, l);
           ++seg;
         }
         c.advance(A, Q);
       }
     }
-  } else if (kQ && warp >= 4 + kSoftmaxWarps) {
-    // ---------------- codes to operand tiles, 16 rows a warp ----------------
+  } else if (kQ && warp >= 4 + 2 * kSideWarps) {
+    // ---------------- codes to operand tiles, 32 rows a warp ----------------
     constexpr bool kE4m3 = kType == TG_E4M3;
-    const int cw = warp - 4 - kSoftmaxWarps;
+    const int cw = warp - 4 - 2 * kSideWarps;
     // Eight lanes take one 16-code column of eight rows, so that reads of the swizzled raw
     // tile and stores to the swizzled operand tile both fall into different banks.
     constexpr int kC16 = DH / 16;                          // 16-code columns of a row
     constexpr int kRows = kBN / kConvWarps;                // rows of a warp
     constexpr int kPasses = kRows * kC16 / 32;
     const int rl = lane & 7, cl = lane >> 3;               // row of eight, column of four
-    Tile cur = {}, prev = {};
-    int r = 0, gk = 0, gv = 0;
+    int gk = 0, gv = 0, keys = 0, last_keys = 0;
 #pragma unroll 1
-    for (int i = 0; i < 2 * n; ++i) {
-      const bool val = value_turn(i, n);
+    for (int r = 0; r < 2 * n; ++r) {
+      const bool val = value_turn(r, n);
       if (!val) {
-        prev = cur;
-        cur = tile_of(c);
+        last_keys = keys;
+        keys = c.keys();
         c.advance(A, Q);
       }
-      const Tile t = val && i < 2 * n - 1 ? prev : cur;
-      const int g = val ? gv++ : gk++;
-      const int n_st = val ? C::kV : C::kK, s = g % n_st;
-      uint64_t* full = val ? &S.v_full[s] : &S.k_full[s];
-      uint64_t* empty = val ? &S.v_empty[s] : &S.k_empty[s];
-      uint8_t* dst = val ? S.v[0][0] : S.k[0][0];
-      dst += s * kTileBytes;
+      const int g = val ? gv++ : gk++, n_st = val ? C::kV : C::kK, s = g % n_st;
+      const int nv = val && r < 2 * n - 1 ? last_keys : keys;
+      uint64_t* full = val ? &S.v_full[s % C::kV] : &S.k_full[s % C::kK];
+      uint64_t* empty = val ? &S.v_empty[s % C::kV] : &S.k_empty[s % C::kK];
+      uint8_t* dst = val ? S.v[s % C::kV][0] : S.k[s % C::kK][0];
+      const int rs = r % C::kRaw;
+      if (!all_alive(wait(&S.raw_full[rs], (r / C::kRaw) & 1, A.status, &S.abort_flag))) break;
+      const uint8_t* src = S.raw[rs];
+      uint4 x[kPasses];
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int rr = kRows * cw + 8 * (p / (kC16 / 4)) + rl, cc = cl + 4 * (p % (kC16 / 4));
+        x[p] = *reinterpret_cast<const uint4*>(src + rr * DH + ((DH == 128 ? cc ^ rl : cc ^ ((rl >> 1) & 3)) << 4));
+        if (val && rr >= nv) x[p] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
+      }
+      __syncwarp();
+      if (lane == 0) tg::mbar_arrive(&S.raw_empty[rs]);
       if (g >= n_st && !all_alive(wait(empty, ((g / n_st) - 1) & 1, A.status, &S.abort_flag))) break;
-      {
-        const int rs = r % C::kRaw;
-        if (!all_alive(wait(&S.raw_full[rs], (r / C::kRaw) & 1, A.status, &S.abort_flag))) break;
-        const uint8_t* src = S.raw[0] + rs * C::kRawBytes;
-        uint4 x[kPasses];
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-          const int rr = kRows * cw + 8 * (p / (kC16 / 4)) + rl, cc = cl + 4 * (p % (kC16 / 4));
-          x[p] = *reinterpret_cast<const uint4*>(src + rr * DH + ((DH == 128 ? cc ^ rl : cc ^ ((rl >> 1) & 3)) << 4));
-        }
+      for (int p = 0; p < kPasses; ++p) {
+        const int rr = kRows * cw + 8 * (p / (kC16 / 4)) + rl, cc = cl + 4 * (p % (kC16 / 4));
+        const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+        uint32_t y[8];
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-          const int rr = kRows * cw + 8 * (p / (kC16 / 4)) + rl, cc = cl + 4 * (p % (kC16 / 4));
-          if (val && rr >= t.nv) x[p] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
-          const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-          uint32_t y[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            tg::widen4<kE4m3>(w[e] ^ (kE4m3 ? 0u : 0x80808080u), y[2 * e], y[2 * e + 1]);
-          *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-        }
-        __syncwarp();
-        if (lane == 0) tg::mbar_arrive(&S.raw_empty[rs]);
-        ++r;
+        for (int e = 0; e < 4; ++e)
+          tg::widen4<kE4m3>(w[e] ^ (kE4m3 ? 0u : 0x80808080u), y[2 * e], y[2 * e + 1]);
+        *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
       }
       tg::fence_proxy_async_shared();
       __syncwarp();
@@ -800,7 +763,8 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
 
 // Adds up what the CTAs left of every output row and brings in the drafted rows that its
 // token sees, key by key, so that what it does not see is not even read. kW warps a row: the
-// row's partials (of the CTAs c0 .. c1 that share its item, kw each, in order) and drafted
+// row's partials (of the CTAs c0 .. c1 that share its item, in order: those of a row tile's
+// side, or of all kw parts of its keys) and drafted
 // rows in turn, joined at the end. CTA c's partial of item i (numbered over all sequences)
 // is in slot c + i.
 template <int DH, int kW>
@@ -860,10 +824,12 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
     const tg::Shares share(A, W);
     const int group = kvh / A.hw, hd = kvh - group * A.hw, mt = t / A.tm;
     const int row = (t - mt * A.tm) * A.group + hr - kvh * A.group, rows = A.group * A.tm;
-    const int first = first0 + (group * tg::row_tiles(A, sl.y) + mt) * nt;
+    const bool two = (mt | 1) < tg::row_tiles(A, sl.y);   // a side of its own
+    const int first = first0 + (group * tg::row_pairs(A, sl.y) + mt / 2) * nt;
     const int c0 = share.cta_of(first), c1 = share.cta_of(first + nt - 1);
-    const int slot0 = c0 + (b * tg::head_groups(A) + group) * tg::row_tiles(A, A.n_draft) + mt;
-    const int parts = A.hw * A.kw, n = (c1 - c0 + 1) * A.kw;
+    const int slot0 = c0 + (b * tg::head_groups(A) + group) * tg::row_pairs(A, A.n_draft) + mt / 2;
+    const int parts = A.hw * A.kw, kw = two ? 1 : A.kw, part0 = hd * A.kw + (two ? mt & 1 : 0);
+    const int n = (c1 - c0 + 1) * kw;
     const float* ml = tg::part_ml(A, rows, DH);
     // eight partials at a time, sums and O together
 #pragma unroll 1
@@ -872,8 +838,8 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
       Vec x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i = i0 + kW * k, ci = A.kw == 1 ? i : i / A.kw;
-        const int64_t at = (static_cast<int64_t>(slot0 + ci) * parts + hd * A.kw + (i - ci * A.kw)) * rows + row;
+        const int i = i0 + kW * k, ci = kw == 1 ? i : i / kw;
+        const int64_t at = (static_cast<int64_t>(slot0 + ci) * parts + part0 + (i - ci * kw)) * rows + row;
         v[k] = make_float2(-INFINITY, 0.f);
         x[k] = Vec{};
         if (i < n) {
@@ -892,6 +858,7 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float wk = tg::exp2_approx(v[k].x - base);
+        if (v[k].y == 0.f) continue;   // a part without keys has no O
         L = fmaf(wk, v[k].y, L);
 #pragma unroll
         for (int e = 0; e < kE; ++e) acc[e] = fmaf(wk, reinterpret_cast<const float*>(&x[k])[e], acc[e]);
@@ -979,15 +946,16 @@ struct Plan {
 Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim, bool codes) {
   Plan p;
   const int group = n_hq / n_hkv;
-  p.tm = kBM / group < n_draft ? kBM / group : n_draft;
+  const int most_tm = kBM / group, tiles = (n_draft + most_tm - 1) / most_tm;
+  p.tm = (n_draft + tiles - 1) / tiles;   // tiles alike
   const int rows = group * p.tm;
   p.few = head_dim == 128 && rows <= tg::kTreeRowsMax;
   const int warps = tg::tree_rows_warps(codes, rows);
   p.hw = p.few ? (n_hkv < warps ? n_hkv : warps) : 1;
-  p.kw = p.few ? warps / p.hw : 1;
+  p.kw = p.few ? warps / p.hw : 2;
   p.unit = p.few ? 16 * p.kw : kBN;
   auto units_of = [&](int64_t keys) { return (keys + p.unit - 1) / p.unit; };
-  const int64_t items = static_cast<int64_t>(batch) * ((n_hkv + p.hw - 1) / p.hw) * ((n_draft + p.tm - 1) / p.tm);
+  const int64_t items = static_cast<int64_t>(batch) * ((n_hkv + p.hw - 1) / p.hw) * ((tiles + 1) / 2);
   p.units = items * units_of(max_len);
   const int64_t most = p.few ? tg::tree_rows_ctas(codes, rows) : kMaxCtas;
   // few rows: no fewer than kMinUnits units a CTA, since every CTA leaves a partial
