@@ -15,7 +15,7 @@
 // kernel at the end adds the partials up in CTA order, so results do not depend on timing,
 // and brings in the drafted rows that each token sees.
 //
-// A CTA has two sides, each with its own softmax warps (a thread a row), S buffers and O in
+// A CTA has two sides, each with its own softmax warps, S buffers and O in
 // TMEM. The sides take the two row tiles of an item, which then share every K and V tile
 // and its widening; of an item of one row tile they take half of every unit's keys each,
 // and each leaves a partial. A job is 64 keys of a side; it has two S buffers, so that its
@@ -26,12 +26,12 @@
 //                raw ring). A bf16 tile that ends inside is copied row by row.
 //   warp 3       V tiles likewise (bf16 cache)
 //   warp 2       the rows' queries, and per key: score, scales (a ring of four tiles)
-//   warps 12-15  codes only: widen the raw tiles into fp16 operand tiles. Codes are exact in
+//   warps 20-23  codes only: widen the raw tiles into fp16 operand tiles. Codes are exact in
 //                fp16, so scales are applied in fp32, to logits and weights.
 //   warp 1       MMA issuer (one thread), the sides in turn: S_0, S_1, then PV_k, S_{k + 2}, ..;
 //                S = Q K^T into one of the side's TMEM buffers, O += P V with P read from TMEM
 //                (it overwrites S) and V as an MN-major shared-memory operand.
-//   warps 4-11   softmax, four warps a side, those with rows only: logits in the log2 domain
+//   warps 4-19   softmax, 16 rows a warp, those with rows only: logits in the log2 domain
 //                less the row's running reference, which moves only when one exceeds it by more
 //                than it may (O is then rescaled in TMEM).
 // A side's S_k is issued after its PV_{k - 2}, and products end in the order they are issued:
@@ -53,7 +53,7 @@ constexpr int kBN = 128;           // keys of a unit
 constexpr int kJob = 64;           // keys of a job
 constexpr int kMaxDraft = 64;
 constexpr int kKeyStages = 4;
-constexpr int kSideWarps = 4;      // softmax warps of a side
+constexpr int kSideWarps = 8;      // softmax warps of a side
 constexpr int kConvWarps = 4;
 constexpr int kMaxCtas = 148;      // one per SM
 constexpr uint32_t kHalfBytes = kBN * 128;  // 64 columns of 128 rows, bf16, 128-byte swizzle
@@ -177,6 +177,34 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// 16 rows by 32 columns, as the 16x256b loads of 64 columns
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32"
+      " [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 16 rows by 32 columns: thread l holds (row l/4, column 4i + l%4) in register 2i and
+// the same column of row l/4 + 8 in register 2i + 1.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32"
+      " [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // acc += the low (lo) or high (hi) bf16 half of a packed pair, widened exactly
 __device__ __forceinline__ void add_bf16_lo(float& acc, uint32_t u) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, l, %0;\n\t}" : "+f"(acc) : "r"(u));
@@ -216,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
   Smem& S = *reinterpret_cast<Smem*>(smem_raw + pad);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = A.group * A.tm;                    // rows in use of a row tile
-  const int n_act = (rows + 31) / 32;                 // softmax warps of a side with rows
+  const int n_act = (rows + 15) / 16;                 // softmax warps of a side with rows
 
   if (tid == 0) {
     tg::mbar_init(&S.q_full, 1);
@@ -481,52 +509,64 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 4 + 2 * kSideWarps) {
-    // ---------------- softmax: one thread per row ----------------
-    const int side = (warp - 4) / kSideWarps, row = (warp & 3) * 32 + lane;
-    if ((warp & 3) < n_act) {
-      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t s0 = tmem + lane_base + 128u * side, obuf = s0 + kColO;
-      float ch = 0.f, gh = 0.f, l = 0.f, nm = 0.f, most = 0.f;
+    // ---------------- softmax: one warp per 16 rows ----------------
+    // 16x256b TMEM loads: thread l holds rows ra = l/4 and rb = ra + 8 of the warp's 16
+    // at columns 8i + 2(l%4) + {0, 1}, so a row's keys sit in one quad of threads.
+    const int side = (warp - 4) / kSideWarps, w8 = (warp - 4) % kSideWarps;
+    const int row0 = (w8 & 3) * 32 + (w8 >> 2) * 16;
+    if (row0 < rows) {
+      const int r2[2] = {row0 + (lane >> 2), row0 + (lane >> 2) + 8};
+      const int cq = 2 * (lane & 3);
+      const uint32_t s0 = tmem + (static_cast<uint32_t>(row0) << 16) + 128u * side, obuf = s0 + kColO;
+      float ch[2] = {}, gh[2] = {}, l[2] = {}, nm[2] = {}, most[2] = {};
       int seg = 0, jobs = 0, item_jobs = 0;   // jobs of this side
       bool first = true, alive = true;
 #pragma unroll 1
       for (int g = 0; g < n; ++g) {
         if (first) {   // a new item
-          float up = 1.f;
+          float up[2] = {1.f, 1.f};
           if constexpr (kQ) {
-            // The queries to fp16: the row is multiplied by the power of two that brings its
-            // largest value (exponent field x) to [2^8, 2^9), so that values down to 2^-22 of it
-            // stay exact; the inverse joins the row's factor.
+            // The queries to fp16, two lanes a row: the row is multiplied by the power of two that
+            // brings its largest value (exponent field x) to [2^8, 2^9), so that values down to
+            // 2^-22 of it stay exact; the inverse joins the row's factor.
             alive = wait(&S.q_full, seg & 1, A.status, &S.abort_flag);
             if (!all_alive(alive)) break;
-            uint8_t* q = S.q[side][0] + row * 128;
+            constexpr int kPer = DH / 16;   // 16-byte columns a lane
+            const int row = row0 + (lane >> 1);
+            uint8_t* q = S.q[side][0] + row * 128 + (DH == 128 ? (lane & 1) * kHalfBytes : 0);
+            const int c0 = DH == 128 ? 0 : 4 * (lane & 1);
             uint32_t mx = 0;
 #pragma unroll 4
-            for (int k = 0; k < DH / 8; ++k) {
-              const uint4 x = *reinterpret_cast<const uint4*>(q + (k >> 3) * kHalfBytes + (((k ^ row) & 7) << 4));
+            for (int k = 0; k < kPer; ++k) {
+              const uint4 x = *reinterpret_cast<const uint4*>(q + (((c0 + k) ^ (row & 7)) << 4));
               mx = tg::max_u16x2(mx, tg::max_u16x2(tg::max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
                                                    tg::max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
             }
+            mx = tg::max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
             const int xp = max(static_cast<int>(max(mx >> 16, mx & 0xFFFFu) >> 7), 9);
-            const float down = __int_as_float((262 - xp) << 23);
-            up = __int_as_float((xp - 8) << 23);
+            const float down = __int_as_float((262 - xp) << 23), inv = __int_as_float((xp - 8) << 23);
 #pragma unroll 4
-            for (int k = 0; k < DH / 8; ++k) {
-              uint4* at = reinterpret_cast<uint4*>(q + (k >> 3) * kHalfBytes + (((k ^ row) & 7) << 4));
+            for (int k = 0; k < kPer; ++k) {
+              uint4* at = reinterpret_cast<uint4*>(q + (((c0 + k) ^ (row & 7)) << 4));
               const uint4 x = *at;
               *at = make_uint4(tg::bf16x2_to_f16x2(x.x, down), tg::bf16x2_to_f16x2(x.y, down),
                                tg::bf16x2_to_f16x2(x.z, down), tg::bf16x2_to_f16x2(x.w, down));
             }
+            up[0] = __shfl_sync(0xFFFFFFFFu, inv, 2 * (lane >> 2));
+            up[1] = __shfl_sync(0xFFFFFFFFu, inv, 2 * (lane >> 2) + 16);
             tg::fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) tg::mbar_arrive(&S.q_ready);
           }
           // rows behind the last hold anything: with factors of zero they leave the reference alone
-          const int hq = c.kvh * A.group + row - tg::token_of(A, row) * A.group;
-          ch = row < rows ? kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]) * up : 0.f;
-          gh = row < rows ? A.gain[hq] * kLog2e : 0.f;
-          most = -INFINITY;   // nothing seen: logits as they are, and any of them moves the reference
-          nm = l = 0.f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int hq = c.kvh * A.group + r2[e] - tg::token_of(A, r2[e]) * A.group;
+            ch[e] = r2[e] < rows ? kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]) * up[e] : 0.f;
+            gh[e] = r2[e] < rows ? A.gain[hq] * kLog2e : 0.f;
+            most[e] = -INFINITY;   // nothing seen: logits as they are, and any of them moves the reference
+            nm[e] = l[e] = 0.f;
+          }
           item_jobs = 0;
         }
         const int s = g % kKeyStages;
@@ -538,126 +578,121 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           alive = wait(&S.s_full[side][jobs & 1], (jobs >> 1) & 1, A.status, &S.abort_flag);
           if (!all_alive(alive)) { alive = false; break; }
           tg::tc_fence_after();
-          // 32 keys at a time: registers and code stay few
           const int nh = nv - kJob * half;
+          const float* key = S.key[s][0] + kJob * half + cq;
+          float z[32];
+          // A row's reference is a whole number at or above its largest logit (fp16 weights: 6
+          // below that, to keep small ones exact) when it is set, so that moving it scales by an
+          // exact power of two; it moves when a logit exceeds it by 2^8 more, so that bf16 weights
+          // stay below 2^8 and fp16 ones below 2^14.
+          constexpr float kLift = kQ ? 6.f : 0.f, kMost = kLift + tg::kRescaleThreshold;
 #pragma unroll 1
-          for (int part = 0; part < kJob / 32 && 32 * part < nh; ++part) {
-            const float4* key = reinterpret_cast<const float4*>(S.key[s][0] + kJob * half + 32 * part);
-            float z[32];
-            {
-              uint32_t u[32];
-              tg::tmem_ld32(sbuf + 32u * part, u);
-              tg::tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 sk = key[i];
-                float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
-                              __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
-                float b[4] = {nm, nm, nm, nm};
-                if constexpr (kQ) {
-                  const float4 ks = key[kBN / 4 + i], lv = key[2 * (kBN / 4) + i];
-                  fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
-                  fmul2(x[2], x[3], x[2], x[3], ks.z, ks.w);
-                  fadd2(b[0], b[1], lv.x, lv.y, nm, nm);
-                  fadd2(b[2], b[3], lv.z, lv.w, nm, nm);
-                }
-                ffma2(b[0], b[1], gh, gh, sk.x, sk.y, b[0], b[1]);
-                ffma2(b[2], b[3], gh, gh, sk.z, sk.w, b[2], b[3]);
-                ffma2(z[4 * i], z[4 * i + 1], x[0], x[1], ch, ch, b[0], b[1]);
-                ffma2(z[4 * i + 2], z[4 * i + 3], x[2], x[3], ch, ch, b[2], b[3]);
-              }
-            }
-            if (nh - 32 * part < 32) {   // keys that are not there
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * part + i >= nh) z[i] = -INFINITY;
-            }
-            float t0 = fmaxf(z[0], z[1]), t1 = fmaxf(z[2], z[3]);
-#pragma unroll
-            for (int i = 4; i < 32; i += 4) {
-              t0 = fmax3(t0, z[i], z[i + 1]);
-              t1 = fmax3(t1, z[i + 2], z[i + 3]);
-            }
-            const float mx = fmaxf(t0, t1);
-            // A row's reference is a whole number at or above its largest logit (fp16 weights: 6
-            // below that, to keep small ones exact) when it is set, so that moving it scales by an
-            // exact power of two; it moves when a logit exceeds it by 2^8 more, so that bf16 weights
-            // stay below 2^8 and fp16 ones below 2^14.
-            if (__any_sync(0xFFFFFFFFu, mx > most)) {
-              constexpr float kLift = kQ ? 6.f : 0.f;
-              float alpha = 1.f, up = 0.f;   // up: by how much the reference moves
-              if (mx > most) {
-                const float to = nm - (ceilf(mx) - kLift);
-                up = nm - to;
-                nm = to;
-                alpha = most == -INFINITY ? 0.f : tg::exp2_approx(-up);   // 0 where nothing was seen
-                most = kLift + tg::kRescaleThreshold;
-                l *= alpha;
-              }
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] -= up;
-              if (item_jobs > 0) {   // once O holds the jobs before
-                alive = wait(&S.o_done[side][(jobs - 1) & 1], ((jobs - 1) >> 1) & 1, A.status, &S.abort_flag);
-                __syncwarp();
-                tg::tc_fence_after();
-#pragma unroll 1
-                for (int h = 0; h < DH / 16; ++h) {
-                  uint32_t o[16];
-                  tg::tmem_ld16(obuf + 16u * h, o);
-                  tg::tmem_ld_wait();
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                  tg::tmem_st16(obuf + 16u * h, o);
-                }
-              }
-              tg::tmem_st_wait();
-#pragma unroll 1
-              for (int h = 0; h < part; ++h) {   // and the job's first weights
-                uint32_t w[16];
-                tg::tmem_ld16(sbuf + 16u * h, w);
-                tg::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  if constexpr (kQ) {
-                    const float2 v = tg::f16x2_to_float2(w[i]);
-                    w[i] = tg::pack_f16x2(v.x * alpha, v.y * alpha);
-                  } else {
-                    w[i] = tg::pack_bf16x2(bf16_lo(w[i]) * alpha, bf16_hi(w[i]) * alpha);
-                  }
-                }
-                tg::tmem_st16(sbuf + 16u * h, w);
-              }
-            }
-            // Weights 2^z. Codes: log2 v is part of z, so these are what the codes are multiplied
-            // by and the reference follows their largest; the row sum takes them in fp32, divided by
-            // v. bf16: the row sum adds the rounded weights, so that a key which dominates its row
-            // gives its value exactly.
-            uint32_t pk[16];
-            float sum[4] = {};
+          for (bool again = false;; again = true) {   // twice where the reference moves, never more
+            uint32_t u[32];
+            tg::tmem_ld_16x256b_x8(sbuf, u);
+            tg::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              float p[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) p[e] = tg::exp2_approx(z[4 * i + e]);
+              const float2 sk = *reinterpret_cast<const float2*>(key + 8 * i);
+              float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                            __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
+              float2 lv = {};
               if constexpr (kQ) {
-                const float4 iv = key[3 * (kBN / 4) + i];
-                pk[2 * i] = tg::pack_f16x2(p[0], p[1]);
-                pk[2 * i + 1] = tg::pack_f16x2(p[2], p[3]);
-                ffma2(sum[0], sum[1], p[0], p[1], iv.x, iv.y, sum[0], sum[1]);
-                ffma2(sum[2], sum[3], p[2], p[3], iv.z, iv.w, sum[2], sum[3]);
-              } else {
+                const float2 ks = *reinterpret_cast<const float2*>(key + kBN + 8 * i);
+                lv = *reinterpret_cast<const float2*>(key + 2 * kBN + 8 * i);
+                fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
+                fmul2(x[2], x[3], x[2], x[3], ks.x, ks.y);
+              }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  pk[2 * i + e] = tg::pack_bf16x2(p[2 * e], p[2 * e + 1]);
-                  add_bf16_lo(sum[2 * e], pk[2 * i + e]);
-                  add_bf16_hi(sum[2 * e + 1], pk[2 * i + e]);
-                }
+              for (int e = 0; e < 2; ++e) {
+                float b0 = nm[e], b1 = nm[e];
+                if constexpr (kQ) fadd2(b0, b1, lv.x, lv.y, nm[e], nm[e]);
+                ffma2(b0, b1, gh[e], gh[e], sk.x, sk.y, b0, b1);
+                ffma2(z[4 * i + 2 * e], z[4 * i + 2 * e + 1], x[2 * e], x[2 * e + 1], ch[e], ch[e], b0, b1);
               }
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tg::tmem_st16(sbuf + 16u * part, pk);   // P over S columns that are read
+          if (nh < kJob) {   // keys that are not there
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int f = 0; f < 2; ++f)
+                if (8 * i + cq + f >= nh) z[4 * i + f] = z[4 * i + 2 + f] = -INFINITY;
           }
+          float mx[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t0 = fmaxf(z[2 * e], z[2 * e + 1]), t1 = fmaxf(z[4 + 2 * e], z[5 + 2 * e]);
+#pragma unroll
+            for (int i = 2; i < 8; i += 2) {
+              t0 = fmax3(t0, z[4 * i + 2 * e], z[4 * i + 2 * e + 1]);
+              t1 = fmax3(t1, z[4 * i + 4 + 2 * e], z[4 * i + 5 + 2 * e]);
+            }
+            mx[e] = fmaxf(t0, t1);
+          }
+            if (again) {
+              // No logit exceeds its row's reference by more than it may now, but by rounding one may
+              // that is so large that its last place does: it is brought down.
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (z[i] > kMost) z[i] = kMost;
+              break;
+            }
+            if (!__any_sync(0xFFFFFFFFu, mx[0] > most[0] || mx[1] > most[1])) break;
+            float alpha[2] = {1.f, 1.f};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
+              if (mx[e] > most[e]) {
+                const float to = nm[e] - (ceilf(mx[e]) - kLift);
+                alpha[e] = most[e] == -INFINITY ? 0.f : tg::exp2_approx(to - nm[e]);   // 0 where nothing was seen
+                nm[e] = to;
+                most[e] = kMost;
+                l[e] *= alpha[e];
+              }
+            }
+            if (item_jobs > 0) {   // once O holds the jobs before
+              alive = wait(&S.o_done[side][(jobs - 1) & 1], ((jobs - 1) >> 1) & 1, A.status, &S.abort_flag);
+              __syncwarp();
+              tg::tc_fence_after();
+#pragma unroll 1
+              for (int h = 0; h < DH / 32; ++h) {
+                uint32_t o[16];
+                tmem_ld_16x256b_x4(obuf + 32u * h, o);
+                tg::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
+                tmem_st_16x256b_x4(obuf + 32u * h, o);
+              }
+            }
+          }
+          // Weights 2^z. Codes: log2 v is part of z, so these are what the codes are multiplied
+          // by and the reference follows their largest; the row sum takes them in fp32, divided by
+          // v. bf16: the row sum adds the rounded weights, so that a key which dominates its row
+          // gives its value exactly.
+          uint32_t pk[16];
+          float sum[2][2] = {};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float2 iv = {};
+            if constexpr (kQ) iv = *reinterpret_cast<const float2*>(key + 3 * kBN + 8 * i);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float p0 = tg::exp2_approx(z[4 * i + 2 * e]), p1 = tg::exp2_approx(z[4 * i + 2 * e + 1]);
+              if constexpr (kQ) {
+                pk[2 * i + e] = tg::pack_f16x2(p0, p1);
+                ffma2(sum[e][0], sum[e][1], p0, p1, iv.x, iv.y, sum[e][0], sum[e][1]);
+              } else {
+                pk[2 * i + e] = tg::pack_bf16x2(p0, p1);
+                add_bf16_lo(sum[e][0], pk[2 * i + e]);
+                add_bf16_hi(sum[e][1], pk[2 * i + e]);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[e] += sum[e][0] + sum[e][1];
+          tmem_st_16x128b_x8(sbuf, pk);   // P over S, which is read
           tg::tmem_st_wait();
           tg::tc_fence_before();
           __syncwarp();
@@ -672,29 +707,40 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         if (first) {
           // CTA c and item i (numbered over all sequences): slot c + i grows along the units
           const int item = (c.b * A.n_hkv + c.kvh) * tg::row_pairs(A, A.n_draft) + c.pair;
-          const int64_t at = (static_cast<int64_t>(blockIdx.x + item) * 2 + side) * rows + row;
+          const int64_t slot = (static_cast<int64_t>(blockIdx.x + item) * 2 + side) * rows;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+          }
           if (item_jobs > 0) {
             alive = wait(&S.o_done[side][(jobs - 1) & 1], ((jobs - 1) >> 1) & 1, A.status, &S.abort_flag);
             if (!all_alive(alive)) { alive = false; break; }
             tg::tc_fence_after();
 #pragma unroll 1
-            for (int h = 0; h < DH / 32; ++h) {
-              uint32_t o[32];
-              tg::tmem_ld32(obuf + 32u * h, o);
+            for (int h = 0; h < DH / 32; ++h) {   // columns cq and cq + 1 of each 8
+              uint32_t o[16];
+              tmem_ld_16x256b_x4(obuf + 32u * h, o);
               tg::tmem_ld_wait();
-              if (row < rows) {
-                uint4* p = reinterpret_cast<uint4*>(A.part + at * DH + 32 * h);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              }
+              for (int e = 0; e < 2; ++e)
+                if (r2[e] < rows) {
+                  float* p = A.part + (slot + r2[e]) * DH + 32 * h + cq;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint2*>(p + 8 * i) = make_uint2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
+                }
               __syncwarp();
             }
             tg::tc_fence_before();
             __syncwarp();
             if (lane == 0) tg::mbar_arrive(&S.o_free[side]);   // O may be overwritten
           }
-          if (row < rows)   // without a job: a sum of nothing, whose O is not read
-            *reinterpret_cast<float2*>(tg::part_ml(A, rows, DH) + at * 2) = make_float2(most == -INFINITY ? most : -nm, l);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)   // without a job: a sum of nothing, whose O is not read
+            if ((lane & 3) == 0 && r2[e] < rows)
+              *reinterpret_cast<float2*>(tg::part_ml(A, rows, DH) + (slot + r2[e]) * 2) =
+                  make_float2(most[e] == -INFINITY ? most[e] : -nm[e], l[e]);
           ++seg;
         }
         c.advance(A, Q);
