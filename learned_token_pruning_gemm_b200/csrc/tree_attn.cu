@@ -36,8 +36,6 @@
 //                than it may (O is then rescaled in TMEM).
 // A side's S_k is issued after its PV_{k - 2}, and products end in the order they are issued:
 // when S_k is there, all but PV_{k - 1} are done, so no parity wait is passed by.
-#include <type_traits>
-
 #include "tree.cuh"
 
 namespace {
@@ -808,21 +806,24 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
 }
 
 // Adds up what the CTAs left of every output row and brings in the drafted rows that its
-// token sees, key by key, so that what it does not see is not even read. kW warps a row: the
-// row's partials (of the CTAs c0 .. c1 that share its item, in order: those of a row tile's
-// side, or of all kw parts of its keys) and drafted
-// rows in turn, joined at the end. CTA c's partial of item i (numbered over all sequences)
-// is in slot c + i.
+// token sees, key by key, so that what it does not see is not even read. Eight lanes are a
+// stream with its own running maximum, sum and O (16 or 8 dims a lane); the 4 kW streams of
+// a row take its partials (of the CTAs c0 .. c1 that share its item, in order: those of a
+// row tile's side, or of all kw parts of its keys) and then its drafted rows in turn, two in
+// flight at a time, and are joined in a fixed order. CTA c's partial of item i (numbered over
+// all sequences) is in slot c + i.
 template <int DH, int kW>
 __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant__ TreeArgs A) {
-  constexpr int kE = DH / 32;           // dims of a lane
+  constexpr int kC = DH / 64;           // 8-dim pieces of a lane: dims 64 p + 8 (lane % 8) ..
+  constexpr int kE = 8 * kC;
   constexpr int kRows = 4 / kW;         // rows of a block, neighbouring heads
-  using Vec = typename std::conditional<DH == 128, float4, float2>::type;
-  using Half = typename std::conditional<DH == 128, uint2, uint32_t>::type;
+  constexpr int kNs = 4 * kW;           // streams of a row
+  constexpr int kD = 2;
   __shared__ float red[4][DH + 2];
   tg::pdl_launch_dependents();
   tg::pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp % kW;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i8 = lane & 7;
+  const int stream = (warp % kW) * 4 + (lane >> 3);
   const int hq = blockIdx.x * kRows + warp / kW, t = blockIdx.y, b = blockIdx.z;
   const bool mine = hq < A.n_hq;        // the last block's last warps may have no row
   const int hr = mine ? hq : 0, kvh = hr / A.group;
@@ -831,38 +832,42 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   const int W = A.base[A.batch], first0 = A.base[b];
   const int2 sl = tg::seq_lens(A, b, false);
   uint64_t see = static_cast<uint64_t>(A.mask[bt]);
-  const Half qw = *reinterpret_cast<const Half*>(A.q + (bt * A.n_hq + hr) * DH + kE * lane);
+  uint4 qw[kC];
+#pragma unroll
+  for (int p = 0; p < kC; ++p) qw[p] = *reinterpret_cast<const uint4*>(A.q + (bt * A.n_hq + hr) * DH + 64 * p + 8 * i8);
   const float tau = A.tau[hr], gain = A.gain[hr];
   if (t >= sl.y) return;
-  auto widen = [](const Half& h, float* f) {
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(&h);
+  auto widen = [](const uint4& h, float* f) {
+    const uint32_t u[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
-    for (int e = 0; e < kE; e += 2) {
-      f[e] = bf16_lo(u[e / 2]);
-      f[e + 1] = bf16_hi(u[e / 2]);
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = bf16_lo(u[e]);
+      f[2 * e + 1] = bf16_hi(u[e]);
     }
   };
-  // the warp's drafted rows: visible ones w0, w0 + kW, .., kD in flight at a time
-  constexpr int kD = 4;
+  // the stream's drafted rows: visible ones stream, stream + kNs, ..
   if (sl.y < 64) see &= (1ull << sl.y) - 1;
-  for (int i = 0; i < w0; ++i) see &= see - 1;
-  Half kh[kD], vh[kD];
-  float sd[kD];
+  int left = (__popcll(see) + kNs - 1) / kNs;   // the longest stream's rows
+  for (int i = 0; i < stream; ++i) see &= see - 1;
+  uint4 kh[kD][kC] = {}, vh[kD][kC] = {};
+  float sd[kD] = {};
+  bool has[kD];
   auto drafted = [&]() {
 #pragma unroll
     for (int d = 0; d < kD; ++d) {
-      kh[d] = vh[d] = Half{};
-      sd[d] = 0.f;
-      if (!see) continue;
+      has[d] = see != 0;
+      if (!has[d]) continue;
       const int64_t at = static_cast<int64_t>(b) * A.n_draft + __ffsll(static_cast<long long>(see)) - 1;
-      kh[d] = *reinterpret_cast<const Half*>(A.kd + (at * A.n_hkv + kvh) * DH + kE * lane);
-      vh[d] = *reinterpret_cast<const Half*>(A.vd + (at * A.n_hkv + kvh) * DH + kE * lane);
+#pragma unroll
+      for (int p = 0; p < kC; ++p) {
+        kh[d][p] = *reinterpret_cast<const uint4*>(A.kd + (at * A.n_hkv + kvh) * DH + 64 * p + 8 * i8);
+        vh[d][p] = *reinterpret_cast<const uint4*>(A.vd + (at * A.n_hkv + kvh) * DH + 64 * p + 8 * i8);
+      }
       sd[d] = A.sd[at];
 #pragma unroll
-      for (int i = 0; i < kW; ++i) see &= see - 1;
+      for (int i = 0; i < kNs; ++i) see &= see - 1;
     }
   };
-  int left = (__popcll(see) + kW - 1) / kW;   // rows of this warp
   drafted();
   float M = -INFINITY, L = 0.f, acc[kE] = {};
   const int nt = tg::key_units(A, sl.x);
@@ -877,60 +882,70 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
     const int parts = A.hw * A.kw, kw = two ? 1 : A.kw, part0 = hd * A.kw + (two ? mt & 1 : 0);
     const int n = (c1 - c0 + 1) * kw;
     const float* ml = tg::part_ml(A, rows, DH);
-    // eight partials at a time, sums and O together
 #pragma unroll 1
-    for (int i0 = w0; i0 < n; i0 += 8 * kW) {
-      float2 v[8];
-      Vec x[8];
+    for (int i0 = stream; i0 < n; i0 += kD * kNs) {
+      float2 v[kD];
+      float4 x[kD][2 * kC];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = i0 + kW * k, ci = kw == 1 ? i : i / kw;
+      for (int k = 0; k < kD; ++k) {
+        const int i = i0 + kNs * k, ci = kw == 1 ? i : i / kw;
         const int64_t at = (static_cast<int64_t>(slot0 + ci) * parts + part0 + (i - ci * kw)) * rows + row;
         v[k] = make_float2(-INFINITY, 0.f);
-        x[k] = Vec{};
-        if (i < n) {
-          v[k] = *reinterpret_cast<const float2*>(ml + at * 2);
-          x[k] = *reinterpret_cast<const Vec*>(A.part + at * DH + lane * kE);
-        }
+        if (i >= n) continue;
+        v[k] = *reinterpret_cast<const float2*>(ml + at * 2);
+#pragma unroll
+        for (int p = 0; p < 2 * kC; ++p)
+          x[k][p] = *reinterpret_cast<const float4*>(A.part + at * DH + 64 * (p >> 1) + 8 * i8 + 4 * (p & 1));
       }
       float mb = M;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mb = fmaxf(mb, v[k].x);
+      for (int k = 0; k < kD; ++k) mb = fmaxf(mb, v[k].x);
       const float base = mb == -INFINITY ? 0.f : mb, scale = tg::exp2_approx(M - base);
       M = mb;
       L *= scale;
 #pragma unroll
       for (int e = 0; e < kE; ++e) acc[e] *= scale;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kD; ++k) {
         const float wk = tg::exp2_approx(v[k].x - base);
         if (v[k].y == 0.f) continue;   // a part without keys has no O
         L = fmaf(wk, v[k].y, L);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] = fmaf(wk, reinterpret_cast<const float*>(&x[k])[e], acc[e]);
+        for (int p = 0; p < 2 * kC; ++p) {
+          acc[4 * p] = fmaf(wk, x[k][p].x, acc[4 * p]);
+          acc[4 * p + 1] = fmaf(wk, x[k][p].y, acc[4 * p + 1]);
+          acc[4 * p + 2] = fmaf(wk, x[k][p].z, acc[4 * p + 2]);
+          acc[4 * p + 3] = fmaf(wk, x[k][p].w, acc[4 * p + 3]);
+        }
       }
     }
+    __syncwarp();
   }
-  float qf[kE];
-  widen(qw, qf);
   const float ch = kLog2e / (sqrtf(static_cast<float>(DH)) * tau), gh = gain * kLog2e;
+  float qf[kE];
+#pragma unroll
+  for (int p = 0; p < kC; ++p) widen(qw[p], qf + 8 * p);
 #pragma unroll 1
-  for (; left > 0; left -= kD) {
-    float z[kD], vf[kD][kE], mn = M;
+  for (; left > 0; left -= kD) {   // all streams of the warp together: their shuffles
+    float z[kD], mn = M;
+    uint4 vk[kD][kC];
 #pragma unroll
     for (int d = 0; d < kD; ++d) {
-      float kf[kE];
-      widen(kh[d], kf);
-      widen(vh[d], vf[d]);
       z[d] = 0.f;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) z[d] = fmaf(qf[e], kf[e], z[d]);
+      for (int p = 0; p < kC; ++p) {
+        float kf[8];
+        widen(kh[d][p], kf);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z[d] += __shfl_xor_sync(0xFFFFFFFFu, z[d], o);
-      z[d] = d < left ? fmaf(z[d], ch, gh * sd[d]) : -INFINITY;
+        for (int e = 0; e < 8; ++e) z[d] = fmaf(qf[8 * p + e], kf[e], z[d]);
+        vk[d][p] = vh[d][p];
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) z[d] += __shfl_xor_sync(0xFFFFFFFFu, z[d], o);
+      z[d] = has[d] ? fmaf(z[d], ch, gh * sd[d]) : -INFINITY;
       mn = fmaxf(mn, z[d]);
     }
-    if (left > kD) drafted();
+    drafted();
     const float base = mn == -INFINITY ? 0.f : mn, scale = tg::exp2_approx(M - base);
     M = mn;
     L *= scale;
@@ -942,22 +957,46 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
       const float p = tg::exp2_approx(z[d] - base);
       L += p;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) acc[e] = fmaf(p, vf[d][e], acc[e]);
+      for (int i = 0; i < kC; ++i) {
+        float vf[8];
+        widen(vk[d][i], vf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[8 * i + e] = fmaf(p, vf[e], acc[8 * i + e]);
+      }
     }
+    __syncwarp();
+  }
+  // the warp's streams, then its warps
+  float mw = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, 8));
+  mw = fmaxf(mw, __shfl_xor_sync(0xFFFFFFFFu, mw, 16));
+  const float down = tg::exp2_approx(M - (mw == -INFINITY ? 0.f : mw));
+  L *= down;
+  L += __shfl_xor_sync(0xFFFFFFFFu, L, 8);
+  L += __shfl_xor_sync(0xFFFFFFFFu, L, 16);
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    acc[e] *= down;
+    acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], 8);
+    acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], 16);
   }
   const int64_t at = bt * A.n_hq + hr;
   if constexpr (kW == 1) {
     const float inv = L == 0.f ? 0.f : 1.f / L;   // nothing seen: zeros
-    if (!mine || !tg::in_bounds(at, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)) return;
-    uint32_t y[kE / 2];
+    if (!mine || lane >= 8 || !tg::in_bounds(at, static_cast<int64_t>(A.batch) * A.n_draft * A.n_hq, A.status)) return;
 #pragma unroll
-    for (int e = 0; e < kE; e += 2) y[e / 2] = tg::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    *reinterpret_cast<Half*>(A.out + at * DH + kE * lane) = *reinterpret_cast<const Half*>(y);
+    for (int p = 0; p < kC; ++p) {
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = tg::pack_bf16x2(acc[8 * p + 2 * e] * inv, acc[8 * p + 2 * e + 1] * inv);
+      *reinterpret_cast<uint4*>(A.out + at * DH + 64 * p + 8 * i8) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
   } else {
+    if (lane < 8) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) red[warp][lane * kE + e] = acc[e];
+      for (int e = 0; e < kE; ++e) red[warp][64 * (e >> 3) + 8 * i8 + (e & 7)] = acc[e];
+    }
     if (lane == 0) {
-      red[warp][DH] = M;
+      red[warp][DH] = mw;
       red[warp][DH + 1] = L;
     }
     __syncthreads();
