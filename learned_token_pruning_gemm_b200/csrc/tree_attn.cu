@@ -9,8 +9,8 @@
 // The cache is read once per KV head and serves all drafted tokens and query heads of the
 // group: with R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product and back.
 // Here the rows are packed into M = 128 tiles (row r is token r / G, head r % G) and both
-// products run on the tensor cores with accumulators in TMEM; up to 32 rows of head dim 128
-// take the kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128
+// products run on the tensor cores with accumulators in TMEM; up to 16 rows of head dim
+// 128 over codes take the kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128
 // cache rows; what a CTA has of an item it leaves as partials (max, sum, O), and the
 // kernel at the end adds the partials up in CTA order, so results do not depend on timing,
 // and brings in the drafted rows that each token sees.
@@ -1034,15 +1034,15 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
   const int most_tm = kBM / group, tiles = (n_draft + most_tm - 1) / most_tm;
   p.tm = (n_draft + tiles - 1) / tiles;   // tiles alike
   const int rows = group * p.tm;
-  p.few = head_dim == 128 && rows <= tg::kTreeRowsMax;
-  const int warps = tg::tree_rows_warps(codes, rows);
+  p.few = codes && head_dim == 128 && rows <= tg::kTreeRowsMax;
+  const int warps = tg::tree_rows_warps(rows);
   p.hw = p.few ? (n_hkv < warps ? n_hkv : warps) : 1;
   p.kw = p.few ? warps / p.hw : 2;
   p.unit = p.few ? 16 * p.kw : kBN;
   auto units_of = [&](int64_t keys) { return (keys + p.unit - 1) / p.unit; };
   const int64_t items = static_cast<int64_t>(batch) * ((n_hkv + p.hw - 1) / p.hw) * ((tiles + 1) / 2);
   p.units = items * units_of(max_len);
-  const int64_t most = p.few ? tg::tree_rows_ctas(codes, rows) : kMaxCtas;
+  const int64_t most = p.few ? tg::tree_rows_ctas(rows) : kMaxCtas;
   // few rows: no fewer than kMinUnits units a CTA, since every CTA leaves a partial
   const int64_t want = p.few ? (p.units + kMinUnits - 1) / kMinUnits : p.units;
   p.n_cta = static_cast<int>(want < 1 ? 1 : want < most ? want : most);

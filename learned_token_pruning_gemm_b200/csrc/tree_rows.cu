@@ -1,24 +1,23 @@
-// tg_tree_attention for few rows (drafted tokens x query heads of a KV head, up to 32, head
-// dim 128): the part over the cache. There is little to multiply per byte of cache then,
-// and the 128-row tiles of tree_attn_kernel spend their time in the hand-over between its
-// roles. Here all warps run the same code, straight from a TMA ring into the register
-// fragments of m16n8k16 products, each with its own running reference, sums and O, so
-// nothing joins them but the ring.
+// tg_tree_attention for few rows (drafted tokens x query heads of a KV head, up to 16, head
+// dim 128) over a cache of codes: the part over the cache. There is little to multiply per
+// byte of cache then, and tree_attn_kernel, which widens every code to an operand tile for 128
+// rows, takes longer over the widening than this kernel over everything. Here all warps run
+// the same code, straight from a TMA ring into the register fragments of m16n8k16 products,
+// each with its own running reference, sums and O, so nothing joins them but the ring.
 //
 // A unit is 16 keys a warp: the warps share hw KV heads of the same cache rows (all of them
-// up to four or eight, so that a tile is one contiguous piece of the cache or nearly) and, where there are
-// fewer heads, split the keys in kw parts. Every warp leaves a partial (max, sum, O) per
-// item, and the second kernel adds those up and brings in the drafted rows.
+// up to four or eight, so that a tile is one contiguous piece of the cache or nearly) and, where
+// there are fewer heads, split the keys in kw parts. Every warp leaves a partial (max, sum, O)
+// per item, and the second kernel adds those up and brings in the drafted rows.
 //
 // Products are taken as S^T = K Q^T (16 keys x 8 rows at a time) and O^T = V^T P^T: rows
 // are the short side of a product, so eight rows cost half of sixteen. The weights change
 // from one product's result to the other's operand by a transpose of 8 x 8 in the warp.
 // Any dim may take any place of an inner index or of the 16-high side, as long as both
 // operands agree, so that every thread (g = lane / 4, i = lane % 4) reads 16-byte pieces:
-//   S^T: dims 32 i .. 32 i + 31 of keys g and g + 8 (codes; of a bf16 cache the 8-dim
-//        columns 2 i and 2 i + 1 of both 64-dim halves);
-//   O^T: dims 16 g .. 16 g + 15 (bf16: 8 g .. 8 g + 7 of both halves) of keys 2 i, 2 i + 1,
-//        2 i + 8 and 2 i + 9: product t holds the dims at places 2 t and 2 t + 1 of these.
+//   S^T: dims 32 i .. 32 i + 31 of keys g and g + 8;
+//   O^T: dims 16 g .. 16 g + 15 of keys 2 i, 2 i + 1, 2 i + 8 and 2 i + 9: product t holds the
+//        dims at places 2 t and 2 t + 1 of these.
 // Codes are widened to fp16, which holds them exactly at half the instructions that bf16
 // takes; the queries are then fp16 too, after their largest value is brought near 2^8.
 #include "tree.cuh"
@@ -26,8 +25,6 @@
 namespace {
 
 using tg::TreeArgs;
-using tg::bf16_hi;
-using tg::bf16_lo;
 using tg::bf16x2_to_f16x2;
 using tg::max_u16x2;
 using tg::pack_f16x2;
@@ -37,21 +34,13 @@ using tg::widen4;
 // NT: tiles of eight rows. Several CTAs share an SM, so that one's start and end of an item
 // pass under the others' work; how many goes by registers, then the ring takes the rest of
 // the shared memory.
-struct Shape {
-  int warps, ctas, ring;   // of a CTA; CTAs an SM; tiles
-};
-constexpr Shape shape_of(bool codes, int n_tiles) {
-  if (codes) return n_tiles == 1 ? Shape{8, 2, 5} : n_tiles == 2 ? Shape{4, 3, 7} : Shape{4, 2, 9};
-  return Shape{4, 2, n_tiles == 1 ? 6 : n_tiles == 2 ? 5 : 4};
-}
-template <bool kQ, int NT>
+template <int NT>
 struct Cfg {
-  static constexpr Shape kShape = shape_of(kQ, NT);
-  static constexpr int kWarps = kShape.warps;
+  static constexpr int kWarps = NT == 1 ? 8 : 4;   // of a CTA
+  static constexpr int kCtas = NT == 1 ? 2 : 3;    // an SM
+  static constexpr int kRing = NT == 1 ? 5 : 7;    // tiles
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kHalf = 16 * kWarps * 128;      // 128-byte rows of a tile (bf16: of one half of it)
-  static constexpr int kTile = kHalf * (kQ ? 1 : 2);   // bytes of a K or V tile, at most
-  static constexpr int kRing = kShape.ring;
+  static constexpr int kTile = 16 * kWarps * 128;  // bytes of a K or V tile, at most
   static_assert(kRing >= 4, "a unit's tiles are asked for while the one before is in use");
 };
 
@@ -80,9 +69,9 @@ struct Cursor {
   }
 };
 
-template <bool kQ, int NT>
+template <int NT>
 struct RowSmem {
-  using C = Cfg<kQ, NT>;
+  using C = Cfg<NT>;
   uint8_t tile[C::kRing][C::kTile];
   uint2 q[C::kWarps][NT][8][32];       // B fragments of each warp's queries
   float2 cg[C::kWarps][8 * NT];        // each row's logit factor and gain, log2 domain
@@ -100,22 +89,18 @@ struct RowSmem {
 // Loads tiles as far as the ring reaches (K at even places, V at odd ones): tile t needs
 // tile t - kRing to be consumed by every warp, which is waited for, and all before
 // `consumed` are by this one. One thread.
-template <bool kQ, int NT>
-__device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<kQ, NT>& S, const CUtensorMap* tm_k,
+template <int NT>
+__device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<NT>& S, const CUtensorMap* tm_k,
                                        const CUtensorMap* tm_v, int consumed) {
-  using C = Cfg<kQ, NT>;
+  using C = Cfg<NT>;
   const tg::TreeSeqs Q = S.seqs(A.batch);
   int t = S.issued;
   Cursor c = S.next;
   while (t < consumed + C::kRing && c.u < c.u1) {
     const int s = t % C::kRing;
     if (t >= C::kRing && !wait(&S.empty[s], ((t / C::kRing) - 1) & 1, A.status, &S.abort_flag)) break;
-    const uint32_t half = A.hw * A.unit * 128;
-    tg::mbar_arrive_expect_tx(&S.full[s], kQ ? half : 2 * half);
-    const CUtensorMap* map = t & 1 ? tm_v : tm_k;
-    const int row = c.b * A.cap + c.j * A.unit, kvh = c.group * A.hw;
-    tg::tma_load_3d(S.tile[s], map, &S.full[s], 0, row, kvh);
-    if constexpr (!kQ) tg::tma_load_3d(S.tile[s] + C::kHalf, map, &S.full[s], 64, row, kvh);
+    tg::mbar_arrive_expect_tx(&S.full[s], A.hw * A.unit * 128);
+    tg::tma_load_3d(S.tile[s], t & 1 ? tm_v : tm_k, &S.full[s], 0, c.b * A.cap + c.j * A.unit, c.group * A.hw);
     if (t & 1) c.advance(A, Q);
     ++t;
   }
@@ -123,18 +108,12 @@ __device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<kQ, NT>& S, co
   S.next = c;
 }
 
-// One 16 x 8 x 16 product, bf16 (kF16: fp16) operands, fp32 sums.
-template <bool kF16>
+// One 16 x 8 x 16 product, fp16 operands, fp32 sums.
 __device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-  if constexpr (kF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit values held as product fragments.
@@ -154,16 +133,15 @@ __device__ __forceinline__ void cp8(void* dst, const void* src) {
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <int kType, int NT>
-__global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType != TG_BF16, NT>::kShape.ctas)
+__global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
     tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ TreeArgs A) {
-  constexpr bool kQ = kType != TG_BF16;
   constexpr bool kE4m3 = kType == TG_E4M3;
   constexpr uint32_t kFlip = kType == TG_I8 ? 0x80808080u : 0u;
-  using C = Cfg<kQ, NT>;
+  using C = Cfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (tg::smem_u32(smem_raw) & 1023u)) & 1023u;
-  RowSmem<kQ, NT>& S = *reinterpret_cast<RowSmem<kQ, NT>*>(smem_raw + pad);
+  RowSmem<NT>& S = *reinterpret_cast<RowSmem<NT>*>(smem_raw + pad);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, i4 = lane & 3;
   if (tid == 0) {
@@ -188,7 +166,7 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
   if (loader) {
     S.issued = 0;
     S.next = c;
-    row_loads<kQ, NT>(A, S, &tm_k, &tm_v, 0);
+    row_loads<NT>(A, S, &tm_k, &tm_v, 0);
   }
   __syncwarp();
 
@@ -198,25 +176,6 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
   const int hd = warp / A.kw, k0 = 16 * (warp - hd * A.kw);   // head of the item, first key of the unit
   float o[NT][8][4];                  // product t: dims at places 2t, 2t + 1 x rows 2 i4, 2 i4 + 1
   float m[NT][2], l[NT][2];           // of rows 2 i4 and 2 i4 + 1 of every tile
-  // What the thread's keys g and g + 8 of a unit bring besides K and V. Keys behind the last
-  // one read its place and are masked below, as are units without keys for this warp.
-  float next_s[2], next_k[2], next_v[2];
-  auto key_data = [&](const Cursor& t) {
-    const int64_t row0 = static_cast<int64_t>(t.b) * A.cap;
-    const int kvh = min(t.group * A.hw + hd, A.n_hkv - 1);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int64_t row = row0 + min(t.j * A.unit + k0 + g + 8 * x, t.len - 1);
-      next_s[x] = next_k[x] = next_v[x] = 0.f;
-      if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
-      next_s[x] = A.sc[row];
-      if constexpr (kQ) {
-        next_k[x] = A.ks[row * A.n_hkv + kvh];
-        next_v[x] = A.vs[row * A.n_hkv + kvh];
-      }
-    }
-  };
-  key_data(c);
   bool first = true;
   int r = 0;
 #pragma unroll 1
@@ -225,12 +184,20 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
     const bool head = hd < A.hw && kvh < A.n_hkv;   // else this warp only keeps the ring going
     const int nv = min(A.unit, c.len - c.j * A.unit);
     const bool any = head && k0 < nv;
-    // the next unit's scores and scales are on their way while this one is worked on
-    const float sk[2] = {next_s[0], next_s[1]}, ks[2] = {next_k[0], next_k[1]};
-    float vs[2] = {next_v[0], next_v[1]};
-    Cursor next = c;
-    next.advance(A, Q);
-    if (u + 1 < n) key_data(next);
+    // What the thread's keys g and g + 8 bring besides K and V. Keys behind the last one read its
+    // place and are masked below.
+    float sk[2] = {}, ks[2] = {}, vs[2] = {};
+    if (any) {
+      const int64_t row0 = static_cast<int64_t>(c.b) * A.cap + c.j * A.unit;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int64_t row = row0 + min(k0 + g + 8 * x, nv - 1);
+        if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
+        sk[x] = A.sc[row];
+        ks[x] = A.ks[row * A.n_hkv + kvh];
+        vs[x] = A.vs[row * A.n_hkv + kvh];
+      }
+    }
     if (first && head) {   // a new item: its queries, and nothing seen yet
       __syncwarp();
       const int64_t row_q = static_cast<int64_t>(c.b) * A.n_draft * A.n_hq + kvh * A.group;
@@ -241,7 +208,7 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
 #pragma unroll
         for (int t = 0; t < 8; ++t)   // dims as the keys' below
           cp8(&S.q[warp][nt][t][lane],
-              p + (kQ ? 32 * i4 + 4 * t : 64 * (t >> 2) + 16 * i4 + 8 * ((t >> 1) & 1) + 4 * (t & 1)));
+              p + 32 * i4 + 4 * t);
       }
       if (lane < 8 * NT) {
         const int row = min(lane, rows - 1), hq = kvh * A.group + row - tg::token_of(A, row) * A.group;
@@ -249,29 +216,27 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
       }
       cp_wait_all();
       __syncwarp();
-      if constexpr (kQ) {
-        // to fp16: the row is multiplied by the power of two that brings its largest value
-        // (exponent field e) to [2^8, 2^9), so that values down to 2^-22 of it stay exact
+      // to fp16: the row is multiplied by the power of two that brings its largest value
+      // (exponent field e) to [2^8, 2^9), so that values down to 2^-22 of it stay exact
 #pragma unroll 1
-        for (int nt = 0; nt < NT; ++nt) {
-          uint2 x[8];
-          uint32_t mx = 0;
+      for (int nt = 0; nt < NT; ++nt) {
+        uint2 x[8];
+        uint32_t mx = 0;
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            x[t] = S.q[warp][nt][t][lane];
-            mx = max_u16x2(mx, max_u16x2(x[t].x & 0x7FFF7FFFu, x[t].y & 0x7FFF7FFFu));
-          }
-          mx = max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-          mx = max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-          const int e = max(static_cast<int>(max(mx >> 16, mx & 0xFFFFu) >> 7), 9);
-          const float down = __int_as_float((262 - e) << 23);
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-            S.q[warp][nt][t][lane] = make_uint2(bf16x2_to_f16x2(x[t].x, down), bf16x2_to_f16x2(x[t].y, down));
-          if (i4 == 0) S.cg[warp][8 * nt + g].x *= __int_as_float((e - 8) << 23);
+        for (int t = 0; t < 8; ++t) {
+          x[t] = S.q[warp][nt][t][lane];
+          mx = max_u16x2(mx, max_u16x2(x[t].x & 0x7FFF7FFFu, x[t].y & 0x7FFF7FFFu));
         }
-        __syncwarp();
+        mx = max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = max_u16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        const int e = max(static_cast<int>(max(mx >> 16, mx & 0xFFFFu) >> 7), 9);
+        const float down = __int_as_float((262 - e) << 23);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          S.q[warp][nt][t][lane] = make_uint2(bf16x2_to_f16x2(x[t].x, down), bf16x2_to_f16x2(x[t].y, down));
+        if (i4 == 0) S.cg[warp][8 * nt + g].x *= __int_as_float((e - 8) << 23);
       }
+      __syncwarp();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         m[nt][0] = m[nt][1] = -INFINITY;
@@ -294,49 +259,47 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[nt][e] = 0.f;
+      float z2[NT][4] = {};   // every other product's sums: two chains are half as long
 #pragma unroll
-      for (int i = 0; i < (kQ ? 2 : 4); ++i) {
-        const uint8_t* at = p + (kQ ? 0 : (i >> 1) * C::kHalf) + (((2 * i4 + (i & 1)) ^ g) << 4);
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* at = p + (((2 * i4 + i) ^ g) << 4);
         const uint4 x0 = *reinterpret_cast<const uint4*>(at), x1 = *reinterpret_cast<const uint4*>(at + 8 * 128);
 #pragma unroll
-        for (int e = 0; e < (kQ ? 4 : 2); ++e) {   // product t: four dims of the thread's part
-          const int t = (kQ ? 4 : 2) * i + e;
+        for (int e = 0; e < 4; ++e) {   // product t: four dims of the thread's part
+          const int t = 4 * i + e;
           uint32_t a0, a1, a2, a3;
-          if constexpr (kQ) {
-            widen4<kE4m3>(word_of(x0, e) ^ kFlip, a0, a2);
-            widen4<kE4m3>(word_of(x1, e) ^ kFlip, a1, a3);
-          } else {
-            a0 = word_of(x0, 2 * e), a2 = word_of(x0, 2 * e + 1);
-            a1 = word_of(x1, 2 * e), a3 = word_of(x1, 2 * e + 1);
-          }
+          widen4<kE4m3>(word_of(x0, e) ^ kFlip, a0, a2);
+          widen4<kE4m3>(word_of(x1, e) ^ kFlip, a1, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 b = S.q[warp][nt][t][lane];
-            mma_16816<kQ>(z[nt], a0, a1, a2, a3, b.x, b.y);
+            mma_16816(e & 1 ? z2[nt] : z[nt], a0, a1, a2, a3, b.x, b.y);
           }
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[nt][e] += z2[nt][e];
     }
     __syncwarp();
     if (lane == 0) tg::mbar_arrive(&S.empty[s]);
     // the ring goes on where every warp is through with the unit before
-    if (loader) row_loads<kQ, NT>(A, S, &tm_k, &tm_v, r);
+    if (loader) row_loads<NT>(A, S, &tm_k, &tm_v, r);
     __syncwarp();
     uint32_t b[NT][2];   // the weights as fragments
     if (any) {
       // ---- weights ----
-      // Codes: the value scale v joins the logit, z + log2 v, so that the fp16 weights
+      // The value scale v joins the logit, z + log2 v, so that the fp16 weights
       // 2^(z + log2 v - m) are what the codes are multiplied by and m follows their largest;
       // the row sum takes them in fp32, divided by v. Where v is 0 all codes are, and any v
       // small enough not to lead will do.
-      float lv[2] = {}, iv[2] = {1.f, 1.f};
-      if constexpr (kQ) {
+      float lv[2], iv[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (vs[x] == 0.f) vs[x] = 0x1p-40f;
-          lv[x] = __log2f(vs[x]);
-          iv[x] = __frcp_rn(vs[x]);
-        }
+      for (int x = 0; x < 2; ++x) {
+        if (vs[x] == 0.f) vs[x] = 0x1p-40f;
+        lv[x] = __log2f(vs[x]);
+        iv[x] = __frcp_rn(vs[x]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -344,19 +307,14 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float &y0 = z[nt][2 * x], &y1 = z[nt][2 * x + 1];
-          if constexpr (kQ) {
-            y0 = fmaf(y0 * ks[x], cg.x, fmaf(cg.y, sk[x], lv[x]));
-            y1 = fmaf(y1 * ks[x], cg.z, fmaf(cg.w, sk[x], lv[x]));
-          } else {
-            y0 = fmaf(y0, cg.x, cg.y * sk[x]);
-            y1 = fmaf(y1, cg.z, cg.w * sk[x]);
-          }
+          y0 = fmaf(y0 * ks[x], cg.x, fmaf(cg.y, sk[x], lv[x]));
+          y1 = fmaf(y1 * ks[x], cg.z, fmaf(cg.w, sk[x], lv[x]));
           if (k0 + g + 8 * x >= nv) y0 = y1 = -INFINITY;   // a key that is not there
         }
-        // A row's reference is a whole number at or above its largest logit (fp16 weights: 6
-        // below that, to keep small ones exact) when it is set, and moves when a logit exceeds
-        // it by 2^8 more, so that bf16 weights stay below 2^8 and fp16 ones below 2^14.
-        constexpr float kLift = kQ ? 6.f : 0.f, kMost = kLift + tg::kRescaleThreshold;
+        // A row's reference is a whole number 6 below its largest logit or less (which keeps small
+        // fp16 weights exact) when it is set, and moves when a logit exceeds it by 2^14, so that
+        // the weights stay in fp16's range.
+        constexpr float kLift = 6.f, kMost = kLift + tg::kRescaleThreshold;
         const float m0 = fmaxf(z[nt][0], z[nt][2]), m1 = fmaxf(z[nt][1], z[nt][3]);
         if (__any_sync(0xFFFFFFFFu, m0 > m[nt][0] + kMost || m1 > m[nt][1] + kMost)) {
 #pragma unroll
@@ -379,16 +337,9 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float p0 = tg::exp2_approx(z[nt][2 * x] + n0), p1 = tg::exp2_approx(z[nt][2 * x + 1] + n1);
-          uint32_t w;
-          if constexpr (kQ) {
-            w = pack_f16x2(p0, p1);
-            l[nt][0] = fmaf(p0, iv[x], l[nt][0]);
-            l[nt][1] = fmaf(p1, iv[x], l[nt][1]);
-          } else {   // the sum of the rounded weights: a key that dominates gives its value exactly
-            w = tg::pack_bf16x2(p0, p1);
-            l[nt][0] += bf16_lo(w);
-            l[nt][1] += bf16_hi(w);
-          }
+          const uint32_t w = pack_f16x2(p0, p1);
+          l[nt][0] = fmaf(p0, iv[x], l[nt][0]);
+          l[nt][1] = fmaf(p1, iv[x], l[nt][1]);
           b[nt][x] = transpose8(w);
         }
       }
@@ -397,33 +348,23 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
     __syncwarp();
     if (any) {
       // ---- O^T += V^T P^T ----
-      uint4 xv[4][kQ ? 1 : 2];   // keys 2 i4 + {0, 1, 8, 9}
+      uint4 xv[4];   // keys 2 i4 + {0, 1, 8, 9}
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int key = k0 + 2 * i4 + (y & 1) + 8 * (y >> 1);
-        const uint8_t* p = S.tile[sv] + (hd * A.unit + key) * 128 + ((g ^ (key & 7)) << 4);
-#pragma unroll
-        for (int h = 0; h < (kQ ? 1 : 2); ++h) {
-          xv[y][h] = *reinterpret_cast<const uint4*>(p + h * C::kHalf);
-          if (nv - k0 < 16 && key >= nv) xv[y][h] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
-        }
+        xv[y] = *reinterpret_cast<const uint4*>(S.tile[sv] + (hd * A.unit + key) * 128 + ((g ^ (key & 7)) << 4));
+        if (nv - k0 < 16 && key >= nv) xv[y] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
       }
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         uint32_t a[4];   // [key half][place]
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if constexpr (kQ) {
-            const uint32_t x = word_of(xv[2 * h][0], t >> 1), y = word_of(xv[2 * h + 1][0], t >> 1);
-            widen4<kE4m3>(__byte_perm(x, y, t & 1 ? 0x7362 : 0x5140) ^ kFlip, a[2 * h], a[2 * h + 1]);
-          } else {
-            const uint32_t x = word_of(xv[2 * h][t >> 2], t & 3), y = word_of(xv[2 * h + 1][t >> 2], t & 3);
-            a[2 * h] = __byte_perm(x, y, 0x5410);
-            a[2 * h + 1] = __byte_perm(x, y, 0x7632);
-          }
+          const uint32_t x = word_of(xv[2 * h], t >> 1), y = word_of(xv[2 * h + 1], t >> 1);
+          widen4<kE4m3>(__byte_perm(x, y, t & 1 ? 0x7362 : 0x5140) ^ kFlip, a[2 * h], a[2 * h + 1]);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816<kQ>(o[nt][t], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][t], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
       }
     }
     __syncwarp();
@@ -443,16 +384,15 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
           for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
           const int row = 8 * nt + 2 * i4 + e;
           if (row >= rows) continue;
-          // the thread's 16 dims: contiguous (bf16: eight of both halves)
-          float* p = A.part + (slot + row) * 128 + (kQ ? 16 : 8) * g;
+          float* p = A.part + (slot + row) * 128 + 16 * g;   // the thread's 16 dims
 #pragma unroll
           for (int h = 0; h < 4; ++h)
-            *reinterpret_cast<float4*>(p + (kQ ? 4 * h : 64 * (h >> 1) + 4 * (h & 1))) =
+            *reinterpret_cast<float4*>(p + 4 * h) =
                 make_float4(o[nt][2 * h][e], o[nt][2 * h][2 + e], o[nt][2 * h + 1][e], o[nt][2 * h + 1][2 + e]);
           if (g == 0) *reinterpret_cast<float2*>(pl + 2 * row) = make_float2(m[nt][e], sum);
         }
     }
-    c = next;
+    c.advance(A, Q);
   }
   if (loader && S.abort_flag)   // let copies in flight land before the CTA exits
     for (int i = S.issued > C::kRing ? S.issued - C::kRing : 0; i < S.issued; ++i)
@@ -461,35 +401,28 @@ __global__ void __launch_bounds__(Cfg<kType != TG_BF16, NT>::kThreads, Cfg<kType
 
 template <int kType, int NT>
 tg_status launch(const TreeArgs& a, cudaStream_t st) {
-  constexpr bool kQ = kType != TG_BF16;
+  using C = Cfg<NT>;
   CUtensorMap tk, tv;
-  if (!tg::tree_cache_map(a, a.kc, 128, kQ, a.unit, a.hw, &tk) ||
-      !tg::tree_cache_map(a, a.vc, 128, kQ, a.unit, a.hw, &tv))
+  if (!tg::tree_cache_map(a, a.kc, 128, true, a.unit, a.hw, &tk) ||
+      !tg::tree_cache_map(a, a.vc, 128, true, a.unit, a.hw, &tv))
     return TG_ERR_CUDA;
-  constexpr int fixed = sizeof(RowSmem<kQ, NT>) + 1024;
-  static_assert((fixed + 1024 + 512) * Cfg<kQ, NT>::kShape.ctas <= 233472, "an SM's shared memory");
+  constexpr int fixed = sizeof(RowSmem<NT>) + 1024;
+  static_assert((fixed + 1024 + 512) * C::kCtas <= 233472, "an SM's shared memory");
   const int smem = fixed + 9 * a.batch + 8;
   if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_rows_kernel<kType, NT>), smem)) return TG_ERR_CUDA;
-  return tg::launch(tree_rows_kernel<kType, NT>, dim3(a.n_cta), dim3(Cfg<kQ, NT>::kThreads), smem, st, 0, tk, tv, a);
+  return tg::launch(tree_rows_kernel<kType, NT>, dim3(a.n_cta), dim3(C::kThreads), smem, st, 0, tk, tv, a);
 }
 
 template <int kType>
 tg_status launch_type(const TreeArgs& a, cudaStream_t st) {
-  const int rows = a.group * a.n_draft;
-  if (rows <= 8) return launch<kType, 1>(a, st);
-  return rows <= 16 ? launch<kType, 2>(a, st) : launch<kType, 4>(a, st);
+  return a.group * a.n_draft <= 8 ? launch<kType, 1>(a, st) : launch<kType, 2>(a, st);
 }
 
 }  // namespace
 
-namespace {
-Shape shape_for(bool codes, int rows) { return shape_of(codes, rows <= 8 ? 1 : rows <= 16 ? 2 : 4); }
-}  // namespace
-
-int tg::tree_rows_ctas(bool codes, int rows) { return 148 * shape_for(codes, rows).ctas; }
-int tg::tree_rows_warps(bool codes, int rows) { return shape_for(codes, rows).warps; }
+int tg::tree_rows_ctas(int rows) { return 148 * (rows <= 8 ? Cfg<1>::kCtas : Cfg<2>::kCtas); }
+int tg::tree_rows_warps(int rows) { return rows <= 8 ? Cfg<1>::kWarps : Cfg<2>::kWarps; }
 
 tg_status tg::launch_tree_rows(const TreeArgs& a, tg_dtype cache_dtype, cudaStream_t stream) {
-  if (cache_dtype == TG_BF16) return launch_type<TG_BF16>(a, stream);
   return cache_dtype == TG_I8 ? launch_type<TG_I8>(a, stream) : launch_type<TG_E4M3>(a, stream);
 }
