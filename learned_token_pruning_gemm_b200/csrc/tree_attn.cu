@@ -1017,8 +1017,16 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   }
 }
 
+// Fewer units a CTA than this cost more in partials than the CTAs are worth. One single token
+// / eight tokens of two heads over 1868 rows: 12.3 / 17.9 us with one, 11.6 / 15.9 us with two,
+// 14.2 / 19.1 us with four.
 constexpr int kMinUnits = 2;
-constexpr int64_t kFewRows = 2048;
+
+// Warps a row in the combining kernel: four where there are few rows, or not many and each
+// with many partials; one where the rows fill the machine anyhow. With one and with four:
+// 128 rows 14.1 and 12.9 us, 1024 rows of 28 partials 105 and 72 us, 1024 rows of 3 partials
+// 19.4 and 21.6 us, 1664 rows of 7 partials 57.2 and 61.9 us, 4096 rows 27.9 and 44.0 us.
+bool four_warps(int64_t rows, int64_t partials) { return rows <= 512 || (rows <= 2048 && partials > 16); }
 
 // How a call is laid out: which kernel, tokens per row tile, units, CTAs and the
 // workspace's two parts.
@@ -1054,12 +1062,11 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
   return p;
 }
 
-// Four warps a row where there are few rows, one where they fill the machine anyhow.
 template <int DH>
 tg_status launch_combine(const TreeArgs& a, tg_status r, cudaStream_t st) {
   if (r != TG_OK) return r;
   const int64_t rows = static_cast<int64_t>(a.batch) * a.n_draft * a.n_hq;
-  if (rows <= kFewRows)
+  if (four_warps(rows, a.n_cta / (a.slots - a.n_cta) * a.kw))
     return tg::launch(tree_combine_kernel<DH, 4>, dim3(a.n_hq, a.n_draft, a.batch), dim3(128), 0, st, 0, a);
   return tg::launch(tree_combine_kernel<DH, 1>, dim3((a.n_hq + 3) / 4, a.n_draft, a.batch), dim3(128), 0, st, 0, a);
 }
