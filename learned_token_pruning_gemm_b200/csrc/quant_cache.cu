@@ -5,12 +5,16 @@
 // tg_quant_cache_append writes rows: for one row's head x (dh bf16 values)
 //     scale = fl32(max|x| / qmax), qmax = 127 (int8) or 448 (e4m3),
 //     code  = x / scale rounded to the nearest code, ties to even.
-// The code is that of the exact quotient: x * (1/scale) is taken in fp32 and widened
-// by 2^-21 to both sides, which holds the quotient (a reciprocal to 2^-23 and roundings of
-// 2^-24); only where the two ends round to different codes is the border between them
-// compared with x, and border * scale - x is one exact fused product (at most 5 or 8 bits
-// times 24). Rows of bf16 values meet such borders often, since their quotients are of few
-// bits, so a quotient that was rounded first would store other codes.
+// The code is that of the exact quotient x / scale, without a division. Let X and A be the
+// 8-bit significands of x and the maximum, B = 2n + 1 that of a border between two codes (at
+// most 8 bits for int8, 5 for e4m3), Q = 127 or 7 the odd part of qmax: up to powers of two
+// x qmax / max over the border is Q X / (B A), which is 1 or differs from it by at least
+// 1 / (253 * 255) > 2^-16. So only an exact tie comes near a border, and there the rounding of
+// the scale decides: a scale above max / qmax makes the quotient less than the border, one
+// below it more. Its sign is that of scale * qmax - max (one exact fused product); x is
+// multiplied by 1 / scale (off by 2^-22 with all roundings) times 1 -+ 2^-18, and the product
+// rounded to 20 bits, which gives a tie back where the scale is exact and moves nothing else
+// over a border.
 // A scale below 2^-60 is stored as 0 with codes 0; a row that holds an infinity or a
 // NaN gets a NaN scale and codes 0, so it reads back as NaN.
 //
@@ -117,41 +121,20 @@ __device__ __forceinline__ uint32_t codes_of(float y0, float y1) {
     return __byte_perm(a, b, 0x0040) & 0xFFFFu;
   }
 }
-template <bool kE4m3>
-__device__ __forceinline__ float value_of(uint32_t code) {
-  if constexpr (kE4m3) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code & 0xFFu)));
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
-  } else {
-    return static_cast<float>(static_cast<int8_t>(code));
-  }
+// A quotient to 20 bits.
+__device__ __forceinline__ float to_20_bits(float y) {
+  return __uint_as_float((__float_as_uint(y) + 4) & ~7u);
 }
-
-// The code of x / scale where the rounded quotients to its two sides disagree: the border m
-// between the codes lies next to the quotient, so x is compared with m * scale.
+// The codes of bf16 pairs; inv is 1 / scale with the nudge.
 template <bool kE4m3>
-__device__ __noinline__ uint32_t border_code(float x, float scale, uint32_t lo, uint32_t hi) {
-  if (lo == hi) return lo;
-  const float m = 0.5f * (value_of<kE4m3>(lo) + value_of<kE4m3>(hi));
-  const float d = fmaf(-m, scale, x) * (x < 0.f ? -1.f : 1.f);
-  return d > 0.f || (d == 0.f && (hi & 1) == 0) ? hi : lo;
-}
-
-// The codes of a bf16 pair; inv is 1 / scale to 2^-23.
-template <bool kE4m3>
-__device__ __forceinline__ uint32_t encode2(uint32_t u, float inv, float scale) {
-  const float x0 = __uint_as_float(u << 16), x1 = __uint_as_float(u & 0xFFFF0000u);
-  const float y0 = x0 * inv, y1 = x1 * inv;
-  const uint32_t lo = codes_of<kE4m3>(y0 * (1.f - 0x1p-21f), y1 * (1.f - 0x1p-21f));
-  const uint32_t hi = codes_of<kE4m3>(y0 * (1.f + 0x1p-21f), y1 * (1.f + 0x1p-21f));
-  if (lo == hi) return lo;
-  return border_code<kE4m3>(x0, scale, lo & 0xFFu, hi & 0xFFu) | border_code<kE4m3>(x1, scale, lo >> 8, hi >> 8) << 8;
+__device__ __forceinline__ uint32_t encode2(uint32_t u, float inv) {
+  return codes_of<kE4m3>(to_20_bits(__uint_as_float(u << 16) * inv),
+                         to_20_bits(__uint_as_float(u & 0xFFFF0000u) * inv));
 }
 template <bool kE4m3>
-__device__ __forceinline__ uint2 encode8(const uint4& x, float inv, float scale) {
-  return make_uint2(encode2<kE4m3>(x.x, inv, scale) | encode2<kE4m3>(x.y, inv, scale) << 16,
-                    encode2<kE4m3>(x.z, inv, scale) | encode2<kE4m3>(x.w, inv, scale) << 16);
+__device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
+  return make_uint2(encode2<kE4m3>(x.x, inv) | encode2<kE4m3>(x.y, inv) << 16,
+                    encode2<kE4m3>(x.z, inv) | encode2<kE4m3>(x.w, inv) << 16);
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -236,8 +219,10 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
         if (finite && scale > 0.f) {
           float inv;
           asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
-          a = encode8<kE4m3>(x[u][0], inv, scale);
-          b2 = encode8<kE4m3>(x[u][1], inv, scale);
+          const float over = fmaf(scale, kE4m3 ? 448.f : 127.f, -__uint_as_float(m << 16));
+          if (over != 0.f) inv *= over > 0.f ? 1.f - 0x1p-18f : 1.f + 0x1p-18f;
+          a = encode8<kE4m3>(x[u][0], inv);
+          b2 = encode8<kE4m3>(x[u][1], inv);
         }
         if (h < heads) {
           const int64_t hr = row * A.n_hkv + (val ? h - A.n_hkv : h);
