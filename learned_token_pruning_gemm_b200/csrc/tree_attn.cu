@@ -175,23 +175,16 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// 16 rows by 32 columns, as the 16x256b loads of 64 columns
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
-      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// 16 rows by 16 columns, as the 16x256b loads of 64 columns
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32"
-      " [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // 16 rows by 32 columns: thread l holds (row l/4, column 4i + l%4) in register 2i and
 // the same column of row l/4 + 8 in register 2i + 1.
@@ -579,13 +572,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           const int nh = nv - kJob * half;
           const float* key = S.key[s][0] + kJob * half + cq;
           float z[32];
-          // A row's reference is a whole number at or above its largest logit (fp16 weights: 6
-          // below that, to keep small ones exact) when it is set, so that moving it scales by an
-          // exact power of two; it moves when a logit exceeds it by 2^8 more, so that bf16 weights
-          // stay below 2^8 and fp16 ones below 2^14.
-          constexpr float kLift = kQ ? 6.f : 0.f, kMost = kLift + tg::kRescaleThreshold;
-#pragma unroll 1
-          for (bool again = false;; again = true) {   // twice where the reference moves, never more
+          {
             uint32_t u[32];
             tg::tmem_ld_16x256b_x8(sbuf, u);
             tg::tmem_ld_wait();
@@ -603,12 +590,13 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
               }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float b0 = nm[e], b1 = nm[e];
-                if constexpr (kQ) fadd2(b0, b1, lv.x, lv.y, nm[e], nm[e]);
-                ffma2(b0, b1, gh[e], gh[e], sk.x, sk.y, b0, b1);
+                float b0, b1;
+                if constexpr (kQ) ffma2(b0, b1, gh[e], gh[e], sk.x, sk.y, lv.x, lv.y);
+                else fmul2(b0, b1, gh[e], gh[e], sk.x, sk.y);
                 ffma2(z[4 * i + 2 * e], z[4 * i + 2 * e + 1], x[2 * e], x[2 * e + 1], ch[e], ch[e], b0, b1);
               }
             }
+          }
           if (nh < kJob) {   // keys that are not there
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -627,25 +615,23 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
             }
             mx[e] = fmaxf(t0, t1);
           }
-            if (again) {
-              // No logit exceeds its row's reference by more than it may now, but by rounding one may
-              // that is so large that its last place does: it is brought down.
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (z[i] > kMost) z[i] = kMost;
-              break;
-            }
-            if (!__any_sync(0xFFFFFFFFu, mx[0] > most[0] || mx[1] > most[1])) break;
+          // A row's reference is a whole number at or above its largest logit (fp16 weights: 6
+          // below that, to keep small ones exact) when it is set, so that moving it scales by an
+          // exact power of two; it moves when a logit exceeds it by 2^8 more, so that bf16 weights
+          // stay below 2^8 and fp16 ones below 2^14. It is taken off logits that are rounded
+          // already: of the largest nothing but the lift is left, however large they are.
+          if (__any_sync(0xFFFFFFFFu, mx[0] + nm[0] > most[0] || mx[1] + nm[1] > most[1])) {
+            constexpr float kLift = kQ ? 6.f : 0.f;
             float alpha[2] = {1.f, 1.f};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
               mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
-              if (mx[e] > most[e]) {
-                const float to = nm[e] - (ceilf(mx[e]) - kLift);
+              if (mx[e] + nm[e] > most[e]) {
+                const float to = kLift - ceilf(mx[e]);
                 alpha[e] = most[e] == -INFINITY ? 0.f : tg::exp2_approx(to - nm[e]);   // 0 where nothing was seen
                 nm[e] = to;
-                most[e] = kMost;
+                most[e] = kLift + tg::kRescaleThreshold;
                 l[e] *= alpha[e];
               }
             }
@@ -654,14 +640,14 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
               __syncwarp();
               tg::tc_fence_after();
 #pragma unroll 1
-              for (int h = 0; h < DH / 32; ++h) {
-                uint32_t o[16];
-                tmem_ld_16x256b_x4(obuf + 32u * h, o);
+              for (int h = 0; h < DH / 16; ++h) {
+                uint32_t o[8];
+                tmem_ld_16x256b_x2(obuf + 16u * h, o);
                 tg::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 8; ++i)
                   o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
-                tmem_st_16x256b_x4(obuf + 32u * h, o);
+                tmem_st_16x256b_x2(obuf + 16u * h, o);
               }
             }
           }
@@ -677,7 +663,9 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
             if constexpr (kQ) iv = *reinterpret_cast<const float2*>(key + 3 * kBN + 8 * i);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float p0 = tg::exp2_approx(z[4 * i + 2 * e]), p1 = tg::exp2_approx(z[4 * i + 2 * e + 1]);
+              float p0, p1;
+              fadd2(p0, p1, z[4 * i + 2 * e], z[4 * i + 2 * e + 1], nm[e], nm[e]);
+              p0 = tg::exp2_approx(p0), p1 = tg::exp2_approx(p1);
               if constexpr (kQ) {
                 pk[2 * i + e] = tg::pack_f16x2(p0, p1);
                 ffma2(sum[e][0], sum[e][1], p0, p1, iv.x, iv.y, sum[e][0], sum[e][1]);
@@ -716,16 +704,16 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
             if (!all_alive(alive)) { alive = false; break; }
             tg::tc_fence_after();
 #pragma unroll 1
-            for (int h = 0; h < DH / 32; ++h) {   // columns cq and cq + 1 of each 8
-              uint32_t o[16];
-              tmem_ld_16x256b_x4(obuf + 32u * h, o);
+            for (int h = 0; h < DH / 16; ++h) {   // columns cq and cq + 1 of each 8
+              uint32_t o[8];
+              tmem_ld_16x256b_x2(obuf + 16u * h, o);
               tg::tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 2; ++e)
                 if (r2[e] < rows) {
-                  float* p = A.part + (slot + r2[e]) * DH + 32 * h + cq;
+                  float* p = A.part + (slot + r2[e]) * DH + 16 * h + cq;
 #pragma unroll
-                  for (int i = 0; i < 4; ++i)
+                  for (int i = 0; i < 2; ++i)
                     *reinterpret_cast<uint2*>(p + 8 * i) = make_uint2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
                 }
               __syncwarp();

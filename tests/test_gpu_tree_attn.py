@@ -273,3 +273,46 @@ def test_no_sequences_and_no_drafts(api):
     e = {n: t[:, :0].contiguous() if n in ("q", "kd", "vd", "sd", "mask") else t for n, t in st.items()}
     e["dl"] = e["dl"] * 0
     assert run(api, e).shape == (1, 0, 4, 128)
+
+
+EDGES = [  # rows around the tiles of the few-row kernel, heads it cannot share evenly; pairs of row tiles
+    (2, 8, 300, [300, 17], 3, 3, 128, [8, 7]),
+    (2, 9, 300, [299, 16], 5, 5, 128, None),
+    (1, 8, 700, [700], 24, 12, 128, None),
+    (2, 17, 333, [333, 15], 12, 12, 128, [17, 16]),
+    (3, 64, 400, [400, 192, 193], 5, 1, 128, [64, 44, 20]),     # three row tiles, two, one
+    (2, 64, 400, [65, 64], 10, 2, 64, [64, 23]),
+    (4, 64, 90, [1, 90, 64, 65], 2, 1, 128, [64, 64, 63, 1]),   # one full row tile: units with and without a second half
+    (5, 64, 2000, [2000, 3, 1999, 0, 640], 12, 3, 128, [64, 64, 1, 9, 43]),
+    (64, 3, 400, [(53 * b) % 401 for b in range(64)], 16, 8, 64, None),   # more items than CTAs
+]
+
+
+@pytest.mark.parametrize("fmt", [BF, I8, E4])
+@pytest.mark.parametrize("B,T,cap,lens,hq,hkv,dh,dls", EDGES)
+def test_edges(api, fmt, B, T, cap, lens, hq, hkv, dh, dls):
+    st = make(B * 100 + T + 7, B, T, cap, lens, hq, hkv, dh, fmt, dls)
+    check(run(api, st, out=torch.full_like(st["q"], 9.0)), reference(st))
+
+
+@pytest.mark.parametrize("fmt", [BF, I8, E4])
+@pytest.mark.parametrize("T,hq,dh", [(2, 4, 128), (40, 8, 128), (8, 4, 64)])
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 40, 2.0 ** 80])
+def test_logits_whose_last_place_exceeds_any_weight(api, fmt, T, hq, dh, size):
+    # Logits of this size differ by far more than a softmax tells apart: every row is its
+    # best key's value, and nothing may be lost in taking the reference off. The best
+    # key is ahead by more than the logits' rounding (2^-20 of the largest).
+    st = make(31, 1, T, 600, [577], hq, 2, dh, fmt, garbage=False)
+    st["q"] = (st["q"].float() * size).to(BF)
+    st["gain"].zero_()
+    st["mask"][:] = 0
+    k, v = values(st)
+    z = torch.einsum("tghd,ngd->tghn", st["q"][0].double().reshape(T, 2, hq // 2, dh), k[0, :577])
+    top = z.topk(2, -1)
+    ahead = (top.values[..., 0] - top.values[..., 1]) > z.abs().amax(-1) * 2.0 ** -17
+    assert ahead.float().mean() > 0.9
+    want = torch.einsum("tghn,ngd->tghd", torch.nn.functional.one_hot(top.indices[..., 0], 577).double(), v[0, :577])
+    got = run(api, st)[0].double().reshape(T, 2, hq // 2, dh)
+    assert torch.isfinite(got).all()
+    err = (got - want).abs()[ahead]
+    assert (err <= want.abs()[ahead] * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12)).all(), float(err.max())
