@@ -245,3 +245,25 @@ def test_many_sequences(api):
                                      dtype=torch.float32)
     q, sc = ops_ref.quantise(k, torch.int8)
     assert torch.equal(kr, (q.float() * sc[..., None])) and torch.equal(sr, s)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_every_significand_against_every_maximum(api, fmt):
+    # all 128 significands of a maximum, those of the values in 16 binades below it: every
+    # quotient that can be a tie between two codes, and every one next to it
+    x = torch.arange(128, 256, dtype=torch.float32)
+    rows = []
+    for top in range(128, 256):
+        v = torch.cat([x[x <= top] * 2.0 ** -e for e in range(16)])
+        v = torch.cat([v, v.new_zeros(-v.numel() % 127)]).reshape(-1, 127)
+        rows.append(torch.cat([torch.full((v.shape[0], 1), float(top)), v], 1))
+    x = torch.cat(rows).to(torch.bfloat16).cuda()[:, None]
+    R = x.shape[0]
+    for size in (1.0, 2.0 ** -40, 2.0 ** 90):
+        y = (x.float() * size).to(torch.bfloat16)
+        c = _empty(1, R, 1, 128, fmt)
+        _append(api, c, torch.zeros(1, dtype=torch.int32).cuda(), y, -y, torch.zeros(R).cuda(), _cu([R]))
+        for n, t in (("k", y), ("v", -y)):
+            q, sc = ops_ref.quantise(t, fmt)
+            assert torch.equal(c[n + "s"][0], sc)
+            assert torch.equal(c[n + "c"][0].double(), q)
