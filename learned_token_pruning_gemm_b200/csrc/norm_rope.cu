@@ -8,9 +8,12 @@
 //
 // Both are bound by memory: each element is read and written once (16-bit: 4 bytes
 // forward, 6 backward). A warp takes a token (or, for few tokens, part of its heads),
-// so the angles are formed once per token and serve every head: lane c of the dh/8
-// lanes of a head holds the four pairs 4c .. 4c+3 (elements 4c.. and rot/2 + 4c..), so
-// a rotation needs no exchange between lanes, and the mean is log2(dh/8) shuffles.
+// so the angles are formed once per token, a part by each of the heads that are side by side,
+// and serve every head: lane c of a head holds E pairs from E c on (elements E c .. and
+// rot/2 + E c ..; E = 8 or 4), so a rotation needs no exchange between lanes, and the mean
+// is a few shuffles. 16384 tokens of 24 bf16 heads of 128 take 40.0 us (5.0 TB/s, 77% of a
+// plain copy's rate), backward over 10721 tokens 46.8 us (4.2 TB/s): what is left is
+// issue slots (58% busy) and latency at 20 and 12 warps an SM, not DRAM.
 //
 // The angle of position p and frequency i is taken in turns, p * F_i mod 1 with F_i =
 // theta_i / (2 pi) as a 64-bit fixed-point fraction (an integer product, exact modulo
@@ -95,19 +98,17 @@ struct Io<float, 4> {
   static __device__ __forceinline__ Vec pack(const float2* f) { return make_float4(f[0].x, f[0].y, f[1].x, f[1].y); }
 };
 
-// The lane's frequencies F_i = ratio^i / (2 pi) in turns, 0.64 fixed point, i = E c + j.
-template <int E>
-__device__ __forceinline__ void lane_turns(double ratio, int c, uint64_t* f) {
+// Frequencies F_i = ratio^i / (2 pi) in turns, 0.64 fixed point, i = i0 .. i0 + N - 1 (i0 < 128).
+template <int N>
+__device__ __forceinline__ void turns_from(double ratio, int i0, uint64_t* f) {
   double t = 0.15915494309189535, p = ratio;
 #pragma unroll
-  for (int b = 1; b < E; b <<= 1) p *= p;   // ratio^E
-#pragma unroll
-  for (int b = 0; b < 5; ++b) {
-    if ((c >> b) & 1) t *= p;
+  for (int b = 0; b < 7; ++b) {
+    if ((i0 >> b) & 1) t *= p;
     p *= p;
   }
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
+  for (int j = 0; j < N; ++j) {
     f[j] = __double2ull_rn(t * 18446744073709551616.0);
     t *= ratio;
   }
@@ -140,20 +141,21 @@ __device__ __forceinline__ float head_sum(float v) {
 // E: elements of a lane in either half of its pairs, LPH lanes per head (at least dh / (2 E)).
 // kU heads of each lane group are in flight at once.
 template <typename T, int E, int LPH, bool kBwd>
-__global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) norm_rope_kernel(const NormRopeArgs A) {
+__global__ void __launch_bounds__(kThreads, kBwd ? 3 : 5) norm_rope_kernel(const NormRopeArgs A) {
   using IO = Io<T, E>;
   using Vec = typename IO::Vec;
   constexpr int kP = E / 2;
   constexpr int kHpw = 32 / LPH;   // heads a warp handles side by side
-  constexpr int kU = kBwd || E == 4 ? 2 : 4;
+  constexpr int kU = 2;
+  constexpr int kNa = E / kHpw;    // angles that a lane forms
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = lane % LPH, sub = lane / LPH;
   const int nc = A.dh / (2 * E), nr = A.rot / (2 * E);
   const bool active = c < nc, turns = c < nr;
   const int offa = !active ? 0 : turns ? E * c : A.rot + 2 * E * (c - nr);
   const int offb = !active ? 0 : turns ? A.rot / 2 + E * c : offa + E;
-  uint64_t freq[E];
-  lane_turns<E>(A.ratio, turns ? c : 0, freq);
+  uint64_t freq[kNa];
+  turns_from<kNa>(A.ratio, turns ? E * c + kNa * sub : 0, freq);
   tg::pdl_launch_dependents();
   tg::pdl_wait();   // global memory only from here on
 
@@ -173,11 +175,19 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 4) norm_rope_kernel(const
     const int64_t t = A.parts == 1 ? wk : wk / A.parts;
     const int part = static_cast<int>(wk - t * A.parts);
     const int64_t p = A.pos[t];
+    // The heads side by side need the same angles: each forms a part of them.
+    float s_own[kNa], c_own[kNa];
+#pragma unroll
+    for (int j = 0; j < kNa; ++j) {
+      s_own[j] = 0.f, c_own[j] = 1.f;
+      if (turns) angle<sizeof(T) == 4>(p, freq[j], &s_own[j], &c_own[j]);
+    }
+    __syncwarp();
     float2 sn[kP], cs[kP];
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      float s = 0.f, k = 1.f;
-      if (turns) angle<sizeof(T) == 4>(p, freq[j], &s, &k);
+      const float s = __shfl_sync(0xFFFFFFFFu, s_own[j % kNa], c + LPH * (j / kNa));
+      const float k = __shfl_sync(0xFFFFFFFFu, c_own[j % kNa], c + LPH * (j / kNa));
       if (j & 1) sn[j / 2].y = s, cs[j / 2].y = k;
       else sn[j / 2].x = s, cs[j / 2].x = k;
     }
@@ -321,13 +331,16 @@ __global__ void __launch_bounds__(1024)
   if (threadIdx.x == 0 && out < n) (out < dh ? dwq[out] : dwk[out - dh]) = s;
 }
 
-// Blocks of a launch: as many as the SMs hold (four forward, three backward, whose sums
-// then are few), walking the tokens.
-int most_blocks(bool bwd) { return 148 * (bwd ? 3 : 4); }
+// Blocks of a launch: as many as the SMs hold, walking the tokens: forward five (two heads in
+// flight; 16384 tokens of 24 heads of 128: 40.0 us, 41.4 with four blocks, 41.8 with six, 44.3
+// with three heads in flight), backward three (10721 tokens: 46.8 us, 49.9 with four), whose
+// sums then are few.
+int most_blocks(bool bwd) { return 148 * (bwd ? 3 : 5); }
 
 // Whether lanes take eight elements of either half (16-byte loads of bf16): the halves of
 // the rotated part and the rest must be made of whole such pieces. 16384 tokens of 24 heads
-// of 128: 56 us with four, 42 us with eight (backward, 10721 tokens: 69 and 49 us).
+// of 128: 56 us with four, 42 us with eight (backward, 10721 tokens: 69 and 49 us; both
+// before the angles were shared).
 bool wide_lanes(tg_dtype dtype, int dh, int rot) { return dtype == TG_BF16 && dh % 16 == 0 && rot % 16 == 0; }
 
 // Warps per token: one, unless there are too few tokens to fill the machine.
