@@ -34,6 +34,17 @@
 //   warps 4-19   softmax, 16 rows a warp, those with rows only: logits in the log2 domain
 //                less the row's running reference, which moves only when one exceeds it by more
 //                than it may (O is then rescaled in TMEM).
+// What bounds it: the softmax's instructions (about 9 an element with the scales, 16 warps an SM,
+// half of the issue slots busy), then the products (two thirds of the MMA rate would be
+// reached at twice the softmax's speed) and, with few rows, the way of a unit through the
+// roles. 2 x 64 tokens of 32 heads over 65500 int8 rows of four heads: 226 us (0.61 PFLOP/s, 84.5
+// us at a plain GEMM's rate; 200 us without the combining kernel); 8 x 13 tokens of 16 heads
+// over 50 thousand bf16 rows of eight: 57 us (31.3 us at a plain copy's rate). Steps that
+// made it so, on the long case: one row tile a CTA 379 us; two tiles that share K, V and
+// their widening 318; queries, keys and values waiting less for one another 246; one thread
+// chosen by elect.sync for the products (a lane picked by its number costs 80 to 110 cycles an
+// MMA, an elected one 25 to 45) and jobs of 64 keys 253; 16 rows a warp 229; streams of eight
+// lanes in the combining kernel 224.
 // A side's S_k is issued after its PV_{k - 2}, and products end in the order they are issued:
 // when S_k is there, all but PV_{k - 1} are done, so no parity wait is passed by.
 #include "tree.cuh"
@@ -1030,6 +1041,9 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
   const int most_tm = kBM / group, tiles = (n_draft + most_tm - 1) / most_tm;
   p.tm = (n_draft + tiles - 1) / tiles;   // tiles alike
   const int rows = group * p.tm;
+  // Which kernel (this one and tree_rows.cu): codes, 8 x 10721 rows of eight heads: 2 rows a KV
+  // head (32 x 1868) 79 and 38 us, 16 rows 104 and 72 us, 26 rows 105 and 113 us; a bf16 cache:
+  // 2 rows 52.6 and 52.8 us, 16 rows (one of 1868) 12.9 and 14.4 us, 26 rows 61 and 67 us.
   p.few = codes && head_dim == 128 && rows <= tg::kTreeRowsMax;
   const int warps = tg::tree_rows_warps(rows);
   p.hw = p.few ? (n_hkv < warps ? n_hkv : warps) : 1;

@@ -18,6 +18,11 @@
 //   S^T: dims 32 i .. 32 i + 31 of keys g and g + 8;
 //   O^T: dims 16 g .. 16 g + 15 of keys 2 i, 2 i + 1, 2 i + 8 and 2 i + 9: product t holds the
 //        dims at places 2 t and 2 t + 1 of these.
+// What bounds it is the instructions, about 480 a unit, and their latency at 12 to 16 warps an SM
+// (43% of issue slots busy). 32 sequences of 1868 e4m3 rows of eight heads, a token of 16 heads:
+// 37.6 us with the combining kernel (33 without; 19.4 us is the read at a plain copy's
+// rate); eight tokens over 8 x 10721 rows: 72 us (27.9).
+//
 // Codes are widened to fp16, which holds them exactly at half the instructions that bf16
 // takes; the queries are then fp16 too, after their largest value is brought near 2^8.
 #include "tree.cuh"
@@ -34,6 +39,10 @@ using tg::widen4;
 // NT: tiles of eight rows. Several CTAs share an SM, so that one's start and end of an item
 // pass under the others' work; how many goes by registers, then the ring takes the rest of
 // the shared memory.
+// NT tiles of eight rows. Several CTAs share an SM, so that one's start and end of an item
+// pass under the others' work; registers say how many, and the ring takes the rest of the
+// shared memory. Single tokens as below: 37.6 us with 2 CTAs of 8 warps, 39.0 with 4 of 4
+// (a ring of 5), 43.8 with 3 of 4 (a ring of 8), 61.9 with 5 of 4 (registers spill).
 template <int NT>
 struct Cfg {
   static constexpr int kWarps = NT == 1 ? 8 : 4;   // of a CTA
@@ -188,14 +197,15 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
     // place and are masked below.
     float sk[2] = {}, ks[2] = {}, vs[2] = {};
     if (any) {
-      const int64_t row0 = static_cast<int64_t>(c.b) * A.cap + c.j * A.unit;
+      const int row0 = c.b * A.cap + c.j * A.unit;   // batch * cap is below 2^31
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int64_t row = row0 + min(k0 + g + 8 * x, nv - 1);
+        const int row = row0 + min(k0 + g + 8 * x, nv - 1);
         if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
+        const int64_t at = static_cast<int64_t>(row) * A.n_hkv + kvh;
         sk[x] = A.sc[row];
-        ks[x] = A.ks[row * A.n_hkv + kvh];
-        vs[x] = A.vs[row * A.n_hkv + kvh];
+        ks[x] = A.ks[at];
+        vs[x] = A.vs[at];
       }
     }
     if (first && head) {   // a new item: its queries, and nothing seen yet
