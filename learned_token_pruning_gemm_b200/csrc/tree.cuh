@@ -7,8 +7,6 @@
 // and few heads fill the machine alike.
 #pragma once
 
-#include <cuda_fp16.h>
-
 #include "common.cuh"
 
 namespace tg {
@@ -167,9 +165,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float scale) {
   return pack_f16x2(bf16_lo(w) * scale, bf16_hi(w) * scale);
-}
-__device__ __forceinline__ float2 f16x2_to_float2(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 // The map of a K or V cache, rows of dh (bf16: halves of 64), 128-byte swizzle (64-byte for

@@ -699,6 +699,7 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           if (!c.two) break;
         }
         if (!all_alive(alive)) { alive = false; break; }
+        __syncwarp();
         if (lane == 0) tg::mbar_arrive(&S.b_empty[s]);   // this warp is done with the keys' data
         first = c.run() == 1;   // the last unit of its item here: O is complete after the last PV
         if (first) {
@@ -777,8 +778,6 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         x[p] = *reinterpret_cast<const uint4*>(src + rr * DH + ((DH == 128 ? cc ^ rl : cc ^ ((rl >> 1) & 3)) << 4));
         if (val && rr >= nv) x[p] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
       }
-      __syncwarp();
-      if (lane == 0) tg::mbar_arrive(&S.raw_empty[rs]);
       if (g >= n_st && !all_alive(wait(empty, ((g / n_st) - 1) & 1, A.status, &S.abort_flag))) break;
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
@@ -791,9 +790,15 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
         *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc)) = make_uint4(y[0], y[1], y[2], y[3]);
         *reinterpret_cast<uint4*>(dst + tile_off(rr, 2 * cc + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
       }
+      // The raw tile is given back only now: its loads have all arrived and are ordered before
+      // the next copy into it. Given back when they were only under way, it was overwritten
+      // under one about once in 200 calls.
       tg::fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) tg::mbar_arrive(full);
+      if (lane == 0) {
+        tg::mbar_arrive(&S.raw_empty[rs]);
+        tg::mbar_arrive(full);
+      }
     }
   }
   tg::tc_fence_before();
