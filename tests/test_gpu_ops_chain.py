@@ -201,3 +201,43 @@ def test_training_step_of_normed_attention(api):
     for name, a, b in zip(("dq", "dk", "dv", "ds", "dwq", "dwk"), (dq, dk, dv, ds, dwq, dwk), want):
         # as above, and a gradient's terms may exceed it: by less than four times its largest
         assert ((a.double() - b).abs() <= 2.0 ** -12 * b.abs().max()).all(), name
+
+
+@pytest.mark.parametrize("fmt", [I8, BF])
+@pytest.mark.parametrize("T,dh", [(1, 128), (12, 128), (3, 64)])
+def test_offsets_behind_32_bits(api, fmt, T, dh):
+    # the last sequence of a cache of more than 2^31 elements, as it is in a cache of its own
+    from test_gpu_tree_attn import check, make, reference, run
+    cap, n, hkv = 60000, 1500, HKV
+    B = 2 ** 31 // (cap * hkv * dh) + 2
+    small = make(41, 1, T, cap, [n], HQ, hkv, dh, fmt, garbage=False)
+    st = {}
+    for name, t in small.items():
+        st[name] = t if t is None or name in ("gain", "tau") else torch.empty((B,) + t.shape[1:], dtype=t.dtype,
+                                                                              device=t.device)
+        if st[name] is not None and st[name] is not t:
+            st[name][-1] = t[0]
+            if name in ("len", "dl"):
+                st[name][:-1] = 0
+    assert st["kc"].numel() > 2 ** 31
+    out = torch.full_like(st["q"], 9.0)
+    if fmt == BF:
+        check(run(api, st, out=out)[-1:], reference(small))
+        return
+    # rows are appended behind those there, attended over, and read back
+    g = torch.Generator().manual_seed(42)
+    rows = 77
+    k, v, s = (torch.randn(rows, hkv, dh, generator=g).to(BF).cuda(), torch.randn(rows, hkv, dh, generator=g).to(BF).cuda(),
+               torch.randn(rows, generator=g).cuda())
+    for c in (st, small):
+        m = c["len"].numel()
+        c["start"] = c["len"].clone()
+        api.quant_cache_append(k, v, s, _i32([0] * m + [rows]), c["kc"], c["vc"], c["ks"], c["vs"], c["sc"], c["len"])
+        c["read"] = api.quant_cache_read(c["kc"], c["vc"], c["ks"], c["vs"], c["sc"], c["len"], _i32([0] * m + [rows]),
+                                         rows, start=c["start"])
+    assert int(st["len"][-1]) == n + rows and not st["len"][:-1].any()
+    for a, b in zip(st["read"], small["read"]):
+        assert torch.equal(a, b)
+    for name in ("kc", "vc", "ks", "vs", "sc"):
+        assert torch.equal(st[name][-1, :n + rows], small[name][0, :n + rows])
+    check(run(api, st, out=out)[-1:], reference(small))
