@@ -180,10 +180,10 @@ inline bool tree_cache_map(const TreeArgs& a, const void* cache, int dh, bool co
                      str, box, codes && dh == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// tree_rows.cu: the part over a cache of codes for up to kTreeRowsMax rows of head_dim 128.
+// tree_rows.cu: the part over a cache of codes for up to kTreeRowsMax rows.
 constexpr int kTreeRowsMax = 16;
 int tree_rows_ctas(int rows);    // CTAs that fill the machine
 int tree_rows_warps(int rows);   // warps of a CTA: hw * kw is at most these
-tg_status launch_tree_rows(const TreeArgs& a, tg_dtype cache_dtype, cudaStream_t stream);
+tg_status launch_tree_rows(const TreeArgs& a, int head_dim, tg_dtype cache_dtype, cudaStream_t stream);
 
 }  // namespace tg

@@ -9,8 +9,8 @@
 // The cache is read once per KV head and serves all drafted tokens and query heads of the
 // group: with R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product and back.
 // Here the rows are packed into M = 128 tiles (row r is token r / G, head r % G) and both
-// products run on the tensor cores with accumulators in TMEM; up to 16 rows of head dim
-// 128 over codes take the kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128
+// products run on the tensor cores with accumulators in TMEM; up to 16 rows
+// over codes take the kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128
 // cache rows; what a CTA has of an item it leaves as partials (max, sum, O), and the
 // kernel at the end adds the partials up in CTA order, so results do not depend on timing,
 // and brings in the drafted rows that each token sees.
@@ -1047,9 +1047,10 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
   p.tm = (n_draft + tiles - 1) / tiles;   // tiles alike
   const int rows = group * p.tm;
   // Which kernel (this one and tree_rows.cu): codes, 8 x 10721 rows of eight heads: 2 rows a KV
-  // head (32 x 1868) 79 and 38 us, 16 rows 104 and 72 us, 26 rows 105 and 113 us; a bf16 cache:
+  // head (32 x 1868) 79 and 38 us, 16 rows 104 and 72 us, 26 rows 105 and 113 us (head dim 64: 62
+  // and 33 us, 77 and 62 us); a bf16 cache:
   // 2 rows 52.6 and 52.8 us, 16 rows (one of 1868) 12.9 and 14.4 us, 26 rows 61 and 67 us.
-  p.few = codes && head_dim == 128 && rows <= tg::kTreeRowsMax;
+  p.few = codes && rows <= tg::kTreeRowsMax;
   const int warps = tg::tree_rows_warps(rows);
   p.hw = p.few ? (n_hkv < warps ? n_hkv : warps) : 1;
   p.kw = p.few ? warps / p.hw : 2;
@@ -1154,7 +1155,10 @@ extern "C" tg_status tg_tree_attention(
   a.slots = p.slots;
   a.status = tg::status_word();
   if (!a.status) return TG_ERR_CUDA;
-  if (p.few) return launch_combine<128>(a, tg::launch_tree_rows(a, cache_dtype, stream), stream);
+  if (p.few) {
+    const tg_status r = tg::launch_tree_rows(a, head_dim, cache_dtype, stream);
+    return head_dim == 128 ? launch_combine<128>(a, r, stream) : launch_combine<64>(a, r, stream);
+  }
   if (head_dim == 128) {
     if (cache_dtype == TG_BF16) return launch_tree<128, TG_BF16>(a, stream);
     return cache_dtype == TG_I8 ? launch_tree<128, TG_I8>(a, stream) : launch_tree<128, TG_E4M3>(a, stream);

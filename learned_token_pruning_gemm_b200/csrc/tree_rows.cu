@@ -1,5 +1,5 @@
-// tg_tree_attention for few rows (drafted tokens x query heads of a KV head, up to 16, head
-// dim 128) over a cache of codes: the part over the cache. There is little to multiply per
+// tg_tree_attention for few rows (drafted tokens x query heads of a KV head, up to 16) over a
+// cache of codes: the part over the cache. There is little to multiply per
 // byte of cache then, and tree_attn_kernel, which widens every code to an operand tile for 128
 // rows, takes longer over the widening than this kernel over everything. Here all warps run
 // the same code, straight from a TMA ring into the register fragments of m16n8k16 products,
@@ -17,7 +17,8 @@
 // operands agree, so that every thread (g = lane / 4, i = lane % 4) reads 16-byte pieces:
 //   S^T: dims 32 i .. 32 i + 31 of keys g and g + 8;
 //   O^T: dims 16 g .. 16 g + 15 of keys 2 i, 2 i + 1, 2 i + 8 and 2 i + 9: product t holds the
-//        dims at places 2 t and 2 t + 1 of these.
+//        dims at places 2 t and 2 t + 1 of these
+// (head dim 64: half of these, and 8-byte pieces of V).
 // What bounds it is the instructions, about 480 a unit, and their latency at 12 to 16 warps an SM
 // (43% of issue slots busy). 32 sequences of 1868 e4m3 rows of eight heads, a token of 16 heads:
 // 37.6 us with the combining kernel (33 without; 19.4 us is the read at a plain copy's
@@ -43,13 +44,13 @@ using tg::widen4;
 // pass under the others' work; registers say how many, and the ring takes the rest of the
 // shared memory. Single tokens as below: 37.6 us with 2 CTAs of 8 warps, 39.0 with 4 of 4
 // (a ring of 5), 43.8 with 3 of 4 (a ring of 8), 61.9 with 5 of 4 (registers spill).
-template <int NT>
+template <int DH, int NT>
 struct Cfg {
   static constexpr int kWarps = NT == 1 ? 8 : 4;   // of a CTA
   static constexpr int kCtas = NT == 1 ? 2 : 3;    // an SM
-  static constexpr int kRing = NT == 1 ? 5 : 7;    // tiles
+  static constexpr int kRing = (NT == 1 ? 5 : 7) * (128 / DH);   // tiles
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kTile = 16 * kWarps * 128;  // bytes of a K or V tile, at most
+  static constexpr int kTile = 16 * kWarps * DH;   // bytes of a K or V tile, at most
   static_assert(kRing >= 4, "a unit's tiles are asked for while the one before is in use");
 };
 
@@ -78,11 +79,11 @@ struct Cursor {
   }
 };
 
-template <int NT>
+template <int DH, int NT>
 struct RowSmem {
-  using C = Cfg<NT>;
+  using C = Cfg<DH, NT>;
   uint8_t tile[C::kRing][C::kTile];
-  uint2 q[C::kWarps][NT][8][32];       // B fragments of each warp's queries
+  uint2 q[C::kWarps][NT][DH / 16][32];       // B fragments of each warp's queries
   float2 cg[C::kWarps][8 * NT];        // each row's logit factor and gain, log2 domain
   uint64_t full[C::kRing], empty[C::kRing];
   Cursor next;                      // the unit that is loaded next, and
@@ -98,17 +99,17 @@ struct RowSmem {
 // Loads tiles as far as the ring reaches (K at even places, V at odd ones): tile t needs
 // tile t - kRing to be consumed by every warp, which is waited for, and all before
 // `consumed` are by this one. One thread.
-template <int NT>
-__device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<NT>& S, const CUtensorMap* tm_k,
+template <int DH, int NT>
+__device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<DH, NT>& S, const CUtensorMap* tm_k,
                                        const CUtensorMap* tm_v, int consumed) {
-  using C = Cfg<NT>;
+  using C = Cfg<DH, NT>;
   const tg::TreeSeqs Q = S.seqs(A.batch);
   int t = S.issued;
   Cursor c = S.next;
   while (t < consumed + C::kRing && c.u < c.u1) {
     const int s = t % C::kRing;
     if (t >= C::kRing && !wait(&S.empty[s], ((t / C::kRing) - 1) & 1, A.status, &S.abort_flag)) break;
-    tg::mbar_arrive_expect_tx(&S.full[s], A.hw * A.unit * 128);
+    tg::mbar_arrive_expect_tx(&S.full[s], A.hw * A.unit * DH);
     tg::tma_load_3d(S.tile[s], t & 1 ? tm_v : tm_k, &S.full[s], 0, c.b * A.cap + c.j * A.unit, c.group * A.hw);
     if (t & 1) c.advance(A, Q);
     ++t;
@@ -141,16 +142,16 @@ __device__ __forceinline__ void cp8(void* dst, const void* src) {
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <int kType, int NT>
-__global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
+template <int kType, int DH, int NT>
+__global__ void __launch_bounds__(Cfg<DH, NT>::kThreads, Cfg<DH, NT>::kCtas)
     tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ TreeArgs A) {
   constexpr bool kE4m3 = kType == TG_E4M3;
   constexpr uint32_t kFlip = kType == TG_I8 ? 0x80808080u : 0u;
-  using C = Cfg<NT>;
+  using C = Cfg<DH, NT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (tg::smem_u32(smem_raw) & 1023u)) & 1023u;
-  RowSmem<NT>& S = *reinterpret_cast<RowSmem<NT>*>(smem_raw + pad);
+  RowSmem<DH, NT>& S = *reinterpret_cast<RowSmem<DH, NT>*>(smem_raw + pad);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, i4 = lane & 3;
   if (tid == 0) {
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
   if (loader) {
     S.issued = 0;
     S.next = c;
-    row_loads<NT>(A, S, &tm_k, &tm_v, 0);
+    row_loads<DH, NT>(A, S, &tm_k, &tm_v, 0);
   }
   __syncwarp();
 
@@ -183,7 +184,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
   // returns at once: the loops below take the same steps either way.
   const int rows = A.group * A.n_draft;
   const int hd = warp / A.kw, k0 = 16 * (warp - hd * A.kw);   // head of the item, first key of the unit
-  float o[NT][8][4];                  // product t: dims at places 2t, 2t + 1 x rows 2 i4, 2 i4 + 1
+  constexpr int kT = DH / 16;         // products of a unit, of either kind
+  float o[NT][kT][4];                  // product t: dims at places 2t, 2t + 1 x rows 2 i4, 2 i4 + 1
   float m[NT][2], l[NT][2];           // of rows 2 i4 and 2 i4 + 1 of every tile
   bool first = true;
   int r = 0;
@@ -214,15 +216,15 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
 #pragma unroll 1
       for (int nt = 0; nt < NT; ++nt) {   // rows behind the last: any row that is there
         const int row = min(8 * nt + g, rows - 1), tok = tg::token_of(A, row);
-        const __nv_bfloat16* p = A.q + (row_q + tok * A.n_hq + row - tok * A.group) * 128;
+        const __nv_bfloat16* p = A.q + (row_q + tok * A.n_hq + row - tok * A.group) * DH;
 #pragma unroll
-        for (int t = 0; t < 8; ++t)   // dims as the keys' below
+        for (int t = 0; t < kT; ++t)   // dims as the keys' below
           cp8(&S.q[warp][nt][t][lane],
-              p + 32 * i4 + 4 * t);
+              p + DH / 4 * i4 + 4 * t);
       }
       if (lane < 8 * NT) {
         const int row = min(lane, rows - 1), hq = kvh * A.group + row - tg::token_of(A, row) * A.group;
-        S.cg[warp][lane] = make_float2(tg::kLog2e / (sqrtf(128.f) * A.tau[hq]), A.gain[hq] * tg::kLog2e);
+        S.cg[warp][lane] = make_float2(tg::kLog2e / (sqrtf(static_cast<float>(DH)) * A.tau[hq]), A.gain[hq] * tg::kLog2e);
       }
       cp_wait_all();
       __syncwarp();
@@ -230,10 +232,10 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
       // (exponent field e) to [2^8, 2^9), so that values down to 2^-22 of it stay exact
 #pragma unroll 1
       for (int nt = 0; nt < NT; ++nt) {
-        uint2 x[8];
+        uint2 x[kT];
         uint32_t mx = 0;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
+        for (int t = 0; t < kT; ++t) {
           x[t] = S.q[warp][nt][t][lane];
           mx = max_u16x2(mx, max_u16x2(x[t].x & 0x7FFF7FFFu, x[t].y & 0x7FFF7FFFu));
         }
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
         const int e = max(static_cast<int>(max(mx >> 16, mx & 0xFFFFu) >> 7), 9);
         const float down = __int_as_float((262 - e) << 23);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < kT; ++t)
           S.q[warp][nt][t][lane] = make_uint2(bf16x2_to_f16x2(x[t].x, down), bf16x2_to_f16x2(x[t].y, down));
         if (i4 == 0) S.cg[warp][8 * nt + g].x *= __int_as_float((e - 8) << 23);
       }
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
         m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < kT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.f;
       }
@@ -264,16 +266,16 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
     __syncwarp();
     if (any) {
       // a head's rows of the tile follow each other; the places of both keys among eight are g
-      const uint8_t* p = S.tile[s] + (hd * A.unit + k0 + g) * 128;
+      const uint8_t* p = S.tile[s] + (hd * A.unit + k0 + g) * DH;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[nt][e] = 0.f;
       float z2[NT][4] = {};   // every other product's sums: two chains are half as long
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint8_t* at = p + (((2 * i4 + i) ^ g) << 4);
-        const uint4 x0 = *reinterpret_cast<const uint4*>(at), x1 = *reinterpret_cast<const uint4*>(at + 8 * 128);
+      for (int i = 0; i < DH / 64; ++i) {
+        const uint8_t* at = p + ((DH == 128 ? (2 * i4 + i) ^ g : i4 ^ (g >> 1)) << 4);
+        const uint4 x0 = *reinterpret_cast<const uint4*>(at), x1 = *reinterpret_cast<const uint4*>(at + 8 * DH);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {   // product t: four dims of the thread's part
           const int t = 4 * i + e;
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
     __syncwarp();
     if (lane == 0) tg::mbar_arrive(&S.empty[s]);
     // the ring goes on where every warp is through with the unit before
-    if (loader) row_loads<NT>(A, S, &tm_k, &tm_v, r);
+    if (loader) row_loads<DH, NT>(A, S, &tm_k, &tm_v, r);
     __syncwarp();
     uint32_t b[NT][2];   // the weights as fragments
     if (any) {
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
             m[nt][e] = t;
             l[nt][e] *= alpha;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kT; ++k) {
               o[nt][k][e] *= alpha;
               o[nt][k][2 + e] *= alpha;
             }
@@ -358,19 +360,26 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
     __syncwarp();
     if (any) {
       // ---- O^T += V^T P^T ----
-      uint4 xv[4];   // keys 2 i4 + {0, 1, 8, 9}
+      uint32_t xv[4][DH / 32];   // keys 2 i4 + {0, 1, 8, 9}
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int key = k0 + 2 * i4 + (y & 1) + 8 * (y >> 1);
-        xv[y] = *reinterpret_cast<const uint4*>(S.tile[sv] + (hd * A.unit + key) * 128 + ((g ^ (key & 7)) << 4));
-        if (nv - k0 < 16 && key >= nv) xv[y] = make_uint4(0, 0, 0, 0);   // rows behind the end weigh 0
+        const uint8_t* p = S.tile[sv] + (hd * A.unit + key) * DH;
+        const bool ok = nv - k0 >= 16 || key < nv;   // rows behind the end weigh 0
+        if constexpr (DH == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p + ((g ^ (key & 7)) << 4));
+          xv[y][0] = ok ? x.x : 0u, xv[y][1] = ok ? x.y : 0u, xv[y][2] = ok ? x.z : 0u, xv[y][3] = ok ? x.w : 0u;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(p + (((g >> 1) ^ ((key >> 1) & 3)) << 4) + 8 * (g & 1));
+          xv[y][0] = ok ? x.x : 0u, xv[y][1] = ok ? x.y : 0u;
+        }
       }
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
+      for (int t = 0; t < kT; ++t) {
         uint32_t a[4];   // [key half][place]
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t x = word_of(xv[2 * h], t >> 1), y = word_of(xv[2 * h + 1], t >> 1);
+          const uint32_t x = xv[2 * h][t >> 1], y = xv[2 * h + 1][t >> 1];
           widen4<kE4m3>(__byte_perm(x, y, t & 1 ? 0x7362 : 0x5140) ^ kFlip, a[2 * h], a[2 * h + 1]);
         }
 #pragma unroll
@@ -384,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
     if (first && head) {
       // CTA c and item i (numbered over all sequences): slot c + i grows along the units
       const int64_t slot = (static_cast<int64_t>(blockIdx.x + c.b * tg::head_groups(A) + c.group) * A.hw * A.kw + warp) * rows;
-      float* pl = tg::part_ml(A, rows, 128) + slot * 2;
+      float* pl = tg::part_ml(A, rows, DH) + slot * 2;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -394,9 +403,9 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
           for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
           const int row = 8 * nt + 2 * i4 + e;
           if (row >= rows) continue;
-          float* p = A.part + (slot + row) * 128 + 16 * g;   // the thread's 16 dims
+          float* p = A.part + (slot + row) * DH + DH / 8 * g;   // the thread's dims
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
+          for (int h = 0; h < kT / 2; ++h)
             *reinterpret_cast<float4*>(p + 4 * h) =
                 make_float4(o[nt][2 * h][e], o[nt][2 * h][2 + e], o[nt][2 * h + 1][e], o[nt][2 * h + 1][2 + e]);
           if (g == 0) *reinterpret_cast<float2*>(pl + 2 * row) = make_float2(m[nt][e], sum);
@@ -409,30 +418,32 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas)
       wait(&S.full[i % C::kRing], (i / C::kRing) & 1, A.status, nullptr);
 }
 
-template <int kType, int NT>
+template <int kType, int DH, int NT>
 tg_status launch(const TreeArgs& a, cudaStream_t st) {
-  using C = Cfg<NT>;
+  using C = Cfg<DH, NT>;
   CUtensorMap tk, tv;
-  if (!tg::tree_cache_map(a, a.kc, 128, true, a.unit, a.hw, &tk) ||
-      !tg::tree_cache_map(a, a.vc, 128, true, a.unit, a.hw, &tv))
+  if (!tg::tree_cache_map(a, a.kc, DH, true, a.unit, a.hw, &tk) ||
+      !tg::tree_cache_map(a, a.vc, DH, true, a.unit, a.hw, &tv))
     return TG_ERR_CUDA;
-  constexpr int fixed = sizeof(RowSmem<NT>) + 1024;
+  constexpr int fixed = sizeof(RowSmem<DH, NT>) + 1024;
   static_assert((fixed + 1024 + 512) * C::kCtas <= 233472, "an SM's shared memory");
   const int smem = fixed + 9 * a.batch + 8;
-  if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_rows_kernel<kType, NT>), smem)) return TG_ERR_CUDA;
-  return tg::launch(tree_rows_kernel<kType, NT>, dim3(a.n_cta), dim3(C::kThreads), smem, st, 0, tk, tv, a);
+  if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_rows_kernel<kType, DH, NT>), smem)) return TG_ERR_CUDA;
+  return tg::launch(tree_rows_kernel<kType, DH, NT>, dim3(a.n_cta), dim3(C::kThreads), smem, st, 0, tk, tv, a);
 }
 
 template <int kType>
-tg_status launch_type(const TreeArgs& a, cudaStream_t st) {
-  return a.group * a.n_draft <= 8 ? launch<kType, 1>(a, st) : launch<kType, 2>(a, st);
+tg_status launch_type(const TreeArgs& a, int head_dim, cudaStream_t st) {
+  const bool one = a.group * a.n_draft <= 8;
+  if (head_dim == 128) return one ? launch<kType, 128, 1>(a, st) : launch<kType, 128, 2>(a, st);
+  return one ? launch<kType, 64, 1>(a, st) : launch<kType, 64, 2>(a, st);
 }
 
 }  // namespace
 
-int tg::tree_rows_ctas(int rows) { return 148 * (rows <= 8 ? Cfg<1>::kCtas : Cfg<2>::kCtas); }
-int tg::tree_rows_warps(int rows) { return rows <= 8 ? Cfg<1>::kWarps : Cfg<2>::kWarps; }
+int tg::tree_rows_ctas(int rows) { return 148 * (rows <= 8 ? Cfg<128, 1>::kCtas : Cfg<128, 2>::kCtas); }
+int tg::tree_rows_warps(int rows) { return rows <= 8 ? Cfg<128, 1>::kWarps : Cfg<128, 2>::kWarps; }
 
-tg_status tg::launch_tree_rows(const TreeArgs& a, tg_dtype cache_dtype, cudaStream_t stream) {
-  return cache_dtype == TG_I8 ? launch_type<TG_I8>(a, stream) : launch_type<TG_E4M3>(a, stream);
+tg_status tg::launch_tree_rows(const TreeArgs& a, int head_dim, tg_dtype cache_dtype, cudaStream_t stream) {
+  return cache_dtype == TG_I8 ? launch_type<TG_I8>(a, head_dim, stream) : launch_type<TG_E4M3>(a, head_dim, stream);
 }
