@@ -6,17 +6,15 @@
 // is set in tree_mask[b][t]:
 //     z_j = q . k_j / (sqrt(dh) tau_h) + g_h s_j,   O = sum_j softmax_j(z) v_j.
 //
-// The cache is read once per KV head and serves all drafted tokens and query heads of the
-// group: with R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product and back.
+// The cache is read once per KV head and 256 rows and serves all drafted tokens and query heads
+// of the group: with R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product and back.
 // Here the rows are packed into M = 128 tiles (row r is token r / G, head r % G) and both
-// products run on the tensor cores with accumulators in TMEM; up to 16 rows
-// over codes take the kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128
-// cache rows; what a CTA has of an item it leaves as partials (max, sum, O), and the
+// products run on the tensor cores with accumulators in TMEM; up to 16 rows over codes take the
+// kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128 cache rows; what a CTA has of an item it leaves as partials (max, sum, O), and the
 // kernel at the end adds the partials up in CTA order, so results do not depend on timing,
 // and brings in the drafted rows that each token sees.
 //
-// A CTA has two sides, each with its own softmax warps, S buffers and O in
-// TMEM. The sides take the two row tiles of an item, which then share every K and V tile
+// A CTA has two sides, each with its own softmax warps, S buffers and O in TMEM. The sides take the two row tiles of an item, which then share every K and V tile
 // and its widening; of an item of one row tile they take half of every unit's keys each,
 // and each leaves a partial. A job is 64 keys of a side; it has two S buffers, so that its
 // products run while the softmax is at the job before.
@@ -34,10 +32,8 @@
 //   warps 4-19   softmax, 16 rows a warp, those with rows only: logits in the log2 domain
 //                less the row's running reference, which moves only when one exceeds it by more
 //                than it may (O is then rescaled in TMEM).
-// What bounds it: the softmax's instructions (about 9 an element with the scales, 16 warps an SM,
-// half of the issue slots busy), then the products (two thirds of the MMA rate would be
-// reached at twice the softmax's speed) and, with few rows, the way of a unit through the
-// roles. 2 x 64 tokens of 32 heads over 65500 int8 rows of four heads: 226 us (0.61 PFLOP/s, 84.5
+// What bounds it: the softmax's instructions (57% of the issue slots are busy, at 24 warps an SM;
+// the tensor pipe 30% of the time) and, with few rows, the way of a unit through the roles. 2 x 64 tokens of 32 heads over 65500 int8 rows of four heads: 226 us (0.61 PFLOP/s, 84.5
 // us at a plain GEMM's rate; 200 us without the combining kernel); 8 x 13 tokens of 16 heads
 // over 50 thousand bf16 rows of eight: 57 us (31.3 us at a plain copy's rate). Steps that
 // made it so, on the long case: one row tile a CTA 379 us; two tiles that share K, V and
