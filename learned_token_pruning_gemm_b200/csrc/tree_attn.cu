@@ -82,7 +82,9 @@ struct TreeSmem {
   uint8_t k[C::kK][C::kHalves][kHalfBytes];
   uint8_t v[C::kV][C::kHalves][kHalfBytes];
   uint8_t raw[C::kRaw][C::kRawBytes];
-  float key[kKeyStages][kQ ? 4 : 1][kBN];   // score, then (codes) key scale, log2 of the value scale, its inverse
+  // score; codes: scores and key scales of two keys side by side (2 x kBN), then log2 of the value
+  // scale, then its inverse
+  alignas(16) float key[kKeyStages][kQ ? 4 : 1][kBN];
   int base[tg::kTreeMaxBatch + 1];
   int len[tg::kTreeMaxBatch];
   uint8_t dl[tg::kTreeMaxBatch];
@@ -400,9 +402,10 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           const int j = lane + 32 * i;
           const int64_t row = row0 + min(j, last);
           if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
-          cp4(&S.key[s][0][j], A.sc + row);
+          float* at = S.key[s][0] + (kQ ? 4 * (j >> 1) + (j & 1) : j);
+          cp4(at, A.sc + row);
           if constexpr (kQ) {
-            cp4(&S.key[s][1][j], A.ks + row * A.n_hkv + la.kvh);
+            cp4(at + 2, A.ks + row * A.n_hkv + la.kvh);
             cp4(&S.key[s][2][j], A.vs + row * A.n_hkv + la.kvh);
           }
         }
@@ -585,15 +588,17 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
             tg::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float2 sk = *reinterpret_cast<const float2*>(key + 8 * i);
               float x[4] = {__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
                             __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])};
-              float2 lv = {};
+              float2 sk, lv = {};
               if constexpr (kQ) {
-                const float2 ks = *reinterpret_cast<const float2*>(key + kBN + 8 * i);
+                const float4 both = *reinterpret_cast<const float4*>(S.key[s][0] + 2 * (kJob * half + cq + 8 * i));
+                sk = make_float2(both.x, both.y);
                 lv = *reinterpret_cast<const float2*>(key + 2 * kBN + 8 * i);
-                fmul2(x[0], x[1], x[0], x[1], ks.x, ks.y);
-                fmul2(x[2], x[3], x[2], x[3], ks.x, ks.y);
+                fmul2(x[0], x[1], x[0], x[1], both.z, both.w);
+                fmul2(x[2], x[3], x[2], x[3], both.z, both.w);
+              } else {
+                sk = *reinterpret_cast<const float2*>(key + 8 * i);
               }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
