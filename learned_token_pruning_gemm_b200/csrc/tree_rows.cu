@@ -1,8 +1,7 @@
 // tg_tree_attention for few rows (drafted tokens x query heads of a KV head, up to 16) over a
-// cache of codes: the part over the cache. There is little to multiply per
-// byte of cache then, and tree_attn_kernel, which widens every code to an operand tile for 128
-// rows, takes longer over the widening than this kernel over everything. Here all warps run
-// the same code, straight from a TMA ring into the register fragments of m16n8k16 products,
+// cache of codes: the part over the cache. There is little to multiply per byte of cache then,
+// and tree_attn_kernel, which widens every code to an operand tile for 128 rows, takes longer
+// over the widening than this kernel over everything. Here all warps run the same code, straight from a TMA ring into the register fragments of m16n8k16 products,
 // each with its own running reference, sums and O, so nothing joins them but the ring.
 //
 // A unit is 16 keys a warp: the warps share hw KV heads of the same cache rows (all of them
@@ -37,12 +36,9 @@ using tg::pack_f16x2;
 using tg::wait;
 using tg::widen4;
 
-// NT: tiles of eight rows. Several CTAs share an SM, so that one's start and end of an item
-// pass under the others' work; how many goes by registers, then the ring takes the rest of
-// the shared memory.
 // NT tiles of eight rows. Several CTAs share an SM, so that one's start and end of an item
 // pass under the others' work; registers say how many, and the ring takes the rest of the
-// shared memory. Single tokens as below: 37.6 us with 2 CTAs of 8 warps, 39.0 with 4 of 4
+// shared memory. Single tokens as above: 37.6 us with 2 CTAs of 8 warps, 39.0 with 4 of 4
 // (a ring of 5), 43.8 with 3 of 4 (a ring of 8), 61.9 with 5 of 4 (registers spill).
 template <int DH, int NT>
 struct Cfg {
