@@ -114,10 +114,12 @@ __device__ __noinline__ void row_loads(const TreeArgs& A, RowSmem<DH, NT>& S, co
   S.next = c;
 }
 
-// One 16 x 8 x 16 product, fp16 operands, fp32 sums.
+// One 16 x 8 x 16 product, fp16 operands, fp32 sums. volatile: it stays before the arrival that
+// gives its tile back, so that the tile's loads are over by then.
 __device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+               "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
