@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(kThreads, kBwd ? 3 : 5) norm_rope_kernel(const
           IO::unpack(vb[u], xb);
 #pragma unroll
           for (int j = 0; j < kP; ++j) ss = fma2(xa[j], xa[j], fma2(xb[j], xb[j], ss));
-          const float r = __frsqrt_rn(fmaf(head_sum<LPH>(ss.x + ss.y), inv_dh, A.eps));
+          float r = __frsqrt_rn(fmaf(head_sum<LPH>(ss.x + ss.y), inv_dh, A.eps));
+          // A head that is not there has r = 0, not 1 / sqrt(eps): infinite without an epsilon, that
+          // times its zeros would be NaN in the weight gradients' sums.
+          if (kBwd && h >= heads) r = 0.f;
           if constexpr (!kBwd) {
 #pragma unroll
             for (int j = 0; j < kP; ++j) {
