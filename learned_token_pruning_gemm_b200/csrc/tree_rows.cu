@@ -322,17 +322,19 @@ __global__ void __launch_bounds__(Cfg<DH, NT>::kThreads, Cfg<DH, NT>::kCtas)
           if (k0 + g + 8 * x >= nv) y0 = y1 = -INFINITY;   // a key that is not there
         }
         // A row's reference is a whole number 6 below its largest logit or less (which keeps small
-        // fp16 weights exact) when it is set, and moves when a logit exceeds it by 2^14, so that
-        // the weights stay in fp16's range.
+        // fp16 weights exact) when it is set, and moves when a logit exceeds it by more than 14, so
+        // that the weights are 2^14 at most, in fp16's range. The difference is compared, as the
+        // weights take it: a sum m + 14 of large numbers is rounded to their last place, and
+        // weights of 2^16 passed under it.
         constexpr float kLift = 6.f, kMost = kLift + tg::kRescaleThreshold;
         const float m0 = fmaxf(z[nt][0], z[nt][2]), m1 = fmaxf(z[nt][1], z[nt][3]);
-        if (__any_sync(0xFFFFFFFFu, m0 > m[nt][0] + kMost || m1 > m[nt][1] + kMost)) {
+        if (__any_sync(0xFFFFFFFFu, m0 - m[nt][0] > kMost || m1 - m[nt][1] > kMost)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float t = e ? m1 : m0;
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, x));
-            t = t > m[nt][e] + kMost ? ceilf(t) - kLift : m[nt][e];
+            t = t - m[nt][e] > kMost ? ceilf(t) - kLift : m[nt][e];
             const float alpha = t == m[nt][e] ? 1.f : tg::exp2_approx(m[nt][e] - t);
             m[nt][e] = t;
             l[nt][e] *= alpha;
