@@ -6,6 +6,7 @@ status. All arithmetic happens in the CUDA kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Optional, Sequence
@@ -413,10 +414,22 @@ def _ptr(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
-def _keep_for(stream, *tensors) -> None:
-    """Tensors allocated here, on the current stream, but used on a given one."""
-    for t in tensors:
-        t.record_stream(stream)
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call on a given stream allocates: with that stream current, so that the
+    allocator hands out blocks whose earlier use is over when the call's kernels run. (A block
+    freed on the current stream may still be in use by kernels queued there.)"""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *tensors) -> None:
+    """Outputs that were allocated with `stream` current and go to a caller who works on the
+    current stream: their blocks are not given away while that one still uses them."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def _heads(t: torch.Tensor, T: int, H: int, dh: int, name: str, dtype) -> int:
@@ -456,7 +469,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
     q_st = _heads(q, T, hq, dh, "q", dt)
     k_st = _heads(k, T, hkv, dh, "k", dt)
     if out is None:
-        qo, ko = q.new_empty((T, hq, dh)), q.new_empty((T, hkv, dh))
+        with _on(stream):
+            qo, ko = q.new_empty((T, hq, dh)), q.new_empty((T, hkv, dh))
         qo_st, ko_st = hq * dh, hkv * dh
     else:
         qo, ko = out
@@ -467,8 +481,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
           (q.data_ptr(), q_st, k.data_ptr(), k_st, _DT[dt], T, hq, hkv, dh, rot,
            _ptr(q_weight, "q_weight"), _ptr(k_weight, "k_weight"), float(eps), float(rope_base), _ptr(pos, "pos"),
            qo.data_ptr(), qo_st, ko.data_ptr(), ko_st))
-    if out is None and stream is not None:
-        _keep_for(stream, qo, ko)
+    if out is None:
+        _hand_over(stream, qo, ko)
     return qo, ko
 
 
@@ -490,10 +504,11 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
     k_st = _heads(k, T, hkv, dh, "k", dt)
     gq_st = _heads(dq_out, T, hq, dh, "dq_out", dt)
     gk_st = _heads(dk_out, T, hkv, dh, "dk_out", dt)
-    new = []
+    new = ()
     if grads is None:
-        grads = new = [q.new_empty((T, hq, dh)), q.new_empty((T, hkv, dh)),
-                       torch.empty_like(q_weight), torch.empty_like(k_weight)]
+        with _on(stream):
+            grads = new = (q.new_empty((T, hq, dh)), q.new_empty((T, hkv, dh)),
+                           torch.empty_like(q_weight), torch.empty_like(k_weight))
     dq, dk, dwq, dwk = grads
     dq_st = _heads(dq, T, hq, dh, "dq", dt)
     dk_st = _heads(dk, T, hkv, dh, "dk", dt)
@@ -502,8 +517,8 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
     lib = _lib.load()
     if workspace is None:
         need = lib.tg_qk_norm_rope_bwd_workspace_size(T, hq, hkv, dh)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        new = [*new, workspace]
+        with _on(stream):
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     _call(lib.tg_qk_norm_rope_bwd, "tg_qk_norm_rope_bwd", stream,
           (q, k, q_weight, k_weight, pos, dq_out, dk_out, dq, dk, dwq, dwk, workspace),
           (q.data_ptr(), q_st, k.data_ptr(), k_st, dq_out.data_ptr(), gq_st, dk_out.data_ptr(), gk_st,
@@ -511,8 +526,7 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
            float(rope_base), _ptr(pos, "pos"), dq.data_ptr(), dq_st, dk.data_ptr(), dk_st,
            _ptr(dwq, "dq_weight"), _ptr(dwk, "dk_weight"), _ptr(workspace, "workspace"),
            workspace.numel() * workspace.element_size()))
-    if stream is not None:
-        _keep_for(stream, *new)
+    _hand_over(stream, *new)
     return dq, dk, dwq, dwk
 
 
@@ -579,8 +593,9 @@ def quant_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torc
     if dtype not in _DT:
         raise TokenGateError(f"quant_cache_read: unsupported dtype {dtype}")
     if out is None:
-        k = k_cache.new_empty((total, hkv, dh), dtype=dtype)
-        v, s_out = torch.empty_like(k), s_cache.new_empty(total)
+        with _on(stream):
+            k = k_cache.new_empty((total, hkv, dh), dtype=dtype)
+            v, s_out = torch.empty_like(k), s_cache.new_empty(total)
     else:
         k, v, s_out = out
         if k.dtype not in _DT:
@@ -594,8 +609,8 @@ def quant_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torc
            _ptr(v_scale, "v_scale"), _ptr(s_cache, "s_cache"), _ptr(cache_len, "cache_len"),
            None if start is None else _ptr(start, "start"), _ptr(cu_rows, "cu_rows"), total, B, cap, hkv,
            dh, _CODE_DT[k_cache.dtype], _DT[k.dtype], _ptr(k, "k"), _ptr(v, "v"), _ptr(s_out, "s")))
-    if out is None and stream is not None:
-        _keep_for(stream, k, v, s_out)
+    if out is None:
+        _hand_over(stream, k, v, s_out)
     return k, v, s_out
 
 
@@ -667,17 +682,18 @@ def tree_attention(q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor
     if q.dtype != torch.bfloat16:
         raise TokenGateError(f"q must be {torch.bfloat16}, got {q.dtype}")
     max_len = int(max_len)
-    new = []
+    new = ()
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        new.append(out)
+        with _on(stream):
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        new = (out,)
     else:
         _shape(out, q.shape, "out", torch.bfloat16)
     lib = _lib.load()
     if workspace is None:
         need = lib.tg_tree_attention_workspace_size(B, T, max_len, hq, hkv, dh)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        new.append(workspace)
+        with _on(stream):
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     _call(lib.tg_tree_attention, "tg_tree_attention", stream,
           (q, k_draft, v_draft, s_draft, tree_mask, draft_len, k_cache, v_cache, k_scale, v_scale, s_cache,
            cache_len, gain, tau, out, workspace),
@@ -686,8 +702,7 @@ def tree_attention(q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor
            _ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache"), cdt, ks, vs, _ptr(s_cache, "s_cache"),
            _ptr(cache_len, "cache_len"), cap, max_len, hq, hkv, dh, _ptr(gain, "gain"), _ptr(tau, "tau"),
            _ptr(out, "out"), _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()))
-    if stream is not None:
-        _keep_for(stream, *new)
+    _hand_over(stream, *new)
     return out
 
 
