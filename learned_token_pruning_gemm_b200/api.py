@@ -48,6 +48,24 @@ def _shape(t: torch.Tensor, shape, name: str, dtype=None) -> None:
         raise TokenGateError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call on a given stream allocates: with that stream current, so that the
+    allocator hands out blocks whose earlier use is over when the call's kernels run. (A block
+    freed on the current stream may still be in use by kernels queued there.)"""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *tensors) -> None:
+    """Outputs that were allocated with `stream` current and go to a caller who works on the
+    current stream: their blocks are not given away while that one still uses them."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 def abi_version() -> int:
     return _lib.load().tg_abi_version()
 
@@ -61,13 +79,17 @@ def gate_score(x: torch.Tensor, w1: torch.Tensor, b1: torch.Tensor, w2: torch.Te
         raise TokenGateError("gate_score: x [N,d] and w1 [h,d] must share a dtype (f32/bf16)")
     _numel(b1, h, "b1")
     _numel(w2, h, "w2")
+    new = ()
     if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=x.device)
+        with _on(stream):
+            out = torch.empty(n, dtype=torch.float32, device=x.device)
+        new = (out,)
     _numel(out, n, "scores")
     st = _lib.load().tg_gate_score(_cuda(x, "x"), _DT[x.dtype], n, d, _cuda(w1, "w1"),
                                    _cuda(b1, "b1", torch.float32), _cuda(w2, "w2", torch.float32),
                                    float(b2), h, _cuda(out, "scores", torch.float32), _stream(stream))
     check(st, "tg_gate_score")
+    _hand_over(stream, *new)
     return out
 
 
@@ -85,14 +107,20 @@ def select_topk(scores: torch.Tensor, cu_seqlens: torch.Tensor, doc_begin: torch
     _numel(cu_seqlens, B + 1, "cu_seqlens")
     _numel(doc_end, B, "doc_end")
     _numel(k_doc, B, "k_doc")
+    new = []
+
+    def empty(n, dtype):
+        with _on(stream):
+            new.append(torch.empty(n, dtype=dtype, device=dev))
+        return new[-1]
     if kept_idx is None:
-        kept_idx = torch.empty(total_kept, dtype=torch.int32, device=dev)
+        kept_idx = empty(total_kept, torch.int32)
     if kept_scores is None and want_scores:
-        kept_scores = torch.empty(total_kept, dtype=torch.float32, device=dev)
+        kept_scores = empty(total_kept, torch.float32)
     if kept_pos is None and want_pos:
-        kept_pos = torch.empty(total_kept, dtype=torch.int32, device=dev)
+        kept_pos = empty(total_kept, torch.int32)
     if cu_kept is None:
-        cu_kept = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        cu_kept = empty(B + 1, torch.int32)
     _numel(kept_idx, total_kept, "kept_idx")
     if kept_scores is not None:
         _numel(kept_scores, total_kept, "kept_scores")
@@ -108,6 +136,7 @@ def select_topk(scores: torch.Tensor, cu_seqlens: torch.Tensor, doc_begin: torch
         _cuda(kept_pos, "kept_pos", torch.int32) if kept_pos is not None else None,
         _cuda(cu_kept, "cu_kept", torch.int32), _stream(stream))
     check(st, "tg_select_topk")
+    _hand_over(stream, *new)
     if kept_pos is not None:
         return kept_idx, kept_scores, cu_kept, kept_pos
     return kept_idx, kept_scores, cu_kept
@@ -119,8 +148,10 @@ def compact_rows(srcs: Sequence[torch.Tensor], kept_idx: torch.Tensor,
     n = kept_idx.numel()
     if not srcs:
         raise TokenGateError("compact_rows: at least one source tensor")
+    new = ()
     if outs is None:
-        outs = [torch.empty((n,) + tuple(s.shape[1:]), dtype=s.dtype, device=s.device) for s in srcs]
+        with _on(stream):
+            outs = new = [torch.empty((n,) + tuple(s.shape[1:]), dtype=s.dtype, device=s.device) for s in srcs]
     k = len(srcs)
     if len(outs) != k:
         raise TokenGateError("compact_rows: one output per source")
@@ -134,6 +165,7 @@ def compact_rows(srcs: Sequence[torch.Tensor], kept_idx: torch.Tensor,
     st = _lib.load().tg_compact_kv(src_arr, dst_arr, rb, k, _cuda(kept_idx, "kept_idx", torch.int32),
                                    n, n_src, _stream(stream))
     check(st, "tg_compact_kv")
+    _hand_over(stream, *new)
     return list(outs)
 
 
@@ -154,8 +186,11 @@ def gated_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s_kept: t
     _numel(tau, hq, "tau")
     if cu_kept.numel() < 1:
         raise TokenGateError("cu_kept must have batch+1 >= 1 elements")
+    new = ()
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
+        new = (out,)
     _shape(out, q.shape, "out", q.dtype)
     if lse is not None:
         _shape(lse, (hq, K), "lse", torch.float32)
@@ -167,6 +202,7 @@ def gated_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s_kept: t
         int(max_kept), hq, hkv, dh, _cuda(out, "out"),
         _cuda(lse, "lse") if lse is not None else None, _stream(stream))
     check(st, "tg_gated_attention")
+    _hand_over(stream, *new)
     return out
 
 
@@ -190,10 +226,12 @@ def gated_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
     _numel(gain, hq, "gain")
     _numel(tau, hq, "tau")
     B = cu_kept.numel() - 1
+    new = ()
     if grads is None:
         f32 = dict(dtype=torch.float32, device=q.device)
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
-                 torch.empty(K, **f32), torch.empty(hq, **f32), torch.empty(hq, **f32))
+        with _on(stream):
+            grads = new = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
+                           torch.empty(K, **f32), torch.empty(hq, **f32), torch.empty(hq, **f32))
     dq, dk, dv, ds, dg, dt = grads
     _shape(dq, q.shape, "dq", q.dtype)
     _shape(dk, k.shape, "dk", q.dtype)
@@ -205,7 +243,8 @@ def gated_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
     need = int(lib.tg_gated_attention_bwd_workspace_size(_DT[q.dtype], B, K, int(max_kept), hq,
                                                            hkv, dh))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     nb = workspace.numel() * workspace.element_size()
     st = lib.tg_gated_attention_bwd(
         _cuda(q, "q"), _cuda(k, "k"), _cuda(v, "v"), _cuda(out, "out"), _cuda(dout, "dout"),
@@ -215,6 +254,7 @@ def gated_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
         _cuda(dk, "dk"), _cuda(dv, "dv"), _cuda(ds, "ds"), _cuda(dg, "dgain"), _cuda(dt, "dtau"),
         _cuda(workspace, "workspace"), nb, _stream(stream))
     check(st, "tg_gated_attention_bwd")
+    _hand_over(stream, *new)
     return dq, dk, dv, ds, dg, dt
 
 
@@ -245,12 +285,16 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: t
     if max_seqlen is None:
         cu_h = cu_seqlens.detach().to("cpu", torch.int64)
         max_seqlen = int((cu_h[1:] - cu_h[:-1]).max()) if B > 0 else 0
+    new = ()
     if out is None:
-        out = torch.empty_like(v)
+        with _on(stream):
+            out = torch.empty_like(v)
+        new = (out,)
     _shape(out, v.shape, "out", v.dtype)
     need = gated_delta_rule_workspace_size(B, T, H, dv)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     if workspace.dtype != torch.uint8 or workspace.numel() < need:
         raise TokenGateError(f"gated_delta_rule: workspace needs {need} bytes (uint8)")
     st = _lib.load().tg_gated_delta_rule(
@@ -259,6 +303,7 @@ def gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: t
         B, T, int(max_seqlen), H, dk, dv, _cuda(out, "out"), _cuda(workspace, "workspace"),
         workspace.numel(), _stream(stream))
     check(st, "tg_gated_delta_rule")
+    _hand_over(stream, *new)
     return out
 
 
@@ -272,10 +317,12 @@ def qkv_rope(xc: torch.Tensor, w_qkv: torch.Tensor, n_hq: int, n_hkv: int, pos: 
         raise TokenGateError("qkv_rope: w_qkv [(Hq+2Hkv)*dh, d] with the dtype of xc")
     dh = n_out // (n_hq + 2 * n_hkv)
     _numel(pos, K, "pos")
+    new = ()
     if out is None:
-        out = (torch.empty(K, n_hq, dh, dtype=xc.dtype, device=xc.device),
-               torch.empty(K, n_hkv, dh, dtype=xc.dtype, device=xc.device),
-               torch.empty(K, n_hkv, dh, dtype=xc.dtype, device=xc.device))
+        with _on(stream):
+            out = new = (torch.empty(K, n_hq, dh, dtype=xc.dtype, device=xc.device),
+                         torch.empty(K, n_hkv, dh, dtype=xc.dtype, device=xc.device),
+                         torch.empty(K, n_hkv, dh, dtype=xc.dtype, device=xc.device))
     q, k, v = out
     _shape(q, (K, n_hq, dh), "q", xc.dtype)
     _shape(k, (K, n_hkv, dh), "k", xc.dtype)
@@ -285,6 +332,7 @@ def qkv_rope(xc: torch.Tensor, w_qkv: torch.Tensor, n_hq: int, n_hkv: int, pos: 
                                  float(rope_base), _cuda(pos, "pos", torch.int32), _cuda(q, "q"),
                                  _cuda(k, "k"), _cuda(v, "v"), _stream(stream))
     check(st, "tg_qkv_rope")
+    _hand_over(stream, *new)
     return q, k, v
 
 
@@ -302,16 +350,21 @@ def compact_qkv_rope(x: torch.Tensor, kept_idx: torch.Tensor, w_qkv: torch.Tenso
         raise TokenGateError("compact_qkv_rope: w_qkv [(Hq+2Hkv)*dh, d] with the dtype of x")
     dh = n_out // (n_hq + 2 * n_hkv)
     _numel(pos, K, "pos")
+    new = []
     if write_xc:
         if xc is None:
-            xc = torch.empty(K, d, dtype=x.dtype, device=x.device)
+            with _on(stream):
+                xc = torch.empty(K, d, dtype=x.dtype, device=x.device)
+            new.append(xc)
         _shape(xc, (K, d), "xc", x.dtype)
     elif xc is not None:
         raise TokenGateError("compact_qkv_rope: xc given with write_xc=False")
     if out is None:
-        out = (torch.empty(K, n_hq, dh, dtype=x.dtype, device=x.device),
-               torch.empty(K, n_hkv, dh, dtype=x.dtype, device=x.device),
-               torch.empty(K, n_hkv, dh, dtype=x.dtype, device=x.device))
+        with _on(stream):
+            out = (torch.empty(K, n_hq, dh, dtype=x.dtype, device=x.device),
+                   torch.empty(K, n_hkv, dh, dtype=x.dtype, device=x.device),
+                   torch.empty(K, n_hkv, dh, dtype=x.dtype, device=x.device))
+        new += out
     q, k, v = out
     _shape(q, (K, n_hq, dh), "q", x.dtype)
     _shape(k, (K, n_hkv, dh), "k", x.dtype)
@@ -322,6 +375,7 @@ def compact_qkv_rope(x: torch.Tensor, kept_idx: torch.Tensor, w_qkv: torch.Tenso
         n_hq, n_hkv, dh, float(rope_base), _cuda(pos, "pos", torch.int32), _cuda(q, "q"),
         _cuda(k, "k"), _cuda(v, "v"), _stream(stream))
     check(st, "tg_compact_qkv_rope")
+    _hand_over(stream, *new)
     return xc, q, k, v
 
 
@@ -364,12 +418,16 @@ def gated_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     _shape(cache_len, (B,), "cache_len", torch.int32)
     _numel(gain, hq, "gain")
     _numel(tau, hq, "tau")
+    new = ()
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
+        new = (out,)
     _shape(out, q.shape, "out", q.dtype)
     need = decode_workspace_size(B, hq, dh, max(int(max_len), 1))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     if workspace.numel() * workspace.element_size() < need:
         raise TokenGateError(f"gated_decode: workspace needs {need} bytes")
     st = _lib.load().tg_gated_decode(
@@ -380,6 +438,7 @@ def gated_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         _cuda(workspace, "workspace"), workspace.numel() * workspace.element_size(),
         _stream(stream))
     check(st, "tg_gated_decode")
+    _hand_over(stream, *new)
     return out
 
 
@@ -412,24 +471,6 @@ def _ptr(t: torch.Tensor, name: str) -> int:
     if not t.is_contiguous():
         raise TokenGateError(f"{name} must be contiguous")
     return t.data_ptr()
-
-
-_CURRENT = contextlib.nullcontext()
-
-
-def _on(stream):
-    """Where a call on a given stream allocates: with that stream current, so that the
-    allocator hands out blocks whose earlier use is over when the call's kernels run. (A block
-    freed on the current stream may still be in use by kernels queued there.)"""
-    return _CURRENT if stream is None else torch.cuda.stream(stream)
-
-
-def _hand_over(stream, *tensors) -> None:
-    """Outputs that were allocated with `stream` current and go to a caller who works on the
-    current stream: their blocks are not given away while that one still uses them."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def _heads(t: torch.Tensor, T: int, H: int, dh: int, name: str, dtype) -> int:

@@ -43,7 +43,22 @@ def _tree(fmt, T):
     return make
 
 
-CASES = {"norm": _norm, "read": _read, "tree, few rows": _tree(torch.int8, 4), "tree": _tree(torch.bfloat16, 64)}
+def _gated(api):
+    g = torch.Generator().manual_seed(8)
+    rnd = lambda *s: torch.randn(*s, generator=g).cuda()
+    K, hq, hkv, dh = 400, 4, 2, 128
+    q, k, v, do = (rnd(K, h, dh).to(torch.bfloat16) for h in (hq, hkv, hkv, hq))
+    s, gain, tau, lse = rnd(K), rnd(hq).abs(), 0.8 + rnd(hq).abs(), torch.empty(hq, K).cuda()
+    cu = torch.tensor([0, 150, 400], dtype=torch.int32).cuda()
+
+    def call(**kw):
+        o = api.gated_attention(q, k, v, s, gain, tau, cu, 250, lse=lse, **kw)
+        return (o,) + api.gated_attention_bwd(q, k, v, o, do, lse, s, gain, tau, cu, 250, **kw)
+    need = api._lib.load().tg_gated_attention_bwd_workspace_size(api.TG_BF16, 2, K, 250, hq, hkv, dh)
+    return call, [q.nbytes, q.nbytes, k.nbytes, v.nbytes, s.nbytes, gain.nbytes, tau.nbytes, need]
+
+
+CASES = {"gated attention": _gated, "norm": _norm, "read": _read, "tree, few rows": _tree(torch.int8, 4), "tree": _tree(torch.bfloat16, 64)}
 
 
 @pytest.mark.parametrize("name", sorted(CASES))

@@ -53,6 +53,8 @@ def fakes(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: CALLER)
     monkeypatch.setattr(api, "_call", lambda fn, what, stream, tensors, args:
                         fn(*args, (stream or CALLER).cuda_stream))
+    monkeypatch.setattr(api, "_cuda", lambda t, name, dtype=None: t.data_ptr())
+    monkeypatch.setattr(api, "_stream", lambda stream=None: (stream or CALLER).cuda_stream)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: recorded.append((self.data_ptr(), s.cuda_stream)),
                         raising=False)
     return current, calls, recorded
@@ -80,12 +82,42 @@ def _tree():
     return (Z(2, 3, 4, 64, **BF), d, d, Z(2, 3), Z(2, 3, dtype=torch.int64), c, c, Z(2, 9), Z(2, **I32), Z(4), Z(4), 9)
 
 
+def _attn():
+    return Z(5, 4, 64), Z(5, 2, 64), Z(5, 2, 64)
+
+
+def _attn_bwd():
+    q, k, v = _attn()
+    return q, k, v, q, q, Z(4, 5), Z(5), Z(4), Z(4), Z(2, **I32), 5
+
+
+def _decode():
+    c = Z(2, 9, 2, 64, **BF)
+    return Z(2, 4, 64, **BF), c, c, Z(2, 9), Z(2, **I32), Z(4), Z(4), 9
+
+
+OLDER = {
+    "gate_score": (api.gate_score, lambda: (Z(5, 8), Z(4, 8), Z(4), Z(4), 0.0), 1),
+    "select_topk": (lambda *a, **kw: api.select_topk(*a, want_pos=True, **kw),
+                    lambda: (Z(5), Z(2, **I32), Z(1, **I32), Z(1, **I32), Z(1, **I32), 3, 5), 4),
+    "compact_rows": (lambda *a, **kw: tuple(api.compact_rows(*a, **kw)), lambda: ([Z(5, 8), Z(5, 4)], Z(3, **I32)), 2),
+    "gated_attention": (api.gated_attention, lambda: (*_attn(), Z(5), Z(4), Z(4), Z(2, **I32), 5), 1),
+    "gated_attention_bwd": (api.gated_attention_bwd, _attn_bwd, 7),
+    "gated_delta_rule": (api.gated_delta_rule, lambda: (*(Z(5, 2, 64, **BF) for _ in range(3)), Z(5, 2), Z(5, 2),
+                                                        Z(2, **I32), 5), 2),
+    "qkv_rope": (api.qkv_rope, lambda: (Z(5, 8, **BF), Z(64, 8, **BF), 2, 1, Z(5, **I32)), 3),
+    "compact_qkv_rope": (api.compact_qkv_rope, lambda: (Z(9, 8, **BF), Z(5, **I32), Z(64, 8, **BF), 2, 1, Z(5, **I32)), 4),
+    "gated_decode": (api.gated_decode, _decode, 2),
+}
 CASES = {   # (call, its inputs, allocations)
     "qk_norm_rope": (api.qk_norm_rope, _norm, 2),
     "qk_norm_rope_bwd": (api.qk_norm_rope_bwd, _norm_bwd, 5),
     "quant_cache_read": (api.quant_cache_read, _read, 3),
     "tree_attention": (api.tree_attention, _tree, 2),
 }
+
+
+CASES.update(OLDER)
 
 
 @pytest.mark.parametrize("name", sorted(CASES))
