@@ -389,7 +389,9 @@ tg_status tg_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, in
  *           there; another array, which must not overlap cache_len, writes from any row
  *           (a sequence taken back to an earlier length)
  * A sequence whose rows do not fit its capacity, or whose offsets are out of order, is
- * left unchanged, its cache_len too, and TG_ERR_DEVICE_CHECK recorded.
+ * left unchanged, its cache_len too, and TG_ERR_DEVICE_CHECK recorded. Where offsets out of
+ * order let several sequences claim the same rows, one of them at most is written, and
+ * every sequence is either written whole or left unchanged.
  */
 tg_status tg_quant_cache_append(const void* k_new, const void* v_new, const float* s_new,
                                 int64_t n_src, const int32_t* src_idx, int64_t n_new,
@@ -404,7 +406,8 @@ tg_status tg_quant_cache_append(const void* k_new, const void* v_new, const floa
  * rows [cu_rows[b], cu_rows[b+1]) of k, v [n_rows, n_hkv, head_dim] (TG_BF16 or TG_F32:
  * code * scale in f32, rounded once) and s [n_rows] f32. start NULL: from row 0. Rows
  * of the outputs behind cu_rows[batch] are left as they were. A sequence that asks for
- * rows behind its cache_len (or cap) is skipped and TG_ERR_DEVICE_CHECK recorded.
+ * rows behind its cache_len (or cap), or whose offsets are out of order, is skipped and
+ * TG_ERR_DEVICE_CHECK recorded; every sequence is either given back whole or skipped.
  */
 tg_status tg_quant_cache_read(const void* k_cache, const void* v_cache, const float* k_scale,
                               const float* v_scale, const float* s_cache,

@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kLenThreads = 32;
 constexpr int kMaxBlocks = 148 * 8;
 constexpr float kMinScale = 0x1p-60f;
 constexpr int kMaxBatch = 65535;
@@ -68,6 +69,27 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int64_t r,
   return lo < batch ? lo : -1;
 }
 
+// Whether the search above gives sequence b for all of its rows c0 .. c1 - 1 (one or more). Where the
+// offsets ascend it does. Where they do not, two sequences may claim the same rows; the
+// search still gives a row to one sequence at most, and since every level's choice grows
+// with r, rows between two that go to b go to b too: it is enough to look at the ends.
+// Not inlined, so that the row loops keep the registers for their loads (4 x 10721 int8 rows
+// read to bf16: 40.0 us, inlined 41.0).
+__device__ __noinline__ bool owns(const int32_t* cu, int batch, int b, int64_t c0, int64_t c1, int lane) {
+  int lo = 0, n = batch + 1;
+  if (static_cast<int64_t>(cu[0]) > c0) return false;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int64_t c = cu[lo + min(lane * step, n - 1)];
+    const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, c <= c0));
+    if (last != 31 - __clz(__ballot_sync(0xFFFFFFFFu, c < c1))) return false;
+    const int at = min(last * step, n - 1);
+    n = min(step, n - at);
+    lo += at;
+  }
+  return lo == b;
+}
+
 // The offsets of up to kSmemBatch sequences and the rows they start at are read once a
 // block: every row then finds its sequence without a load from global memory.
 constexpr int kSmemBatch = 1024;
@@ -76,15 +98,19 @@ struct SeqSmem {
 };
 struct SeqTable {
   const int32_t *cu, *start;   // start: null for 0
+  bool ascends;                // the offsets are known to ascend
 };
 __device__ __forceinline__ SeqTable seq_table(const QuantArgs& A, SeqSmem& S) {
-  if (A.batch > kSmemBatch) return SeqTable{A.cu, A.start};
+  if (A.batch > kSmemBatch) return SeqTable{A.cu, A.start, false};
+  bool ok = true;
   for (int b = threadIdx.x; b <= A.batch; b += kThreads) {
-    S.cu[b] = A.cu[b];
+    const int32_t c = A.cu[b], before = A.cu[b > 0 ? b - 1 : 0];
     if (b < A.batch) S.start[b] = A.start ? A.start[b] : 0;
+    S.cu[b] = c;
+    ok = ok && before <= c;
   }
-  __syncthreads();
-  return SeqTable{S.cu, S.start};
+  ok = __syncthreads_and(ok);
+  return SeqTable{S.cu, S.start, ok};
 }
 
 // A sequence's rows as the call describes them, and whether they fit.
@@ -158,11 +184,12 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
   const SeqTable Q = seq_table(A, S);
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  // lengths, and the record of sequences that do not fit
+  // the record of sequences that do not fit (offsets that do not ascend have one whose end is
+  // before its start), and lengths of those without rows
   for (int64_t b = gw * 32 + lane; b < A.batch; b += n_warps * 32) {
     const SeqRows s = seq_rows(A, Q, static_cast<int>(b), false);
     if (!s.ok) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
-    else if (A.new_len) A.new_len[b] = static_cast<int32_t>(s.start + s.n);
+    else if (A.new_len && s.n == 0) A.new_len[b] = static_cast<int32_t>(s.start);
   }
   const int heads = 2 * A.n_hkv;        // of K, then of V
   const int64_t n_work = A.n_rows * A.parts;
@@ -176,10 +203,12 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
     if (b < 0) continue;
     const SeqRows s = seq_rows(A, Q, b, false);
     if (!s.ok || r - s.first >= s.n) continue;
+    if (!Q.ascends && s.n > 1 && !owns(Q.cu, A.batch, b, s.first, s.first + s.n, lane)) continue;
     const int64_t row = static_cast<int64_t>(b) * A.cap + s.start + (r - s.first);
     if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
     if (part == 0 && lane == 0) {
       if (!have) tg::set_status(A.status, TG_ERR_DEVICE_CHECK);
+      if (A.new_len && r == s.first) A.new_len[b] = static_cast<int32_t>(s.start + s.n);
       A.s_cache[row] = have ? A.s_new[src] : 0.f;
     }
     // heads part*kHpw + sub, then every parts*kHpw-th
@@ -237,13 +266,20 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
 }
 
 // The lengths of an append in place: cache_len is also where the rows start, so it
-// moves only once the copy kernel has read it.
-__global__ void __launch_bounds__(kThreads) quant_len_kernel(const QuantArgs A, int32_t* len) {
+// moves only once the copy kernel has read it. A warp takes 32 sequences, each lane its own but
+// for the search.
+__global__ void __launch_bounds__(kLenThreads) quant_len_kernel(const QuantArgs A, int32_t* len) {
   tg::pdl_launch_dependents();
   tg::pdl_wait();
-  const int b = blockIdx.x * kThreads + threadIdx.x;
-  if (b >= A.batch) return;
-  const SeqRows s = seq_rows(A, SeqTable{A.cu, A.start}, b, false);
+  const int b = blockIdx.x * kLenThreads + threadIdx.x, lane = threadIdx.x & 31;
+  SeqRows s = {};
+  if (b < A.batch) s = seq_rows(A, SeqTable{A.cu, A.start, false}, b, false);
+  for (unsigned left = __ballot_sync(0xFFFFFFFFu, s.ok && s.n > 0); left; left &= left - 1) {
+    const int l = __ffs(left) - 1;
+    const int64_t c0 = __shfl_sync(0xFFFFFFFFu, s.first, l), n = __shfl_sync(0xFFFFFFFFu, s.n, l);
+    const bool all = owns(A.cu, A.batch, b - lane + l, c0, c0 + n, lane);
+    if (lane == l) s.ok = all;
+  }
   if (s.ok) len[b] = static_cast<int32_t>(s.start + s.n);
 }
 
@@ -286,6 +322,7 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const QuantArgs A)
     if (b < 0) continue;
     const SeqRows s = seq_rows(A, Q, b, true);
     if (!s.ok || r - s.first >= s.n) continue;
+    if (!Q.ascends && s.n > 1 && !owns(Q.cu, A.batch, b, s.first, s.first + s.n, lane)) continue;
     const int64_t row = static_cast<int64_t>(b) * A.cap + s.start + (r - s.first);
     if (!tg::in_bounds(row, static_cast<int64_t>(A.batch) * A.cap, A.status)) continue;
     if (part == 0 && lane == 0) A.so[r] = A.s_cache[row];
@@ -394,8 +431,8 @@ extern "C" tg_status tg_quant_cache_append(
     r = cache_dtype == TG_E4M3 ? tg::launch(quant_append_kernel<64, true>, grid, block, 0, stream, 0, a)
                                : tg::launch(quant_append_kernel<64, false>, grid, block, 0, stream, 0, a);
   if (r != TG_OK || !in_place) return r;
-  return tg::launch(quant_len_kernel, dim3((batch + kThreads - 1) / kThreads), block, 0, stream, 0, a,
-                    cache_len);
+  return tg::launch(quant_len_kernel, dim3((batch + kLenThreads - 1) / kLenThreads), dim3(kLenThreads), 0, stream,
+                    0, a, cache_len);
 }
 
 extern "C" tg_status tg_quant_cache_read(const void* k_cache, const void* v_cache,
