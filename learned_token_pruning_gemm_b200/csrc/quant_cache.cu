@@ -33,7 +33,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLenThreads = 32;
 constexpr int kMaxBlocks = 148 * 8;
 constexpr float kMinScale = 0x1p-60f;
 constexpr int kMaxBatch = 65535;
@@ -266,15 +265,19 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
 }
 
 // The lengths of an append in place: cache_len is also where the rows start, so it
-// moves only once the copy kernel has read it. A warp takes 32 sequences, each lane its own but
-// for the search.
-__global__ void __launch_bounds__(kLenThreads) quant_len_kernel(const QuantArgs A, int32_t* len) {
+// moves only once the copy kernel has read it. Every block looks at all offsets; the
+// sequences' rows are searched for only where those do not ascend.
+__global__ void __launch_bounds__(kThreads) quant_len_kernel(const QuantArgs A, int32_t* len) {
   tg::pdl_launch_dependents();
   tg::pdl_wait();
-  const int b = blockIdx.x * kLenThreads + threadIdx.x, lane = threadIdx.x & 31;
+  const int b = blockIdx.x * kThreads + threadIdx.x, lane = threadIdx.x & 31;
   SeqRows s = {};
   if (b < A.batch) s = seq_rows(A, SeqTable{A.cu, A.start, false}, b, false);
-  for (unsigned left = __ballot_sync(0xFFFFFFFFu, s.ok && s.n > 0); left; left &= left - 1) {
+  bool down = false;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < A.batch; i += kThreads) down |= A.cu[i] > A.cu[i + 1];
+  down = __syncthreads_or(down);
+  for (unsigned left = __ballot_sync(0xFFFFFFFFu, down && s.ok && s.n > 0); left; left &= left - 1) {
     const int l = __ffs(left) - 1;
     const int64_t c0 = __shfl_sync(0xFFFFFFFFu, s.first, l), n = __shfl_sync(0xFFFFFFFFu, s.n, l);
     const bool all = owns(A.cu, A.batch, b - lane + l, c0, c0 + n, lane);
@@ -431,8 +434,8 @@ extern "C" tg_status tg_quant_cache_append(
     r = cache_dtype == TG_E4M3 ? tg::launch(quant_append_kernel<64, true>, grid, block, 0, stream, 0, a)
                                : tg::launch(quant_append_kernel<64, false>, grid, block, 0, stream, 0, a);
   if (r != TG_OK || !in_place) return r;
-  return tg::launch(quant_len_kernel, dim3((batch + kLenThreads - 1) / kLenThreads), dim3(kLenThreads), 0, stream,
-                    0, a, cache_len);
+  return tg::launch(quant_len_kernel, dim3((batch + kThreads - 1) / kThreads), block, 0, stream, 0, a,
+                    cache_len);
 }
 
 extern "C" tg_status tg_quant_cache_read(const void* k_cache, const void* v_cache,
