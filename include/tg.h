@@ -434,8 +434,11 @@ tg_status tg_quant_cache_read(const void* k_cache, const void* v_cache, const fl
  *           TG_I8, TG_E4M3: the quantised cache, with its scales (0 or >= 2^-60)
  *   max_len (host) bounds every cache_len[b]; max_len <= cap
  *   out [batch, n_draft, n_hq, head_dim] bf16
- * A token that sees nothing (mask 0 over an empty cache, or every logit -inf) gets
- * zeros. Infinities and NaN in drafted tokens that a token does not see, and in cache
+ * Logits are fp32, in units of log2: next to a score of size S what is below S * 2^-23 is
+ * lost, over codes the value scales' part of the weights with it. Finite scores beyond
+ * +-2^120 count as +-2^120, so a token that sees nothing but scores of the type's lowest
+ * value gets a mean of their values. A token that sees nothing (mask 0 over an empty cache,
+ * or every logit -inf) gets zeros. Infinities and NaN in drafted tokens that a token does not see, and in cache
  * rows behind cache_len, do not reach it. A sequence with cache_len outside
  * [0, min(cap, max_len)] or draft_len outside [0, n_draft] is skipped (its out rows are
  * left as they were) and TG_ERR_DEVICE_CHECK recorded.

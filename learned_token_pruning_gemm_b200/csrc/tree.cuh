@@ -13,6 +13,7 @@ namespace tg {
 
 constexpr int kTreeMaxBatch = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMostScore = 0x1p120f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units a logit may exceed the reference by
 
 struct TreeArgs {
@@ -139,6 +140,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status
 
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// A score as logits take it: gain * score * log2(e) of a finite score is finite too (up to gains of
+// 88), so that rows which see nothing but scores of the type's lowest value still have a
+// largest one. Infinities and NaN stay what they are.
+__device__ __forceinline__ float held(float s) {
+  return fabsf(s) > kMostScore && fabsf(s) < INFINITY ? copysignf(kMostScore, s) : s;
+}
 
 // Four codes (bytes of w; int8 ones with the sign bit flipped) to four fp16 values, exactly.
 template <bool kE4m3>

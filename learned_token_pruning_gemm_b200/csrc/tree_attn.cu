@@ -419,6 +419,8 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
       }
       cp_wait_group<kLag>();
       const int s = (g - kLag) % kKeyStages;
+      auto score = [&](int i) -> float& { return S.key[s][0][kQ ? 4 * ((lane + 32 * i) >> 1) + (lane & 1) : lane + 32 * i]; };
+      const float big = fmaxf(fmaxf(fabsf(score(0)), fabsf(score(1))), fmaxf(fabsf(score(2)), fabsf(score(3))));
       if constexpr (kQ) {
         // The value scale v joins the logit as log2 v (see the softmax); where it is 0 all codes
         // are, and any v small enough not to lead will do.
@@ -430,6 +432,8 @@ __global__ void __launch_bounds__(Cfg<DH, kType != TG_BF16>::kThreads, 1)
           S.key[s][3][j] = __frcp_rn(vs);
         }
       }
+      if (big > tg::kMostScore)
+        for (int i = 0; i < 4; ++i) score(i) = tg::held(score(i));
       tg::mbar_arrive(&S.b_full[s]);
       c.advance(A, Q);
     }
@@ -868,7 +872,7 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
         kh[d][p] = *reinterpret_cast<const uint4*>(A.kd + (at * A.n_hkv + kvh) * DH + 64 * p + 8 * i8);
         vh[d][p] = *reinterpret_cast<const uint4*>(A.vd + (at * A.n_hkv + kvh) * DH + 64 * p + 8 * i8);
       }
-      sd[d] = A.sd[at];
+      sd[d] = tg::held(A.sd[at]);
 #pragma unroll
       for (int i = 0; i < kNs; ++i) see &= see - 1;
     }

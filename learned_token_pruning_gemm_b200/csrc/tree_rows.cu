@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT>::kThreads, Cfg<DH, NT>::kCtas)
       // the row sum takes them in fp32, divided by v. Where v is 0 all codes are, and any v
       // small enough not to lead will do.
       float lv[2], iv[2];
+      if (fmaxf(fabsf(sk[0]), fabsf(sk[1])) > tg::kMostScore) sk[0] = tg::held(sk[0]), sk[1] = tg::held(sk[1]);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (vs[x] == 0.f) vs[x] = 0x1p-40f;

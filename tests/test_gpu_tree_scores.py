@@ -1,9 +1,10 @@
 """GPU tests of tg_tree_attention where scores are large: a common offset that takes the
-logits to where fp32 has steps of 4 to 16 (the weights' range must hold there)."""
+logits to where fp32 has steps of 4 to 16 (the weights' range must hold there), and
+scores of the type's lowest value (finite: a row of them is a mean, not a row of nothing)."""
 import pytest
 import torch
 
-from test_gpu_tree_attn import BF, E4, I8, api, make, run, _status  # noqa: F401 (fixtures)
+from test_gpu_tree_attn import BF, E4, I8, api, check, make, reference, run, values, _status  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,52 @@ def test_keys_one_step_ahead_on_a_large_offset(api, fmt, T, hq, hkv, dh, base, a
         # the output's rounding, the weight's, and A's part
         tol = abs(b) * (2.0 ** -8 + 2.0 ** -11) + (a - b) * 2.0 ** -(ahead // 2)
         assert ((got - b).abs() <= tol).all(), (off, float((got - b).abs().max()), tol)
+
+
+LOWEST, HIGHEST = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+SHAPES = [(1, 4, 2, 128), (3, 8, 4, 64), (20, 8, 2, 128), (64, 8, 2, 64)]   # T, hq, hkv, dh
+
+
+@pytest.mark.parametrize("score", [LOWEST, HIGHEST, -3e38, 2.0 ** 121])
+@pytest.mark.parametrize("gain", [0.25, 1.0, 7.0, 80.0])
+@pytest.mark.parametrize("fmt", [BF, I8])
+def test_a_token_alone_is_its_value_whatever_its_score(api, fmt, gain, score):
+    # over an empty cache, and over one whose rows weigh nothing: the weight is 1 exactly
+    for n in (0, 300):
+        st = make(12, 2, 3, 300, [n, n], 4, 2, 128, fmt, garbage=False)
+        st["gain"].fill_(gain)
+        st["sd"].fill_(score)
+        st["sc"].fill_(float("-inf"))
+        st["mask"].copy_(torch.tensor([1, 2, 4]).cuda())
+        assert torch.equal(run(api, st, max_len=300), st["vd"].repeat_interleave(2, 2))
+
+
+@pytest.mark.parametrize("score", [LOWEST, HIGHEST])
+@pytest.mark.parametrize("T,hq,hkv,dh", SHAPES)
+@pytest.mark.parametrize("fmt", [BF, I8, E4])
+def test_rows_of_nothing_but_lowest_scores(api, fmt, T, hq, hkv, dh, score):
+    # All logits are equal (in 64 bits too: what q and k add is below their last place). Over codes the value
+    # scales' part of the weights is below it as well, so there the output is only known
+    # to lie within the values.
+    st = make(13, 2, T, 400, [400, 77], hq, hkv, dh, fmt, garbage=False)
+    st["gain"].add_(0.3)
+    st["sc"].fill_(score)
+    st["sd"].fill_(score)
+    got = run(api, st)
+    if fmt == BF:
+        check(got, reference(st))
+    v = torch.cat([values(st)[1], st["vd"].double()], 1)
+    for b, n in enumerate((400, 77)):
+        rows = torch.cat([v[b, :n], v[b, 400:]])
+        lo, hi = (f(rows, 0).repeat_interleave(hq // hkv, 0) for f in (torch.amin, torch.amax))
+        assert (got[b] >= lo - 2.0 ** -8 * lo.abs()).all() and (got[b] <= hi + 2.0 ** -8 * hi.abs()).all()
+    # next to others they weigh nothing, or everything
+    st["sc"][:, 5:30] = 0.5
+    st["sd"].fill_(-0.5)
+    if fmt == BF or score == LOWEST:
+        check(run(api, st), reference(st))
+    # and minus infinity weighs nothing next to them
+    st["sc"].fill_(float("-inf"))
+    st["sc"][:, 11] = score
+    st["sd"].fill_(float("-inf"))
+    check(run(api, st), reference(st))
