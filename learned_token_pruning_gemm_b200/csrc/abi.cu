@@ -74,11 +74,14 @@ bool ensure_smem(const void* fn, int bytes) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   std::lock_guard<std::mutex> lk(g_mu);
-  for (int i = 0; i < n; ++i)
-    if (cache[i].dev == dev && cache[i].fn == fn && cache[i].bytes >= bytes) return true;
+  Entry* e = nullptr;   // one for each function and device: its limit so far
+  for (int i = 0; i < n && !e; ++i)
+    if (cache[i].dev == dev && cache[i].fn == fn) e = &cache[i];
+  if (e && e->bytes >= bytes) return true;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return false;
-  if (n < 256) cache[n++] = Entry{dev, fn, bytes};
+  if (e) e->bytes = bytes;
+  else if (n < 256) cache[n++] = Entry{dev, fn, bytes};
   return true;
 }
 

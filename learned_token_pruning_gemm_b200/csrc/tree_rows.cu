@@ -428,8 +428,11 @@ tg_status launch(const TreeArgs& a, cudaStream_t st) {
     return TG_ERR_CUDA;
   constexpr int fixed = sizeof(RowSmem<DH, NT>) + 1024;
   static_assert((fixed + 1024 + 512) * C::kCtas <= 233472, "an SM's shared memory");
-  const int smem = fixed + 9 * a.batch + 8;
-  if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_rows_kernel<kType, DH, NT>), smem)) return TG_ERR_CUDA;
+  auto with_seqs = [](int batch) { return fixed + 9 * batch + 8; };
+  const int smem = with_seqs(a.batch);
+  // the limit that the largest batch needs, so that batches that grow do not raise it step by step
+  if (!tg::ensure_smem(reinterpret_cast<const void*>(tree_rows_kernel<kType, DH, NT>), with_seqs(tg::kTreeMaxBatch)))
+    return TG_ERR_CUDA;
   return tg::launch(tree_rows_kernel<kType, DH, NT>, dim3(a.n_cta), dim3(C::kThreads), smem, st, 0, tk, tv, a);
 }
 
