@@ -624,7 +624,8 @@ def quant_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torc
                      dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
     """Rows of a quantised cache as packed (k [total,Hkv,dh], v, s [total] f32), k and v in
     `dtype` (bf16 or f32): sequence b's cache rows from start[b] (None: 0) on fill rows
-    [cu_rows[b], cu_rows[b+1])."""
+    [cu_rows[b], cu_rows[b+1]). Rows that no sequence fills are not written: without `out`
+    they hold anything."""
     B, cap, hkv, dh = _quant_cache("quant_cache_read", k_cache, v_cache, k_scale, v_scale, s_cache,
                                    cache_len)
     total = int(total)
@@ -691,7 +692,8 @@ def tree_attention(q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor
     drafted tokens in their tree_mask ([B,T] int64, bit i: token i). The cache is bf16
     (cache_append's) or, with k_scale and v_scale, quantised (quant_cache_append's).
     draft_len [B] int32: drafted tokens of each sequence (None: T); rows of out behind
-    them are left as they were. Returns out [B,T,Hq,dh] bf16."""
+    them are left as they were (zeros where out is allocated here). Returns out
+    [B,T,Hq,dh] bf16."""
     if q.dim() != 4 or k_cache.dim() != 4:
         raise TokenGateError("tree_attention: q [B,T,Hq,dh], caches [B,cap,Hkv,dh]")
     B, T, hq, dh = q.shape
@@ -726,7 +728,8 @@ def tree_attention(q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor
     new = ()
     if out is None:
         with _on(stream):
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            make = torch.empty_like if draft_len is None else torch.zeros_like
+            out = make(q, memory_format=torch.contiguous_format)
         new = (out,)
     else:
         _shape(out, q.shape, "out", torch.bfloat16)
