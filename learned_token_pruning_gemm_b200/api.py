@@ -55,7 +55,11 @@ def _on(stream):
     """Where a call on a given stream allocates: with that stream current, so that the
     allocator hands out blocks whose earlier use is over when the call's kernels run. (A block
     freed on the current stream may still be in use by kernels queued there.)"""
-    return _CURRENT if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return _CURRENT
+    if not isinstance(stream, torch.cuda.Stream):   # anything with a cuda_stream is a stream here
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
 
 
 def _hand_over(stream, *tensors) -> None:

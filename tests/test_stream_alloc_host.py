@@ -50,6 +50,7 @@ def fakes(monkeypatch):
             return entry
     monkeypatch.setattr(api._lib, "load", lambda *a: Lib())
     monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: {5: STREAM}[handle])
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: CALLER)
     monkeypatch.setattr(api, "_call", lambda fn, what, stream, tensors, args:
                         fn(*args, (stream or CALLER).cuda_stream))
