@@ -11,9 +11,14 @@
 // so the angles are formed once per token, a part by each of the heads that are side by side,
 // and serve every head: lane c of a head holds E pairs from E c on (elements E c .. and
 // rot/2 + E c ..; E = 8 or 4), so a rotation needs no exchange between lanes, and the mean
-// is a few shuffles. 16384 tokens of 24 bf16 heads of 128 take 40.0 us (5.0 TB/s, 77% of a
+// is a few shuffles. 16384 tokens of 24 bf16 heads of 128 take 39.7 us (5.1 TB/s, 77% of a
 // plain copy's rate), backward over 10721 tokens 46.8 us (4.2 TB/s): what is left is
-// issue slots (58% busy) and latency at 20 and 12 warps an SM, not DRAM.
+// latency at 20 and 12 warps an SM (issue slots 47% and 39% busy, DRAM 48% and 44%). fp32:
+// 8192 tokens 36.2 us (5.6 TB/s), backward over 5000 tokens 40.0 us (4.6 TB/s).
+//
+// The weight gradients are summed in fp32: a lane's chain is its warp's tokens times the
+// heads that its lane group takes (10721 tokens of 16 heads of 128: 24 to 28 terms), then come
+// lane groups, warps and blocks, so the error grows with tokens x heads / 1776 warps.
 //
 // The angle of position p and frequency i is taken in turns, p * F_i mod 1 with F_i =
 // theta_i / (2 pi) as a 64-bit fixed-point fraction (an integer product, exact modulo
@@ -115,7 +120,8 @@ __device__ __forceinline__ void turns_from(double ratio, int i0, uint64_t* f) {
 }
 
 // Sine and cosine of position pos times a turn fraction. kFull: to fp32; otherwise by MUFU,
-// off by about 2^-21, far below half a bf16 step of the result.
+// off by about 2^-21, which moves a rotated element by 2^-20 of its pair's size at most: far
+// below half a bf16 step of the larger one, more than that of one that nearly cancels.
 template <bool kFull>
 __device__ __forceinline__ void angle(int64_t pos, uint64_t turn, float* sn, float* cs) {
   const uint64_t fx = static_cast<uint64_t>(pos) * turn;

@@ -21,9 +21,10 @@
 // tg_quant_cache_read gives rows back: code * scale in fp32, rounded once.
 //
 // Both are bound by memory (append: 2 bytes in and 1 out per value; read: 1 in and 2
-// or 4 out): 14944 rows of eight e4m3 heads of 128 are appended in 32.4 us (65% of issue slots
-// busy), 4 x 10721 int8 rows read back as bf16 in 38.8 us (5.5 TB/s, 84% of a plain copy's
-// rate). A warp takes one row (for few rows: part of its heads); a head's lanes hold 16
+// or 4 out): 12220 rows of eight heads of 128 in eight sequences are appended in 17.9 us (e4m3,
+// 4.2 TB/s, 65% of issue slots busy) and 18.6 us (int8), 34446 int8 rows in four sequences read
+// back as bf16 in 39.1 us (5.5 TB/s, 84% of a plain copy's rate) and as f32 in 76.5 us (4.6 TB/s).
+// A warp takes one row (for few rows: part of its heads); a head's lanes hold 16
 // values each to write (so that the scale is formed by few) and 8 to read.
 #include <cuda_fp16.h>
 
@@ -72,8 +73,8 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int64_t r,
 // offsets ascend it does. Where they do not, two sequences may claim the same rows; the
 // search still gives a row to one sequence at most, and since every level's choice grows
 // with r, rows between two that go to b go to b too: it is enough to look at the ends.
-// Not inlined, so that the row loops keep the registers for their loads (4 x 10721 int8 rows
-// read to bf16: 40.0 us, inlined 41.0).
+// Not inlined, so that the row loops keep the registers for their loads (34446 int8 rows
+// read to bf16 through the binding: 40.0 us, inlined 41.0).
 __device__ __noinline__ bool owns(const int32_t* cu, int batch, int b, int64_t c0, int64_t c1, int lane) {
   int lo = 0, n = batch + 1;
   if (static_cast<int64_t>(cu[0]) > c0) return false;
@@ -369,8 +370,8 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const QuantArgs A)
 }
 
 // Warps per row: one, unless there are too few rows to give every warp of the machine one.
-// Appending 8 x 1868 rows of eight heads of 128: 43 us with one, 46 us with two; 16 x 5 rows:
-// 10.3 us with one, 7.2 us with the four (of four heads each) that this gives.
+// Appending 12220 rows of eight e4m3 heads of 128: 17.9 us with one, 20.3 us with two; 51 rows:
+// 4.3 us with one, 3.3 us with two, 3.1 us with the four (of four heads each) that this gives.
 int warps_per_row(int64_t n_rows, int n_hkv, int dh, int per_lane) {
   const int hpw = 32 / (dh / per_lane);
   const int most = (2 * n_hkv + hpw - 1) / hpw;

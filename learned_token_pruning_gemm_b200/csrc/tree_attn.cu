@@ -6,18 +6,21 @@
 // is set in tree_mask[b][t]:
 //     z_j = q . k_j / (sqrt(dh) tau_h) + g_h s_j,   O = sum_j softmax_j(z) v_j.
 //
-// The cache is read once per KV head and 256 rows and serves all drafted tokens and query heads
-// of the group: with R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product and back.
-// Here the rows are packed into M = 128 tiles (row r is token r / G, head r % G) and both
-// products run on the tensor cores with accumulators in TMEM; up to 16 rows over codes take the
-// kernel of tree_rows.cu instead. Work is split as tree.cuh says, in units of 128 cache rows; what a CTA has of an item it leaves as partials (max, sum, O), and the
-// kernel at the end adds the partials up in CTA order, so results do not depend on timing,
-// and brings in the drafted rows that each token sees.
+// The cache is read once per KV head and pair of row tiles (up to 256 rows; whole tokens, so
+// 192 for 64 tokens of three heads) and serves the drafted tokens and query heads in it: with
+// R = (tokens) x (group) rows this is a [R x dh] x [dh x len] product and back. Here the rows
+// are packed into M = 128 tiles (row r is token r / G, head r % G) and both products run on the
+// tensor cores with accumulators in TMEM; up to 16 rows over codes take the kernel of
+// tree_rows.cu instead. Work is split as tree.cuh says, in units of 128 cache rows; what a CTA
+// has of an item it leaves as partials (max, sum, O), and the kernel at the end adds the
+// partials up in CTA order, so results do not depend on timing, and brings in the drafted rows
+// that each token sees.
 //
-// A CTA has two sides, each with its own softmax warps, S buffers and O in TMEM. The sides take the two row tiles of an item, which then share every K and V tile
-// and its widening; of an item of one row tile they take half of every unit's keys each,
-// and each leaves a partial. A job is 64 keys of a side; it has two S buffers, so that its
-// products run while the softmax is at the job before.
+// A CTA has two sides, each with its own softmax warps, S buffers and O in TMEM. The sides take
+// the two row tiles of an item, which then share every K and V tile and its widening; of an item
+// of one row tile they take half of every unit's keys each, and each leaves a partial. A job is
+// 64 keys of a side; it has two S buffers, so that its products run while the softmax is at the
+// job before.
 //
 // Per CTA, pipelines run over the units:
 //   warp 0       K tiles by TMA (bf16: into the operand ring; codes: K and V codes into a
@@ -32,15 +35,31 @@
 //   warps 4-19   softmax, 16 rows a warp, those with rows only: logits in the log2 domain
 //                less the row's running reference, which moves only when one exceeds it by more
 //                than it may (O is then rescaled in TMEM).
+//
 // What bounds it: the softmax's instructions (57% of the issue slots are busy, at 24 warps an SM;
-// the tensor pipe 30% of the time) and, with few rows, the way of a unit through the roles. 2 x 64 tokens of 32 heads over 65500 int8 rows of four heads: 226 us (0.61 PFLOP/s, 84.5
-// us at a plain GEMM's rate; 200 us without the combining kernel); 8 x 13 tokens of 16 heads
-// over 50 thousand bf16 rows of eight: 57 us (31.3 us at a plain copy's rate). Steps that
-// made it so, on the long case: one row tile a CTA 379 us; two tiles that share K, V and
-// their widening 318; queries, keys and values waiting less for one another 246; one thread
-// chosen by elect.sync for the products (a lane picked by its number costs 80 to 110 cycles an
-// MMA, an elected one 25 to 45) and jobs of 64 keys 253; 16 rows a warp 229; streams of eight
-// lanes in the combining kernel 224.
+// the tensor pipe 30% of the time) and, with few rows, the way of a unit through the roles. 2 x 64
+// tokens of 32 heads over 65500 int8 rows of four heads: 227 us (0.61 PFLOP/s, 84.5 us at a plain
+// GEMM's rate; 200 us without the combining kernel); 8 x 13 tokens of 16 heads over 50 thousand
+// bf16 rows of eight: 57 us (31.3 us at a plain copy's rate). Steps that made it so, on the long
+// case: one row tile a CTA 379 us; two tiles that share K, V and their widening 318; queries, keys
+// and values waiting less for one another 246; one thread chosen by elect.sync for the products (a
+// lane picked by its number costs 80 to 110 cycles an MMA, an elected one 25 to 45) and jobs of 64
+// keys 253; 16 rows a warp 229; streams of eight lanes in the combining kernel 224; the reference
+// taken off rounded logits, and scores held to a finite product, 227.
+//
+// The codes variants hold 80 registers at 768 threads and spill 100 to 124 bytes (stores; loads 172
+// to 188), most likely around the 32 logits of a job; the bf16 ones (96 registers) 4 to 12.
+// Other shapes, floors at a plain copy's and GEMM's rate in brackets: 13 tokens of 16 heads over
+// 8 x 10721 rows of eight: bf16 71 us (54), int8 102 us (28), int8 of head dim 64 92 us (14): one
+// row tile of 26 rows, whose softmax warps share one scheduler, and for codes one V tile, so
+// that the next V is not widened before the last product with this one; 64 tokens of 16 heads of 64
+// over 4 x 10000 int8 rows 61 us (7), 32 tokens over 8 x 1000 bf16 rows 28 us (5.5): about half in the
+// combining kernel, which takes every drafted row again for every token and head.
+//
+// Weights are rounded for the second product, to bf16 beside bf16 values (a product's operands
+// have one type, and fp16 lacks the values' range) and to fp16 beside codes. Of the output, in
+// the 2-norm: 0.0021 and 0.0016 from the 64-bit form, where storing it in bf16 alone is 0.0016.
+//
 // A side's S_k is issued after its PV_{k - 2}, and products end in the order they are issued:
 // when S_k is there, all but PV_{k - 1} are done, so no parity wait is passed by.
 #include "tree.cuh"
@@ -1053,8 +1072,9 @@ Plan plan(int batch, int n_draft, int max_len, int n_hq, int n_hkv, int head_dim
   const int rows = group * p.tm;
   // Which kernel (this one and tree_rows.cu): codes, 8 x 10721 rows of eight heads: 2 rows a KV
   // head (32 x 1868) 79 and 38 us, 16 rows 104 and 72 us, 26 rows 105 and 113 us (head dim 64: 62
-  // and 33 us, 77 and 62 us); a bf16 cache:
-  // 2 rows 52.6 and 52.8 us, 16 rows (one of 1868) 12.9 and 14.4 us, 26 rows 61 and 67 us.
+  // and 33 us, 77 and 62 us, 26 rows not measured); a bf16 cache: 2 rows 52.6 and 52.8 us, 16 rows
+  // (one of 1868) 12.9 and 14.4 us, 26 rows 61 and 67 us. The figures of tree_rows.cu beyond 16
+  // rows and over bf16 are those of forms that it no longer has.
   p.few = codes && rows <= tg::kTreeRowsMax;
   const int warps = tg::tree_rows_warps(rows);
   p.hw = p.few ? (n_hkv < warps ? n_hkv : warps) : 1;
