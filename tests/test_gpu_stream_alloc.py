@@ -98,3 +98,31 @@ def test_busy_current_stream(api, name):
     for got in more:
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert api.device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_captured_on_a_forked_stream(api, name):
+    # inside a capture, on a second stream that joins it: what the call allocates is the graph's, its
+    # outputs are used on the first stream and freed, and the call comes again
+    call, _ = CASES[name](api)
+    want = [t.clone() for t in call()]
+    first, second = torch.cuda.Stream(), torch.cuda.Stream()
+    call(stream=second)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=first):
+        kept = []
+        for _ in range(3):
+            second.wait_stream(first)
+            got = call(stream=second)
+            first.wait_stream(second)
+            kept.append([t.clone() for t in got])
+            del got
+    for _ in range(3):
+        for ts in kept:
+            for t in ts:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for ts in kept for a, b in zip(ts, want))
+    assert api.device_status(reset=True) == 0
